@@ -464,6 +464,44 @@ int muon_clip(const muon_clip_plan_t* plan, void* params, int32_t mode, float ta
               const float* max_logits, void* workspace, size_t workspace_bytes,
               float* norms_out, float* scales_out, hipStream_t stream);
 
+/* ---- embedding: lookup with scaling, gradient by sorted tokens -------- */
+
+/* The embedding beside the AdamW step of its table: the gradient below is
+ * the dense [vocab, dim] gradient that adamw_step and grad_norm_clip read.
+ *
+ * Conventions of the calls from here on, besides those above:
+ *   - Types are MUON_DTYPE_FP32 or MUON_DTYPE_BF16; sums run in fp32 and each
+ *     result is rounded once (nearest even).
+ *   - Token ids and targets are int32 (ids_64 == 0) or int64 (ids_64 != 0).
+ *   - Two-dimensional activations are row-major with a row stride ld >= the
+ *     row length, in elements; tables, weights and their gradients are
+ *     contiguous.  No alignment is required beyond the element size;
+ *     workspaces are 256-byte aligned, scratch only (contents on entry are
+ *     ignored), and calls that overlap in time need one each.
+ *   - Results do not depend on timing: repeated calls give the same bits.
+ *   - 0 <= n < 2^26 positions, 1 <= vocab <= 2^31 - 2, 1 <= dim <= 2^24.  */
+
+/* out[t] = scale * table[ids[t]], t < n.  A position whose id lies outside
+ * [0, vocab) (a padding id such as -1) reads nothing and gets zeros. */
+int embed_forward(const void* table, int32_t table_dtype, int64_t vocab, int64_t dim,
+                  const void* ids, int32_t ids_64, int64_t n, float scale, void* out,
+                  int32_t out_dtype, int64_t ld_out, hipStream_t stream);
+
+/* Device workspace embed_backward needs (0 for n == 0 or sizes it refuses).
+ * Host-only. */
+size_t embed_backward_workspace_size(int64_t n, int64_t vocab, int64_t dim);
+
+/* dtable[v] = scale * sum of dout[t] over the positions with ids[t] == v,
+ * in the order of the positions, for every v < vocab (rows that no position
+ * names become 0).  accumulate != 0: the sums are added to dtable, and rows
+ * that no position names are left as they were; a table that is also the
+ * LM head takes lm_loss_backward's gradient first and this one on top.
+ * Positions with an id outside [0, vocab) contribute nothing. */
+int embed_backward(const void* dout, int32_t dout_dtype, int64_t ld_dout, const void* ids,
+                   int32_t ids_64, int64_t n, float scale, void* dtable, int32_t dtable_dtype,
+                   int64_t vocab, int64_t dim, int32_t accumulate, void* workspace,
+                   size_t workspace_bytes, hipStream_t stream);
+
 const char* muon_status_string(int32_t status);
 const char* muon_last_error(void);
 

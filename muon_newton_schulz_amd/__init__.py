@@ -42,6 +42,7 @@ EXPORTED = [
     "state_stats_workspace_size", "state_stats",
     "muon_clip_plan_create", "muon_clip_plan_destroy", "muon_clip_plan_table_bytes",
     "muon_clip_plan_upload", "muon_clip",
+    "embed_forward", "embed_backward", "embed_backward_workspace_size",
 ]
 
 MUON_CLIP_FROBENIUS = 0
@@ -160,6 +161,11 @@ def lib() -> ctypes.CDLL:
     L.muon_clip_plan_table_bytes.restype = SZ
     L.muon_clip_plan_upload.argtypes = [P, P, SZ, P]
     L.muon_clip.argtypes = [P, P, I32, ctypes.c_float, P, P, SZ, P, P, P]
+    F = ctypes.c_float
+    L.embed_forward.argtypes = [P, I32, I64, I64, P, I32, I64, F, P, I32, I64, P]
+    L.embed_backward_workspace_size.argtypes = [I64, I64, I64]
+    L.embed_backward_workspace_size.restype = SZ
+    L.embed_backward.argtypes = [P, I32, I64, P, I32, I64, F, P, I32, I64, I64, I32, P, SZ, P]
     L.muon_status_string.argtypes = [I32]
     L.muon_status_string.restype = ctypes.c_char_p
     L.muon_last_error.argtypes = []
@@ -167,7 +173,8 @@ def lib() -> ctypes.CDLL:
     for name in EXPORTED:
         if name not in ("muon_plan_destroy", "muon_clip_plan_destroy", "muon_status_string",
                         "muon_last_error", "muon_plan_table_bytes", "muon_clip_plan_table_bytes",
-                        "grad_norm_clip_workspace_size", "state_stats_workspace_size"):
+                        "grad_norm_clip_workspace_size", "state_stats_workspace_size",
+                        "embed_backward_workspace_size"):
             getattr(L, name).restype = ctypes.c_int
     _lib_handle = L
     return L
@@ -646,3 +653,167 @@ def muon_clip(plan: MuonClipPlan, params, mode, tau: float, max_logits=None, wor
                            _ptr(max_logits), _ptr(workspace),
                            _nbytes(workspace) if workspace is not None else 0,
                            _ptr(norms_out), _ptr(scales_out), _stream(stream)))
+
+
+# ------------------------------------------- operators that write gradients
+#
+# They take tensors of one GPU, which need not be torch's current device, and
+# run on that GPU's current stream unless ``stream`` names another of its
+# streams.  What a call allocates (outputs and workspaces left out) belongs
+# to the stream the call runs on.
+
+TRAIN = (MUON_DTYPE_FP32, MUON_DTYPE_BF16)
+
+
+def _rows(t, name: str, rows: int, cols: int, dtypes=TRAIN):
+    """A GPU tensor of ``rows`` x ``cols`` whose rows are contiguous, with any
+    row stride of at least ``cols``.  Returns the row stride."""
+    if t is None:
+        raise MuonError(MUON_ERR_INVALID_ARG, f"{name} is None")
+    if not getattr(t, "is_cuda", False):
+        raise MuonError(MUON_ERR_INVALID_ARG, f"{name} must be a GPU tensor")
+    if tuple(t.shape) != (rows, cols):
+        raise MuonError(MUON_ERR_BAD_SHAPE,
+                        f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
+    if dtype_code(t.dtype) not in dtypes:
+        raise MuonError(MUON_ERR_BAD_DTYPE, f"{name} has dtype {t.dtype}")
+    if cols > 1 and t.stride(1) != 1:
+        raise MuonError(MUON_ERR_INVALID_ARG, f"{name}: a row's elements must be contiguous")
+    if rows <= 1:
+        return cols
+    if t.stride(0) < cols:
+        raise MuonError(MUON_ERR_INVALID_ARG, f"{name}: rows overlap (row stride {t.stride(0)})")
+    return t.stride(0)
+
+
+def _block(t, name: str, shape, dtypes=TRAIN):
+    """A contiguous GPU tensor of exactly ``shape``."""
+    _buf(t, name, dtypes=dtypes)
+    if tuple(t.shape) != tuple(shape):
+        raise MuonError(MUON_ERR_BAD_SHAPE,
+                        f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t
+
+
+def _index(t, name: str, numel: Optional[int] = None) -> int:
+    """A contiguous GPU tensor of int32 or int64.  Returns 1 for int64."""
+    import torch
+    _buf(t, name)
+    if t.dtype not in (torch.int32, torch.int64):
+        raise MuonError(MUON_ERR_BAD_DTYPE, f"{name} must be int32 or int64, has {t.dtype}")
+    if numel is not None and t.numel() != numel:
+        raise MuonError(MUON_ERR_BAD_SHAPE, f"{name} has {t.numel()} elements, expected {numel}")
+    return int(t.dtype == torch.int64)
+
+
+def _one_device(**tensors):
+    dev = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise MuonError(MUON_ERR_INVALID_ARG, f"{name} is on {t.device}, others on {dev}")
+    return dev
+
+
+class _Launch:
+    """Makes ``dev`` current, and ``stream`` (if given) the stream that torch
+    allocates on, around one call; ``handle`` is the hipStream_t."""
+
+    def __init__(self, dev, stream):
+        import torch
+        self._dev = torch.cuda.device(dev)
+        self._stream = None
+        if stream is None:
+            self.handle = torch.cuda.current_stream(dev).cuda_stream
+            return
+        if isinstance(stream, int):
+            stream = (torch.cuda.ExternalStream(stream, device=dev) if stream
+                      else torch.cuda.default_stream(dev))
+        if stream.device != dev:
+            raise MuonError(MUON_ERR_INVALID_ARG, f"stream is on {stream.device}, tensors on {dev}")
+        self.handle = stream.cuda_stream
+        self._stream = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        self._dev.__enter__()
+        if self._stream is not None:
+            self._stream.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self._stream is not None:
+            self._stream.__exit__(*exc)
+        self._dev.__exit__(*exc)
+
+
+def _workspace(workspace, need: int, dev):
+    """The caller's workspace, checked, or a new one on the call's stream."""
+    import torch
+    if workspace is None:
+        return torch.empty(max(1, need), dtype=torch.uint8, device=dev)
+    _buf(workspace, "workspace")
+    return workspace
+
+
+# ---------------------------------------------------------------- embedding
+
+def embed_forward(table, ids, scale: float = 1.0, out=None, out_dtype=None, stream=None):
+    """``scale * table[ids]`` for ids (int32 or int64) of any shape; zeros for
+    an id outside [0, vocab).  out: [ids.numel(), dim], rows may be strided;
+    without it a tensor of shape (*ids.shape, dim) and dtype ``out_dtype``
+    (the table's by default) is allocated.  Returns the output."""
+    import torch
+    _buf(table, "table", dtypes=TRAIN)
+    if len(table.shape) != 2:
+        raise MuonError(MUON_ERR_BAD_SHAPE, f"table must be [vocab, dim], is {tuple(table.shape)}")
+    vocab, dim = table.shape
+    i64 = _index(ids, "ids")
+    n = ids.numel()
+    if out_dtype is not None and dtype_code(out_dtype) not in TRAIN:
+        raise MuonError(MUON_ERR_BAD_DTYPE, f"out_dtype {out_dtype}")
+    ld = dim
+    if out is not None:
+        ld = _rows(out, "out", n, dim)
+        if out_dtype is not None and dtype_code(out_dtype) != dtype_code(out.dtype):
+            raise MuonError(MUON_ERR_BAD_DTYPE, f"out has dtype {out.dtype}, not {out_dtype}")
+    dev = _one_device(table=table, ids=ids, out=out)
+    with _Launch(dev, stream) as on:
+        if out is None:
+            td = {MUON_DTYPE_FP32: torch.float32, MUON_DTYPE_BF16: torch.bfloat16}
+            dt = table.dtype if out_dtype is None else td[dtype_code(out_dtype)]
+            out = torch.empty((*ids.shape, dim), dtype=dt, device=dev)
+        _check(lib().embed_forward(_ptr(table), dtype_code(table.dtype), vocab, dim, _ptr(ids), i64,
+                                   n, float(scale), _ptr(out), dtype_code(out.dtype), ld,
+                                   on.handle))
+    return out
+
+
+def embed_backward_workspace_size(n: int, vocab: int, dim: int) -> int:
+    return int(lib().embed_backward_workspace_size(int(n), int(vocab), int(dim)))
+
+
+def embed_backward(dout, ids, dtable, scale: float = 1.0, accumulate: bool = False,
+                   workspace=None, stream=None):
+    """The dense table gradient: ``dtable[v] = scale * sum of dout[t]`` over the
+    positions with ``ids[t] == v`` (added to dtable with ``accumulate``).
+    dout: [ids.numel(), dim], rows may be strided; dtable: contiguous
+    [vocab, dim], a view of a flat gradient buffer for instance.  Returns
+    dtable."""
+    _buf(dtable, "dtable", dtypes=TRAIN)
+    if len(dtable.shape) != 2:
+        raise MuonError(MUON_ERR_BAD_SHAPE,
+                        f"dtable must be [vocab, dim], is {tuple(dtable.shape)}")
+    vocab, dim = dtable.shape
+    i64 = _index(ids, "ids")
+    n = ids.numel()
+    ld = _rows(dout, "dout", n, dim)
+    dev = _one_device(dtable=dtable, ids=ids, dout=dout, workspace=workspace)
+    with _Launch(dev, stream) as on:
+        ws = _workspace(workspace, embed_backward_workspace_size(n, vocab, dim), dev)
+        _check(lib().embed_backward(_ptr(dout), dtype_code(dout.dtype), ld, _ptr(ids), i64, n,
+                                    float(scale), _ptr(dtable), dtype_code(dtable.dtype), vocab,
+                                    dim, int(bool(accumulate)), _ptr(ws), _nbytes(ws), on.handle))
+    return dtable
