@@ -502,6 +502,70 @@ int embed_backward(const void* dout, int32_t dout_dtype, int64_t ld_dout, const 
                    int64_t vocab, int64_t dim, int32_t accumulate, void* workspace,
                    size_t workspace_bytes, hipStream_t stream);
 
+/* ---- softmax cross entropy over a large vocabulary -------------------- */
+
+/* The loss of a linear head, whose weight [vocab, dim] AdamW steps (the LM
+ * head, or the embedding table itself), in pieces of the vocabulary: the
+ * logits hidden weight^T are never stored.
+ *   lse[t]  = log sum_v exp(hidden[t] . weight[v])
+ *   loss[t] = lse[t] - hidden[t] . weight[targets[t]]
+ * A row whose target lies outside [0, vocab) (an ignore index such as -100)
+ * has loss 0 and no gradient.  Types: hidden and weight share dtype; logits,
+ * statistics and sums are fp32; backward's g (below) is rounded to dtype
+ * before its products.  vocab <= 65535 * 128.
+ * A NaN in a row's logits makes its loss and lse NaN. */
+
+/* Device workspace of the two calls below: with backward != 0 enough for
+ * both, else for the forward (0 for n == 0 or sizes they refuse).  The
+ * backward needs about 256 MiB at least once n * vocab reaches that, for the
+ * gradients of one piece of the logits, and fp32 sums of dhidden.
+ * Host-only. */
+size_t lm_loss_workspace_size(int64_t n, int64_t vocab, int64_t dim, int32_t dtype,
+                              int32_t backward);
+
+/* loss, lse: fp32, n values. */
+int lm_loss_forward(const void* hidden, int64_t ld_hidden, const void* weight, int32_t dtype,
+                    const void* targets, int32_t targets_64, int64_t n, int64_t vocab,
+                    int64_t dim, float* loss, float* lse, void* workspace,
+                    size_t workspace_bytes, hipStream_t stream);
+
+/* Gradients of sum_t dloss[t] loss[t], with lse from the forward call:
+ *   g[t][v] = (exp(l[t][v] - lse[t]) - [v == targets[t]]) * dloss[t]
+ *   dhidden = g weight,   dweight = g^T hidden   (added with accumulate != 0)
+ * dhidden and dweight: either may be null (not computed); each has a type
+ * of its own; dweight is contiguous [vocab, dim]. */
+int lm_loss_backward(const void* hidden, int64_t ld_hidden, const void* weight, int32_t dtype,
+                     const void* targets, int32_t targets_64, int64_t n, int64_t vocab,
+                     int64_t dim, const float* lse, const float* dloss, void* dhidden,
+                     int32_t dhidden_dtype, int64_t ld_dhidden, void* dweight,
+                     int32_t dweight_dtype, int32_t accumulate, void* workspace,
+                     size_t workspace_bytes, hipStream_t stream);
+
+/* ---- matrix products grouped by expert ------------------------------- */
+
+/* Products with the contiguous expert blocks that muon_step steps ([EP]).
+ * Rows sorted by expert: expert e owns rows [offsets[e], offsets[e + 1]) of
+ * the activations (offsets: experts + 1 non-decreasing int32 in device
+ * memory, read by the kernels; values outside [0, rows] are clamped, an
+ * expert whose range is not positive has no rows).  Rows outside every range
+ * are neither read nor written.  1 <= experts <= 4096, 0 <= rows < 2^26,
+ * sides of a weight in [1, 2^22].
+ *
+ * y[r] = x[r] w[e] with w [experts][k][n] (trans_w == 0), or x[r] w[e]^T with
+ * w [experts][n][k] (trans_w != 0).  The gradient by x is the same call on dy
+ * with the other trans_w. */
+int expert_matmul(const void* x, int64_t ldx, const void* w, int32_t dtype,
+                  const int32_t* offsets, int32_t experts, int64_t rows, int64_t k, int64_t n,
+                  int32_t trans_w, void* y, int32_t y_dtype, int64_t ldy, hipStream_t stream);
+
+/* dw[e] = sum over expert e's rows of a[r]^T b[r], [experts][m][n] contiguous
+ * (added with accumulate != 0; without it an expert without rows gets
+ * zeros).  The weight gradient of y = x w is (a, b) = (x, dy); of
+ * y = x w^T it is (dy, x). */
+int expert_wgrad(const void* a, int64_t lda, const void* b, int64_t ldb, int32_t dtype,
+                 const int32_t* offsets, int32_t experts, int64_t rows, int64_t m, int64_t n,
+                 void* dw, int32_t dw_dtype, int32_t accumulate, hipStream_t stream);
+
 const char* muon_status_string(int32_t status);
 const char* muon_last_error(void);
 

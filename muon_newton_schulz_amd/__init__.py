@@ -43,6 +43,8 @@ EXPORTED = [
     "muon_clip_plan_create", "muon_clip_plan_destroy", "muon_clip_plan_table_bytes",
     "muon_clip_plan_upload", "muon_clip",
     "embed_forward", "embed_backward", "embed_backward_workspace_size",
+    "lm_loss_workspace_size", "lm_loss_forward", "lm_loss_backward",
+    "expert_matmul", "expert_wgrad",
 ]
 
 MUON_CLIP_FROBENIUS = 0
@@ -166,6 +168,13 @@ def lib() -> ctypes.CDLL:
     L.embed_backward_workspace_size.argtypes = [I64, I64, I64]
     L.embed_backward_workspace_size.restype = SZ
     L.embed_backward.argtypes = [P, I32, I64, P, I32, I64, F, P, I32, I64, I64, I32, P, SZ, P]
+    L.lm_loss_workspace_size.argtypes = [I64, I64, I64, I32, I32]
+    L.lm_loss_workspace_size.restype = SZ
+    L.lm_loss_forward.argtypes = [P, I64, P, I32, P, I32, I64, I64, I64, P, P, P, SZ, P]
+    L.lm_loss_backward.argtypes = [P, I64, P, I32, P, I32, I64, I64, I64, P, P, P, I32, I64, P,
+                                   I32, I32, P, SZ, P]
+    L.expert_matmul.argtypes = [P, I64, P, I32, P, I32, I64, I64, I64, I32, P, I32, I64, P]
+    L.expert_wgrad.argtypes = [P, I64, P, I64, I32, P, I32, I64, I64, I64, P, I32, I32, P]
     L.muon_status_string.argtypes = [I32]
     L.muon_status_string.restype = ctypes.c_char_p
     L.muon_last_error.argtypes = []
@@ -174,7 +183,7 @@ def lib() -> ctypes.CDLL:
         if name not in ("muon_plan_destroy", "muon_clip_plan_destroy", "muon_status_string",
                         "muon_last_error", "muon_plan_table_bytes", "muon_clip_plan_table_bytes",
                         "grad_norm_clip_workspace_size", "state_stats_workspace_size",
-                        "embed_backward_workspace_size"):
+                        "embed_backward_workspace_size", "lm_loss_workspace_size"):
             getattr(L, name).restype = ctypes.c_int
     _lib_handle = L
     return L
@@ -817,3 +826,160 @@ def embed_backward(dout, ids, dtable, scale: float = 1.0, accumulate: bool = Fal
                                     float(scale), _ptr(dtable), dtype_code(dtable.dtype), vocab,
                                     dim, int(bool(accumulate)), _ptr(ws), _nbytes(ws), on.handle))
     return dtable
+
+
+# --------------------------------------------------------- vocabulary loss
+
+def lm_loss_workspace_size(n: int, vocab: int, dim: int, dtype, backward: bool = True) -> int:
+    return int(lib().lm_loss_workspace_size(int(n), int(vocab), int(dim), dtype_code(dtype),
+                                            int(bool(backward))))
+
+
+def _loss_args(hidden, weight, targets):
+    _buf(weight, "weight", dtypes=TRAIN)
+    if len(weight.shape) != 2:
+        raise MuonError(MUON_ERR_BAD_SHAPE,
+                        f"weight must be [vocab, dim], is {tuple(weight.shape)}")
+    vocab, dim = weight.shape
+    t64 = _index(targets, "targets")
+    n = targets.numel()
+    ld = _rows(hidden, "hidden", n, dim, (dtype_code(weight.dtype),))
+    return n, vocab, dim, ld, t64
+
+
+def lm_loss_forward(hidden, weight, targets, loss=None, lse=None, workspace=None, stream=None):
+    """Softmax cross entropy of ``hidden @ weight.T`` per row, without storing
+    the logits.  hidden: [n, dim], rows may be strided; weight: contiguous
+    [vocab, dim] of the same dtype; targets: n int32 or int64, one outside
+    [0, vocab) marks a row without loss.  Returns (loss, lse), fp32 of n."""
+    import torch
+    n, vocab, dim, ld, t64 = _loss_args(hidden, weight, targets)
+    for name, t in (("loss", loss), ("lse", lse)):
+        if t is not None:
+            _block(t, name, (n,), F32)
+    dev = _one_device(weight=weight, hidden=hidden, targets=targets, loss=loss, lse=lse,
+                      workspace=workspace)
+    with _Launch(dev, stream) as on:
+        if loss is None:
+            loss = torch.empty(n, dtype=torch.float32, device=dev)
+        if lse is None:
+            lse = torch.empty(n, dtype=torch.float32, device=dev)
+        ws = _workspace(workspace, lm_loss_workspace_size(n, vocab, dim, weight.dtype, False), dev)
+        _check(lib().lm_loss_forward(_ptr(hidden), ld, _ptr(weight), dtype_code(weight.dtype),
+                                     _ptr(targets), t64, n, vocab, dim, _ptr(loss), _ptr(lse),
+                                     _ptr(ws), _nbytes(ws), on.handle))
+    return loss, lse
+
+
+def lm_loss_backward(hidden, weight, targets, lse, dloss, dhidden=None, dweight=None,
+                     accumulate: bool = False, workspace=None, stream=None):
+    """Gradients of ``sum(dloss * loss)`` by hidden and weight; lse from
+    lm_loss_forward, dloss fp32 of n.  dhidden ([n, dim], rows may be strided)
+    and dweight (contiguous [vocab, dim], a view of a flat gradient buffer for
+    instance; ``accumulate`` adds to it) may be bf16 or fp32, are allocated
+    in hidden's dtype where None, and not computed where False.  Returns
+    (dhidden, dweight), None for what was not computed."""
+    import torch
+    n, vocab, dim, ld, t64 = _loss_args(hidden, weight, targets)
+    _block(lse, "lse", (n,), F32)
+    _block(dloss, "dloss", (n,), F32)
+    ld_dh = dim
+    if dhidden is not None and dhidden is not False:
+        ld_dh = _rows(dhidden, "dhidden", n, dim)
+    if dweight is not None and dweight is not False:
+        _block(dweight, "dweight", (vocab, dim))
+    elif accumulate:
+        raise MuonError(MUON_ERR_INVALID_ARG, "accumulate needs a dweight to add to")
+    dev = _one_device(weight=weight, hidden=hidden, targets=targets, lse=lse, dloss=dloss,
+                      dhidden=None if dhidden is False else dhidden,
+                      dweight=None if dweight is False else dweight, workspace=workspace)
+    with _Launch(dev, stream) as on:
+        if dhidden is None:
+            dhidden = torch.empty((n, dim), dtype=hidden.dtype, device=dev)
+        if dweight is None:
+            dweight = torch.empty((vocab, dim), dtype=weight.dtype, device=dev)
+        dhidden = None if dhidden is False else dhidden
+        dweight = None if dweight is False else dweight
+        ws = _workspace(workspace, lm_loss_workspace_size(n, vocab, dim, weight.dtype), dev)
+        _check(lib().lm_loss_backward(
+            _ptr(hidden), ld, _ptr(weight), dtype_code(weight.dtype), _ptr(targets), t64, n, vocab,
+            dim, _ptr(lse), _ptr(dloss), _ptr(dhidden),
+            dtype_code(weight.dtype if dhidden is None else dhidden.dtype), ld_dh, _ptr(dweight),
+            dtype_code(weight.dtype if dweight is None else dweight.dtype), int(bool(accumulate)),
+            _ptr(ws), _nbytes(ws), on.handle))
+    return dhidden, dweight
+
+
+# ---------------------------------------------------------- expert products
+
+def _offsets(t, experts: int):
+    import torch
+    _buf(t, "offsets")
+    if t.dtype != torch.int32:
+        raise MuonError(MUON_ERR_BAD_DTYPE, f"offsets must be int32, has {t.dtype}")
+    if t.numel() != experts + 1:
+        raise MuonError(MUON_ERR_BAD_SHAPE,
+                        f"offsets has {t.numel()} elements, expected {experts + 1}")
+
+
+def expert_matmul(x, w, offsets, trans: bool = False, out=None, out_dtype=None, stream=None):
+    """Row r of expert e (offsets[e] <= r < offsets[e + 1], int32 on the GPU)
+    times that expert's weight: ``x[r] @ w[e]`` with w [experts, k, n], or with
+    ``trans`` ``x[r] @ w[e].T`` with w [experts, n, k].  x: [rows, k] of w's
+    dtype, rows may be strided.  out: [rows, n], rows may be strided; its
+    rows that belong to no expert are left as they were.  Without it a tensor
+    of ``out_dtype`` (x's by default) is allocated, with zeros in those rows.
+    Returns the output."""
+    import torch
+    _buf(w, "w", dtypes=TRAIN)
+    if len(w.shape) != 3:
+        raise MuonError(MUON_ERR_BAD_SHAPE, f"w must be [experts, ., .], is {tuple(w.shape)}")
+    experts, k, n = w.shape
+    if trans:
+        k, n = n, k
+    if x is None or len(x.shape) != 2:
+        raise MuonError(MUON_ERR_BAD_SHAPE, "x must be [rows, k]")
+    rows = x.shape[0]
+    ldx = _rows(x, "x", rows, k, (dtype_code(w.dtype),))
+    _offsets(offsets, experts)
+    if out_dtype is not None and dtype_code(out_dtype) not in TRAIN:
+        raise MuonError(MUON_ERR_BAD_DTYPE, f"out_dtype {out_dtype}")
+    ldy = n
+    if out is not None:
+        ldy = _rows(out, "out", rows, n)
+        if out_dtype is not None and dtype_code(out_dtype) != dtype_code(out.dtype):
+            raise MuonError(MUON_ERR_BAD_DTYPE, f"out has dtype {out.dtype}, not {out_dtype}")
+    dev = _one_device(w=w, x=x, offsets=offsets, out=out)
+    with _Launch(dev, stream) as on:
+        if out is None:
+            td = {MUON_DTYPE_FP32: torch.float32, MUON_DTYPE_BF16: torch.bfloat16}
+            dt = x.dtype if out_dtype is None else td[dtype_code(out_dtype)]
+            out = torch.zeros((rows, n), dtype=dt, device=dev)
+        _check(lib().expert_matmul(_ptr(x), ldx, _ptr(w), dtype_code(w.dtype), _ptr(offsets),
+                                   experts, rows, k, n, int(bool(trans)), _ptr(out),
+                                   dtype_code(out.dtype), ldy, on.handle))
+    return out
+
+
+def expert_wgrad(a, b, offsets, dw, accumulate: bool = False, stream=None):
+    """``dw[e] = a_e.T @ b_e`` over expert e's rows (added to dw with
+    ``accumulate``): the weight gradient of ``expert_matmul(x, w, offsets)``
+    with (a, b) = (x, dy), and of its trans form with (dy, x).  a: [rows, m],
+    b: [rows, n] of one dtype, rows may be strided; dw: contiguous
+    [experts, m, n], bf16 or fp32.  Returns dw."""
+    _buf(dw, "dw", dtypes=TRAIN)
+    if len(dw.shape) != 3:
+        raise MuonError(MUON_ERR_BAD_SHAPE, f"dw must be [experts, m, n], is {tuple(dw.shape)}")
+    experts, m, n = dw.shape
+    if a is None or len(a.shape) != 2:
+        raise MuonError(MUON_ERR_BAD_SHAPE, "a must be [rows, m]")
+    rows = a.shape[0]
+    lda = _rows(a, "a", rows, m)
+    ldb = _rows(b, "b", rows, n, (dtype_code(a.dtype),))
+    _offsets(offsets, experts)
+    dev = _one_device(dw=dw, a=a, b=b, offsets=offsets)
+    with _Launch(dev, stream) as on:
+        _check(lib().expert_wgrad(_ptr(a), lda, _ptr(b), ldb, dtype_code(a.dtype), _ptr(offsets),
+                                  experts, rows, m, n, _ptr(dw), dtype_code(dw.dtype),
+                                  int(bool(accumulate)), on.handle))
+    return dw

@@ -1,0 +1,204 @@
+// Matrix products grouped by expert, with ragged group sizes.
+//
+//   y_r  = x_r W_e   or  x_r W_e^T       for offsets[e] <= r < offsets[e+1]
+//   dW_e = sum over those r of a_r^T b_r                     (+ dW_e)
+//
+// The group sizes are device data: no call reads them on the host.  Every
+// workgroup of a product finds its expert and row tile by a scan of the
+// offsets; the launch has as many row tiles as any sizes can need.
+#include <algorithm>
+
+#include "train_gemm.h"
+
+namespace muon {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Rows of expert e, whatever the offsets hold: within [0, rows), never
+// negative.
+__device__ __forceinline__ void group_rows(const int32_t* off, int e, int rows, int& lo, int& n) {
+  lo = min(max(off[e], 0), rows);
+  n = max(min(off[e + 1], rows) - lo, 0);
+}
+
+struct RowTile {
+  int e, lo, n, tile;  // expert, its first row and row count, tile within it; e < 0: none
+};
+// The t-th row tile of the grouped list, each group cut into tiles of bm
+// rows.  Every wave scans the offsets, 64 experts at a time.
+__device__ __forceinline__ RowTile find_row_tile(const int32_t* off, int experts, int rows, int bm,
+                                                 int t) {
+  const int lane = threadIdx.x & 63;
+  int base = 0;
+  for (int e0 = 0; e0 < experts; e0 += 64) {
+    int lo = 0, n = 0;
+    if (e0 + lane < experts) group_rows(off, e0 + lane, rows, lo, n);
+    const int tiles = (n + bm - 1) / bm;
+    int s = tiles;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int u = __shfl_up(s, o, 64);
+      if (lane >= o) s += u;
+    }
+    const uint64_t over = __ballot(base + s > t);
+    if (over != 0) {
+      const int l = __ffsll(static_cast<unsigned long long>(over)) - 1;
+      return RowTile{e0 + l, __shfl(lo, l, 64), __shfl(n, l, 64),
+                     t - base - __shfl(s - tiles, l, 64)};
+    }
+    base += __shfl(s, 63, 64);
+  }
+  return RowTile{-1, 0, 0, 0};
+}
+
+struct MatmulArgs {
+  const void* x;
+  const void* w;
+  void* y;
+  const int32_t* off;
+  int64_t ldx, ldy;
+  int experts, rows, K, N;
+};
+
+// QKS: W_e is [K][N] (y = x W_e); else [N][K] (y = x W_e^T).
+template <typename Core, typename T, bool QKS, typename TO>
+__global__ __launch_bounds__(kThreads) void k_expert_matmul(MatmulArgs a) {
+  __shared__ __attribute__((aligned(16))) char smem[Core::kLdsBytes];
+  const RowTile rt = find_row_tile(a.off, a.experts, a.rows, Core::BM, blockIdx.x);
+  if (rt.e < 0) return;
+  const int i0 = rt.tile * Core::BM, j0 = blockIdx.y * Core::BN;
+  const int64_t row0 = static_cast<int64_t>(rt.lo) + i0;
+  const T* P = static_cast<const T*>(a.x) + row0 * a.ldx;
+  const T* W = static_cast<const T*>(a.w) + static_cast<int64_t>(rt.e) * a.K * a.N;
+  f32x16_t acc[Core::NJ][Core::MI];
+  if (QKS) Core::run(P, a.ldx, rt.n - i0, W + j0, a.N, a.N - j0, a.K, acc, smem);
+  else Core::run(P, a.ldx, rt.n - i0, W + static_cast<int64_t>(j0) * a.K, a.K, a.N - j0, a.K, acc,
+                 smem);
+  TO* Y = static_cast<TO*>(a.y) + row0 * a.ldy + j0;
+  each_quad<Core>(acc, [&](int i, int j, f32x4_t v) {
+    if (i < rt.n - i0) store_quad(Y + i * a.ldy + j, a.N - j0 - j, v, false);
+  });
+}
+
+struct WgradArgs {
+  const void* a;
+  const void* b;
+  void* dw;
+  const int32_t* off;
+  int64_t lda, ldb;
+  int experts, rows, M, N, accumulate;
+};
+
+template <typename Core, typename T, typename TO>
+__global__ __launch_bounds__(kThreads) void k_expert_wgrad(WgradArgs g) {
+  __shared__ __attribute__((aligned(16))) char smem[Core::kLdsBytes];
+  const int e = blockIdx.z, i0 = blockIdx.x * Core::BM, j0 = blockIdx.y * Core::BN;
+  int lo, n;
+  group_rows(g.off, e, g.rows, lo, n);
+  if (n == 0 && g.accumulate) return;
+  f32x16_t acc[Core::NJ][Core::MI];
+  Core::run(static_cast<const T*>(g.a) + lo * g.lda + i0, g.lda, g.M - i0,
+            static_cast<const T*>(g.b) + lo * g.ldb + j0, g.ldb, g.N - j0, n, acc, smem);
+  TO* C = static_cast<TO*>(g.dw) + static_cast<int64_t>(e) * g.M * g.N +
+          static_cast<int64_t>(i0) * g.N + j0;
+  each_quad<Core>(acc, [&](int i, int j, f32x4_t v) {
+    if (i < g.M - i0)
+      store_quad(C + static_cast<int64_t>(i) * g.N + j, g.N - j0 - j, v, g.accumulate != 0);
+  });
+}
+
+// -------------------------------------------------------------------- host
+
+constexpr int kMaxExperts = 4096;
+
+template <typename T, typename TO>
+void run_matmul(const MatmulArgs& a, bool trans, hipStream_t s) {
+  using NT = AnyCore<T, false, false>;
+  using NN = AnyCore<T, false, true>;
+  const dim3 grid(static_cast<unsigned>(a.rows / NT::BM + std::min(a.experts, a.rows)),
+                  static_cast<unsigned>((a.N + NT::BN - 1) / NT::BN));
+  if (trans)
+    hipLaunchKernelGGL((k_expert_matmul<NT, T, false, TO>), grid, dim3(kThreads), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_expert_matmul<NN, T, true, TO>), grid, dim3(kThreads), 0, s, a);
+}
+
+template <typename T, typename TO>
+void run_wgrad(const WgradArgs& g, hipStream_t s) {
+  using TN = AnyCore<T, true, true>;
+  const dim3 grid(static_cast<unsigned>((g.M + TN::BM - 1) / TN::BM),
+                  static_cast<unsigned>((g.N + TN::BN - 1) / TN::BN),
+                  static_cast<unsigned>(g.experts));
+  hipLaunchKernelGGL((k_expert_wgrad<TN, T, TO>), grid, dim3(kThreads), 0, s, g);
+}
+
+int check_group(int64_t rows, int32_t experts, int64_t k, int64_t n) {
+  if (rows < 0 || rows > kMaxTokens)
+    return set_error(MUON_ERR_BAD_SHAPE, "rows must be in [0, 2^26)");
+  if (experts < 1 || experts > kMaxExperts)
+    return set_error(MUON_ERR_BAD_SHAPE, "experts must be in [1, 4096]");
+  // 65535 tiles of 128 is the least any launch dimension holds
+  if (k < 1 || k > (1 << 22) || n < 1 || n > (1 << 22))
+    return set_error(MUON_ERR_BAD_SHAPE, "a weight's sides must be in [1, 2^22]");
+  return MUON_OK;
+}
+
+}  // namespace
+}  // namespace muon
+
+using namespace muon;
+
+extern "C" {
+
+int expert_matmul(const void* x, int64_t ldx, const void* w, int32_t dtype,
+                  const int32_t* offsets, int32_t experts, int64_t rows, int64_t k, int64_t n,
+                  int32_t trans_w, void* y, int32_t y_dtype, int64_t ldy, hipStream_t stream) {
+  const int rc = check_group(rows, experts, k, n);
+  if (rc != MUON_OK) return rc;
+  if (!train_dtype_ok(dtype) || !train_dtype_ok(y_dtype))
+    return set_error(MUON_ERR_BAD_DTYPE, "x, w and y must be fp32 or bf16");
+  if (ldx < k || ldy < n) return set_error(MUON_ERR_BAD_SHAPE, "ldx < k or ldy < n");
+  if (rows == 0) return MUON_OK;
+  if (x == nullptr || w == nullptr || offsets == nullptr || y == nullptr)
+    return set_error(MUON_ERR_INVALID_ARG, "x, w, offsets or y is null");
+  const MatmulArgs a{x, w, y, offsets, ldx, ldy, experts, static_cast<int>(rows),
+                     static_cast<int>(k), static_cast<int>(n)};
+  const bool tr = trans_w != 0, yb = y_dtype == MUON_DTYPE_BF16;
+  if (dtype == MUON_DTYPE_BF16) {
+    if (yb) run_matmul<uint16_t, uint16_t>(a, tr, stream);
+    else run_matmul<uint16_t, float>(a, tr, stream);
+  } else {
+    if (yb) run_matmul<float, uint16_t>(a, tr, stream);
+    else run_matmul<float, float>(a, tr, stream);
+  }
+  return check_launch("expert product launch");
+}
+
+int expert_wgrad(const void* a, int64_t lda, const void* b, int64_t ldb, int32_t dtype,
+                 const int32_t* offsets, int32_t experts, int64_t rows, int64_t m, int64_t n,
+                 void* dw, int32_t dw_dtype, int32_t accumulate, hipStream_t stream) {
+  const int rc = check_group(rows, experts, m, n);
+  if (rc != MUON_OK) return rc;
+  if (!train_dtype_ok(dtype) || !train_dtype_ok(dw_dtype))
+    return set_error(MUON_ERR_BAD_DTYPE, "a, b and dw must be fp32 or bf16");
+  if (lda < m || ldb < n) return set_error(MUON_ERR_BAD_SHAPE, "lda < m or ldb < n");
+  if (dw == nullptr || offsets == nullptr)
+    return set_error(MUON_ERR_INVALID_ARG, "dw or offsets is null");
+  if (rows > 0 && (a == nullptr || b == nullptr))
+    return set_error(MUON_ERR_INVALID_ARG, "a or b is null");
+  if (rows == 0 && accumulate) return MUON_OK;
+  const WgradArgs g{a, b, dw, offsets, lda, ldb, experts, static_cast<int>(rows),
+                    static_cast<int>(m), static_cast<int>(n), accumulate != 0};
+  const bool wb = dw_dtype == MUON_DTYPE_BF16;
+  if (dtype == MUON_DTYPE_BF16) {
+    if (wb) run_wgrad<uint16_t, uint16_t>(g, stream);
+    else run_wgrad<uint16_t, float>(g, stream);
+  } else {
+    if (wb) run_wgrad<float, uint16_t>(g, stream);
+    else run_wgrad<float, float>(g, stream);
+  }
+  return check_launch("expert weight gradient launch");
+}
+
+}  // extern "C"

@@ -1,0 +1,534 @@
+// Softmax cross entropy of a linear head over a large vocabulary, without
+// keeping the logits, and its gradient.
+//
+//   l_tv   = h_t . W_v
+//   lse_t  = log sum_v exp l_tv,   loss_t = lse_t - l_{t, y_t}
+//   g_tv   = (exp(l_tv - lse_t) - [v = y_t]) dloss_t
+//   dh_t   = sum_v g_tv W_v,       dW_v   = sum_t g_tv h_t        (+ dW_v)
+//
+// Forward: every output tile of h W^T stays in registers; a row of it leaves
+// its maximum m and its sum of exp(l - m) (fp32), and the target's logit.
+// A second kernel joins the tiles of a row, in order.
+//
+// Backward, one piece of the vocabulary after another: the piece's logits
+// are computed again and turned into g in the epilogue (stored in the
+// operands' type: for bf16 the rounding is one half-step of each g, as the
+// matrix cores take it), then dW of the piece = g^T h and dh += g W, summed
+// over the pieces in fp32.  Few rows give few tiles of dh with a long sum:
+// it is split over workgroups, which add into fp32 sums of their own, and a
+// last kernel joins those in order.
+#include <algorithm>
+#include <cmath>
+
+#include "train_gemm.h"
+
+namespace muon {
+namespace {
+
+constexpr int kThreads = 256;
+
+// target of row t, -1 if it has none (outside [0, vocab))
+__device__ __forceinline__ int64_t target_of(const void* targets, int t64, int64_t t,
+                                             int64_t vocab) {
+  const int64_t v = t64 ? static_cast<const int64_t*>(targets)[t]
+                        : static_cast<int64_t>(static_cast<const int32_t*>(targets)[t]);
+  return v >= 0 && v < vocab ? v : -1;
+}
+
+// exp: the fp32 path takes the accurate one, the bf16 path the hardware's
+// (relative error 2^-21 at |x| = 8, against bf16's 2^-8)
+template <typename T>
+__device__ __forceinline__ float exp_of(float x) {
+  if constexpr (sizeof(T) == 4) return expf(x);
+  else return __expf(x);
+}
+
+// (m, s) <- (m, s) + (m2, s2): sums of exp(l - m) over disjoint sets.  A set
+// without a value above -inf has s = 0.
+__device__ __forceinline__ void join_stats(float& m, float& s, float m2, float s2) {
+  const float mm = fmaxf(m, m2);
+  const float a = m == mm ? s : s * expf(m - mm);
+  const float b = m2 == mm ? s2 : s2 * expf(m2 - mm);
+  m = mm;
+  s = a + b;
+}
+
+struct StatsArgs {
+  const void* h;
+  const void* w;
+  const void* targets;
+  float* tile_m;  // [vocabulary tiles][n]
+  float* tile_s;
+  float* at;      // [n], the target's logit
+  int64_t ldh, vocab;
+  int n, dim, t64;
+};
+
+// Row statistics of one tile: the maximum and the sum of a lane's 16 NJ
+// values of a row, joined with the lane that holds the row's other columns
+// (lane ^ 32), then with the waves beside it.
+template <typename Core, typename T>
+__global__ __launch_bounds__(kThreads) void k_loss_stats(StatsArgs a) {
+  __shared__ __attribute__((aligned(16))) char smem[Core::kLdsBytes];
+  const int i0 = blockIdx.x * Core::BM;
+  const int64_t v0 = static_cast<int64_t>(blockIdx.y) * Core::BN;
+  const int jn = static_cast<int>(a.vocab - v0 < Core::BN ? a.vocab - v0 : Core::BN);
+  f32x16_t acc[Core::NJ][Core::MI];
+  Core::run(static_cast<const T*>(a.h) + i0 * a.ldh, a.ldh, a.n - i0,
+            static_cast<const T*>(a.w) + v0 * a.dim, a.dim, jn, a.dim, acc, smem);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wi = wave % Core::WM, wj = wave / Core::WM;
+  const int jw = wj * 32 * Core::NJ + 4 * (lane >> 5);
+  float* red = reinterpret_cast<float*>(smem);  // [WN][BM][2]
+  static_assert(Core::WN * Core::BM * 8 <= Core::kLdsBytes, "the waves' row statistics");
+  __syncthreads();
+#pragma unroll
+  for (int bi = 0; bi < Core::MI; ++bi) {
+    const int i = wi * 32 * Core::MI + 32 * bi + (lane & 31);
+    const int64_t t = static_cast<int64_t>(i0) + i;
+    const bool row = t < a.n;
+    const int64_t tgt = row ? target_of(a.targets, a.t64, t, a.vocab) : -1;
+    float m = -INFINITY;
+#pragma unroll
+    for (int bj = 0; bj < Core::NJ; ++bj)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const int j = jw + 32 * bj + 8 * (v >> 2) + (v & 3);
+        if (j < jn) m = fmaxf(m, acc[bj][bi][v]);
+        if (tgt == v0 + j) a.at[t] = acc[bj][bi][v];
+      }
+    float s = 0.0f;
+#pragma unroll
+    for (int bj = 0; bj < Core::NJ; ++bj)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const int j = jw + 32 * bj + 8 * (v >> 2) + (v & 3);
+        const float x = acc[bj][bi][v];
+        if (j < jn && x != -INFINITY) s += exp_of<T>(x - m);
+      }
+    const float m2 = __shfl_xor(m, 32, 64), s2 = __shfl_xor(s, 32, 64);
+    if (lane < 32) {
+      join_stats(m, s, m2, s2);
+      red[(wj * Core::BM + i) * 2] = m;
+      red[(wj * Core::BM + i) * 2 + 1] = s;
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < Core::BM && i0 + i < a.n; i += kThreads) {
+    float m = red[2 * i], s = red[2 * i + 1];
+#pragma unroll
+    for (int w = 1; w < Core::WN; ++w)
+      join_stats(m, s, red[(w * Core::BM + i) * 2], red[(w * Core::BM + i) * 2 + 1]);
+    const int64_t o = static_cast<int64_t>(blockIdx.y) * a.n + i0 + i;
+    a.tile_m[o] = m;
+    a.tile_s[o] = s;
+  }
+}
+
+// Joins a row's tiles: lane l of the wave takes tiles l, l + 64, ... in
+// order, then the lanes are joined in a fixed tree.
+__global__ __launch_bounds__(kThreads) void k_loss_join(const float* __restrict__ tile_m,
+                                                        const float* __restrict__ tile_s,
+                                                        const float* __restrict__ at, int tiles,
+                                                        int n, const void* targets, int t64,
+                                                        int64_t vocab, float* __restrict__ loss,
+                                                        float* __restrict__ lse) {
+  // 64 rows x 4 parts of the tiles, so that loads run along rows
+  __shared__ float red[4][64][2];
+  const int r = threadIdx.x & 63, part = threadIdx.x >> 6;
+  const int t = blockIdx.x * 64 + r;
+  float m = -INFINITY, s = 0.0f;
+  if (t < n)
+    for (int k = part; k < tiles; k += 4)
+      join_stats(m, s, tile_m[static_cast<int64_t>(k) * n + t],
+                 tile_s[static_cast<int64_t>(k) * n + t]);
+  red[part][r][0] = m;
+  red[part][r][1] = s;
+  __syncthreads();
+  if (part != 0 || t >= n) return;
+  for (int p = 1; p < 4; ++p) join_stats(m, s, red[p][r][0], red[p][r][1]);
+  const float l = m + logf(s);
+  lse[t] = l;
+  loss[t] = target_of(targets, t64, t, vocab) >= 0 ? l - at[t] : 0.0f;
+}
+
+struct GradArgs {
+  const void* h;
+  const void* w;       // the piece's first row
+  const void* targets;
+  const float* lse;
+  const float* dloss;
+  void* g;             // [n][ldg]
+  int64_t ldh, ldg, vocab, v0;
+  int n, dim, len, t64;  // len: vocabulary rows of the piece
+};
+
+// g of the piece, in the operands' type.
+template <typename Core, typename T>
+__global__ __launch_bounds__(kThreads) void k_loss_g(GradArgs a) {
+  __shared__ __attribute__((aligned(16))) char smem[Core::kLdsBytes];
+  const int i0 = blockIdx.x * Core::BM, j0 = blockIdx.y * Core::BN;
+  f32x16_t acc[Core::NJ][Core::MI];
+  Core::run(static_cast<const T*>(a.h) + i0 * a.ldh, a.ldh, a.n - i0,
+            static_cast<const T*>(a.w) + static_cast<int64_t>(j0) * a.dim, a.dim, a.len - j0,
+            a.dim, acc, smem);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int iw = (wave % Core::WM) * 32 * Core::MI + (lane & 31);
+  float lse[Core::MI], dl[Core::MI];
+  int64_t tgt[Core::MI];
+#pragma unroll
+  for (int bi = 0; bi < Core::MI; ++bi) {
+    const int64_t t = static_cast<int64_t>(i0) + iw + 32 * bi;
+    lse[bi] = dl[bi] = 0.0f;
+    tgt[bi] = -1;
+    if (t < a.n) {
+      tgt[bi] = target_of(a.targets, a.t64, t, a.vocab);
+      lse[bi] = a.lse[t];
+      dl[bi] = a.dloss[t];
+    }
+  }
+  T* G = static_cast<T*>(a.g) + i0 * a.ldg + j0;
+  each_quad<Core>(acc, [&](int i, int j, f32x4_t v) {
+    const int bi = (i - iw) >> 5;
+    if (i0 + i < a.n) {
+      f32x4_t o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float p = exp_of<T>(v[e] - lse[bi]);
+        // a row without a target has no loss, whatever dloss holds there
+        o[e] = tgt[bi] < 0 ? 0.0f : (tgt[bi] == a.v0 + j0 + j + e ? p - 1.0f : p) * dl[bi];
+      }
+      store_quad(G + i * a.ldg + j, a.len - j0 - j, o, false);
+    }
+  });
+}
+
+struct DhArgs {
+  const void* g;
+  const void* w;  // the piece's first row
+  float* part;    // fp32 sums, [splits][n][dim]
+  void* out;      // dhidden, or null: leave the sums in part
+  int64_t ldg, ld_out;
+  int n, dim, len, splits, first;
+};
+
+// dh (+)= g W of the piece; split s takes its share of the piece's rows.
+template <typename Core, typename T, typename TO>
+__global__ __launch_bounds__(kThreads) void k_loss_dh(DhArgs a) {
+  __shared__ __attribute__((aligned(16))) char smem[Core::kLdsBytes];
+  const int i0 = blockIdx.x * Core::BM, j0 = blockIdx.y * Core::BN, s = blockIdx.z;
+  // shares in whole steps of 64 rows
+  const int share = ((a.len + a.splits - 1) / a.splits + 63) / 64 * 64;
+  const int k0 = min(s * share, a.len), kn = min(share, a.len - k0);
+  f32x16_t acc[Core::NJ][Core::MI];
+  Core::run(static_cast<const T*>(a.g) + i0 * a.ldg + k0, a.ldg, a.n - i0,
+            static_cast<const T*>(a.w) + static_cast<int64_t>(k0) * a.dim + j0, a.dim,
+            a.dim - j0, kn, acc, smem);
+  float* D = a.part + (static_cast<int64_t>(s) * a.n + i0) * a.dim + j0;
+  TO* O = a.out ? static_cast<TO*>(a.out) + i0 * a.ld_out + j0 : nullptr;
+  each_quad<Core>(acc, [&](int i, int j, f32x4_t v) {
+    const int left = a.dim - j0 - j;
+    if (i0 + i >= a.n || left <= 0) return;
+    float* d = D + static_cast<int64_t>(i) * a.dim + j;
+    if (O == nullptr) {
+      store_quad(d, left, v, !a.first);
+      return;
+    }
+    if (!a.first) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < left) v[e] += d[e];
+    }
+    store_quad(O + i * a.ld_out + j, left, v, false);
+  });
+}
+
+// dhidden = sum of the splits, in order.
+template <typename TO>
+__global__ __launch_bounds__(kThreads) void k_loss_dh_join(const float* __restrict__ part,
+                                                           int splits, int n, int dim, TO* out,
+                                                           int64_t ld) {
+  const int64_t total = static_cast<int64_t>(n) * dim;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * kThreads) {
+    float v = part[i];
+    for (int s = 1; s < splits; ++s) v += part[s * total + i];
+    from_f32(v, out + i / dim * ld + i % dim);
+  }
+}
+
+struct DwArgs {
+  const void* g;
+  const void* h;
+  void* dw;  // the piece's first row
+  int64_t ldg, ldh;
+  int n, dim, len, accumulate;
+};
+
+template <typename Core, typename T, typename TO>
+__global__ __launch_bounds__(kThreads) void k_loss_dw(DwArgs a) {
+  __shared__ __attribute__((aligned(16))) char smem[Core::kLdsBytes];
+  const int i0 = blockIdx.x * Core::BM, j0 = blockIdx.y * Core::BN;
+  f32x16_t acc[Core::NJ][Core::MI];
+  Core::run(static_cast<const T*>(a.g) + i0, a.ldg, a.len - i0, static_cast<const T*>(a.h) + j0,
+            a.ldh, a.dim - j0, a.n, acc, smem);
+  TO* C = static_cast<TO*>(a.dw) + static_cast<int64_t>(i0) * a.dim + j0;
+  each_quad<Core>(acc, [&](int i, int j, f32x4_t v) {
+    if (i < a.len - i0)
+      store_quad(C + static_cast<int64_t>(i) * a.dim + j, a.dim - j0 - j, v, a.accumulate != 0);
+  });
+}
+
+template <typename T>
+__global__ void k_zero_rows(T* p, int64_t rows, int64_t cols, int64_t ld) {
+  const int64_t total = rows * cols;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x)
+    p[i / cols * ld + i % cols] = T{};
+}
+
+// -------------------------------------------------------------------- host
+
+constexpr int kTile = 128;
+// Forward: rows per pass, which bounds the tile statistics (vocab / 16 bytes
+// a row) without leaving the GPU short of tiles.
+constexpr int64_t kStatsRows = 32768;
+// Backward: bytes of g at a time.  Fewer pieces mean fewer passes over the
+// fp32 sums of dh; g should stay near what the last-level cache holds.
+constexpr int64_t kPieceBytes = static_cast<int64_t>(256) << 20;
+constexpr int64_t kMinPiece = 2048;
+constexpr int kMaxSplits = 16;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+struct LossWs {
+  int64_t stats_rows, v_tiles;          // forward
+  int64_t piece, ldg;                   // backward
+  int splits;
+  size_t tile_m, tile_s, at, g, part, total;
+};
+LossWs loss_ws(int64_t n, int64_t vocab, int64_t dim, int32_t dtype, bool backward) {
+  LossWs w{};
+  size_t o = 0;
+  // forward
+  w.stats_rows = std::min(n, kStatsRows);
+  w.v_tiles = ceil_div(vocab, kTile);
+  w.tile_m = o;
+  o += align256(static_cast<size_t>(w.stats_rows * w.v_tiles) * 4);
+  w.tile_s = o;
+  o += align256(static_cast<size_t>(w.stats_rows * w.v_tiles) * 4);
+  w.at = o;
+  o += align256(static_cast<size_t>(w.stats_rows) * 4);
+  w.total = o;
+  if (!backward) return w;
+  // backward (the forward's part of the workspace is free again)
+  o = 0;
+  const int64_t sz = static_cast<int64_t>(train_dtype_size(dtype));
+  w.piece = std::max(kMinPiece, kPieceBytes / (sz * n) / kTile * kTile);
+  if (w.piece >= vocab) {
+    w.piece = vocab;
+  } else {
+    // pieces of equal length, whole tiles
+    const int64_t pieces = ceil_div(vocab, w.piece);
+    w.piece = ceil_div(ceil_div(vocab, pieces), kTile) * kTile;
+  }
+  w.ldg = ceil_div(w.piece, 8) * 8;
+  w.g = o;
+  o += align256(static_cast<size_t>(n * w.ldg * sz));
+  // dh tiles against the GPU's 256 workgroups of one tile each
+  const int64_t tiles = ceil_div(n, kTile) * ceil_div(dim, kTile);
+  w.splits = static_cast<int>(
+      std::max<int64_t>(1, std::min<int64_t>({kMaxSplits, 512 / tiles, ceil_div(w.piece, 1024)})));
+  w.part = o;
+  if (w.splits > 1 || w.piece < vocab)
+    o += align256(static_cast<size_t>(w.splits) * static_cast<size_t>(n * dim) * 4);
+  w.total = std::max(w.total, o);
+  return w;
+}
+
+template <typename T>
+void run_stats(const StatsArgs& a, int64_t v_tiles, hipStream_t s) {
+  using NT = AnyCore<T, false, false>;
+  const dim3 grid(static_cast<unsigned>(ceil_div(a.n, NT::BM)), static_cast<unsigned>(v_tiles));
+  hipLaunchKernelGGL((k_loss_stats<NT, T>), grid, dim3(kThreads), 0, s, a);
+}
+
+template <typename T>
+void run_g(const GradArgs& a, hipStream_t s) {
+  using NT = AnyCore<T, false, false>;
+  const dim3 grid(static_cast<unsigned>(ceil_div(a.n, NT::BM)),
+                  static_cast<unsigned>(ceil_div(a.len, NT::BN)));
+  hipLaunchKernelGGL((k_loss_g<NT, T>), grid, dim3(kThreads), 0, s, a);
+}
+
+template <typename T, typename TO>
+void run_dh(const DhArgs& a, hipStream_t s) {
+  using NN = AnyCore<T, false, true>;
+  const dim3 grid(static_cast<unsigned>(ceil_div(a.n, NN::BM)),
+                  static_cast<unsigned>(ceil_div(a.dim, NN::BN)), a.splits);
+  hipLaunchKernelGGL((k_loss_dh<NN, T, TO>), grid, dim3(kThreads), 0, s, a);
+}
+
+template <typename T, typename TO>
+void run_dw(const DwArgs& a, hipStream_t s) {
+  using TN = AnyCore<T, true, true>;
+  const dim3 grid(static_cast<unsigned>(ceil_div(a.len, TN::BM)),
+                  static_cast<unsigned>(ceil_div(a.dim, TN::BN)));
+  hipLaunchKernelGGL((k_loss_dw<TN, T, TO>), grid, dim3(kThreads), 0, s, a);
+}
+
+struct BackwardArgs {
+  const void *h, *w, *targets;
+  const float *lse, *dloss;
+  void *dh, *dw;
+  int64_t n, vocab, dim, ldh, ld_dh;
+  int t64, accumulate;
+  char* ws;
+};
+
+template <typename T, typename TH, typename TW>
+void run_backward(const BackwardArgs& b, const LossWs& w, hipStream_t s) {
+  T* g = reinterpret_cast<T*>(b.ws + w.g);
+  float* part = reinterpret_cast<float*>(b.ws + w.part);
+  for (int64_t v0 = 0; v0 < b.vocab; v0 += w.piece) {
+    const int len = static_cast<int>(std::min(w.piece, b.vocab - v0));
+    const T* wp = static_cast<const T*>(b.w) + v0 * b.dim;
+    run_g<T>(GradArgs{b.h, wp, b.targets, b.lse, b.dloss, g, b.ldh, w.ldg, b.vocab, v0,
+                      static_cast<int>(b.n), static_cast<int>(b.dim), len, b.t64},
+             s);
+    if (b.dh != nullptr) {
+      const bool last = v0 + len == b.vocab;
+      run_dh<T, TH>(DhArgs{g, wp, part, last && w.splits == 1 ? b.dh : nullptr, w.ldg, b.ld_dh,
+                           static_cast<int>(b.n), static_cast<int>(b.dim), len, w.splits,
+                           v0 == 0 ? 1 : 0},
+                    s);
+    }
+    if (b.dw != nullptr)
+      run_dw<T, TW>(DwArgs{g, b.h, static_cast<TW*>(b.dw) + v0 * b.dim, w.ldg, b.ldh,
+                           static_cast<int>(b.n), static_cast<int>(b.dim), len, b.accumulate},
+                    s);
+  }
+  if (b.dh != nullptr && w.splits > 1)
+    hipLaunchKernelGGL(k_loss_dh_join<TH>,
+                       dim3(static_cast<unsigned>(std::min<int64_t>(4096, ceil_div(b.n * b.dim, kThreads)))),
+                       dim3(kThreads), 0, s, part, w.splits, static_cast<int>(b.n),
+                       static_cast<int>(b.dim), static_cast<TH*>(b.dh), b.ld_dh);
+}
+
+int check_loss(int64_t n, int64_t vocab, int64_t dim, int64_t ldh, int32_t dtype) {
+  const int rc = check_token_sizes(n, vocab, dim);
+  if (rc != MUON_OK) return rc;
+  // the vocabulary's tiles are a launch dimension
+  if (vocab > static_cast<int64_t>(65535) * kTile)
+    return set_error(MUON_ERR_UNSUPPORTED, "vocab must be at most 65535 * 128");
+  if (!train_dtype_ok(dtype))
+    return set_error(MUON_ERR_BAD_DTYPE, "hidden and weight must be fp32 or bf16");
+  if (ldh < dim) return set_error(MUON_ERR_BAD_SHAPE, "ld_hidden < dim");
+  return MUON_OK;
+}
+
+int check_ws(const void* ws, size_t bytes, size_t need, const char* who) {
+  if (ws == nullptr || bytes < need || reinterpret_cast<uintptr_t>(ws) % 256 != 0)
+    return set_error(MUON_ERR_WORKSPACE_TOO_SMALL, std::string(who) + " needs " +
+                                                       std::to_string(need) +
+                                                       " bytes of workspace, 256-byte aligned");
+  return MUON_OK;
+}
+
+}  // namespace
+}  // namespace muon
+
+using namespace muon;
+
+extern "C" {
+
+size_t lm_loss_workspace_size(int64_t n, int64_t vocab, int64_t dim, int32_t dtype,
+                              int32_t backward) {
+  if (n <= 0 || check_loss(n, vocab, dim, dim, dtype) != MUON_OK) return 0;
+  return loss_ws(n, vocab, dim, dtype, backward != 0).total;
+}
+
+int lm_loss_forward(const void* hidden, int64_t ld_hidden, const void* weight, int32_t dtype,
+                    const void* targets, int32_t targets_64, int64_t n, int64_t vocab,
+                    int64_t dim, float* loss, float* lse, void* workspace,
+                    size_t workspace_bytes, hipStream_t stream) {
+  int rc = check_loss(n, vocab, dim, ld_hidden, dtype);
+  if (rc != MUON_OK) return rc;
+  if (n == 0) return MUON_OK;
+  if (hidden == nullptr || weight == nullptr || targets == nullptr || loss == nullptr ||
+      lse == nullptr)
+    return set_error(MUON_ERR_INVALID_ARG, "hidden, weight, targets, loss or lse is null");
+  const LossWs w = loss_ws(n, vocab, dim, dtype, false);
+  if ((rc = check_ws(workspace, workspace_bytes, w.total, "lm_loss_forward")) != MUON_OK) return rc;
+  char* ws = static_cast<char*>(workspace);
+  float* tm = reinterpret_cast<float*>(ws + w.tile_m);
+  float* ts = reinterpret_cast<float*>(ws + w.tile_s);
+  float* at = reinterpret_cast<float*>(ws + w.at);
+  const size_t sz = train_dtype_size(dtype), tsz = targets_64 ? 8 : 4;
+  for (int64_t r0 = 0; r0 < n; r0 += w.stats_rows) {
+    const int rows = static_cast<int>(std::min(w.stats_rows, n - r0));
+    const void* tg = static_cast<const char*>(targets) + static_cast<size_t>(r0) * tsz;
+    const StatsArgs a{static_cast<const char*>(hidden) + static_cast<size_t>(r0 * ld_hidden) * sz,
+                      weight, tg, tm, ts, at, ld_hidden, vocab, rows, static_cast<int>(dim),
+                      targets_64 != 0};
+    if (dtype == MUON_DTYPE_BF16) run_stats<uint16_t>(a, w.v_tiles, stream);
+    else run_stats<float>(a, w.v_tiles, stream);
+    hipLaunchKernelGGL(k_loss_join, dim3(static_cast<unsigned>(ceil_div(rows, 64))),
+                       dim3(kThreads), 0, stream, tm, ts, at, static_cast<int>(w.v_tiles), rows,
+                       tg, targets_64 != 0, vocab, loss + r0, lse + r0);
+  }
+  return check_launch("vocabulary loss launch");
+}
+
+int lm_loss_backward(const void* hidden, int64_t ld_hidden, const void* weight, int32_t dtype,
+                     const void* targets, int32_t targets_64, int64_t n, int64_t vocab,
+                     int64_t dim, const float* lse, const float* dloss, void* dhidden,
+                     int32_t dhidden_dtype, int64_t ld_dhidden, void* dweight,
+                     int32_t dweight_dtype, int32_t accumulate, void* workspace,
+                     size_t workspace_bytes, hipStream_t stream) {
+  int rc = check_loss(n, vocab, dim, ld_hidden, dtype);
+  if (rc != MUON_OK) return rc;
+  if (dhidden != nullptr) {
+    if (!train_dtype_ok(dhidden_dtype))
+      return set_error(MUON_ERR_BAD_DTYPE, "dhidden must be fp32 or bf16");
+    if (ld_dhidden < dim) return set_error(MUON_ERR_BAD_SHAPE, "ld_dhidden < dim");
+  }
+  if (dweight != nullptr && !train_dtype_ok(dweight_dtype))
+    return set_error(MUON_ERR_BAD_DTYPE, "dweight must be fp32 or bf16");
+  if (n == 0) {
+    // no rows: dweight is a sum of nothing
+    if (dweight != nullptr && !accumulate) {
+      if (dweight_dtype == MUON_DTYPE_BF16)
+        hipLaunchKernelGGL(k_zero_rows<uint16_t>, dim3(4096), dim3(kThreads), 0, stream,
+                           static_cast<uint16_t*>(dweight), vocab, dim, dim);
+      else
+        hipLaunchKernelGGL(k_zero_rows<float>, dim3(4096), dim3(kThreads), 0, stream,
+                           static_cast<float*>(dweight), vocab, dim, dim);
+      return check_launch("vocabulary loss gradient launch");
+    }
+    return MUON_OK;
+  }
+  if (dhidden == nullptr && dweight == nullptr) return MUON_OK;
+  if (hidden == nullptr || weight == nullptr || targets == nullptr || lse == nullptr ||
+      dloss == nullptr)
+    return set_error(MUON_ERR_INVALID_ARG, "hidden, weight, targets, lse or dloss is null");
+  const LossWs w = loss_ws(n, vocab, dim, dtype, true);
+  if ((rc = check_ws(workspace, workspace_bytes, w.total, "lm_loss_backward")) != MUON_OK) return rc;
+  const BackwardArgs b{hidden, weight, targets, lse, dloss, dhidden, dweight, n, vocab, dim,
+                       ld_hidden, ld_dhidden, targets_64 != 0, accumulate != 0,
+                       static_cast<char*>(workspace)};
+  const bool hb = dhidden_dtype == MUON_DTYPE_BF16, wb = dweight_dtype == MUON_DTYPE_BF16;
+#define MUON_LOSS_BWD(T)                                           \
+  do {                                                             \
+    if (hb && wb) run_backward<T, uint16_t, uint16_t>(b, w, stream); \
+    else if (hb) run_backward<T, uint16_t, float>(b, w, stream);   \
+    else if (wb) run_backward<T, float, uint16_t>(b, w, stream);   \
+    else run_backward<T, float, float>(b, w, stream);              \
+  } while (0)
+  if (dtype == MUON_DTYPE_BF16) MUON_LOSS_BWD(uint16_t);
+  else MUON_LOSS_BWD(float);
+#undef MUON_LOSS_BWD
+  return check_launch("vocabulary loss gradient launch");
+}
+
+}  // extern "C"

@@ -116,3 +116,121 @@ def test_embed_entry_points_refuse():
     assert bwd(ws=None) == WS and bwd(nb=need - 1) == WS and bwd(ws=ctypes.c_void_p(128)) == WS
     assert bwd(n=0, acc=1, dout=None, ids=None, ws=None, nb=0) == M.MUON_OK
     assert "n" in M.muon_last_error() or M.muon_last_error()
+
+
+def test_loss_binding_checks():
+    h, w, t = Fake((6, 16)), Fake((100, 16)), Fake((6,), I64)
+    f32 = torch.float32
+    f = M.lm_loss_forward
+    _err(INVALID, f, Fake((6, 16), cuda=False), w, t)
+    _err(INVALID, f, h, Fake((100, 16), stride=(1, 100)), t)
+    _err(SHAPE, f, h, Fake((1600,)), t)
+    _err(SHAPE, f, Fake((6, 17)), w, t)
+    _err(SHAPE, f, Fake((5, 16)), w, t)
+    _err(DTYPE, f, Fake((6, 16), f32), w, t)
+    _err(DTYPE, f, Fake((6, 16), torch.float16), Fake((100, 16), torch.float16), t)
+    _err(DTYPE, f, h, w, Fake((6,), f32))
+    _err(INVALID, f, h, w, Fake((6,), I64, stride=(2,)))
+    _err(INVALID, f, Fake((6, 16), stride=(8, 1)), w, t)
+    _err(SHAPE, f, h, w, t, loss=Fake((5,), f32))
+    _err(DTYPE, f, h, w, t, lse=Fake((6,)))
+    _err(INVALID, f, h, Fake((100, 16), dev="cuda:1"), t)
+    b, lse, dl = M.lm_loss_backward, Fake((6,), f32), Fake((6,), f32)
+    _err(DTYPE, b, h, w, t, Fake((6,)), dl)
+    _err(SHAPE, b, h, w, t, lse, Fake((7,), f32))
+    _err(INVALID, b, h, w, t, lse, None)
+    _err(SHAPE, b, h, w, t, lse, dl, dhidden=Fake((6, 15)))
+    _err(SHAPE, b, h, w, t, lse, dl, dweight=Fake((16, 100)))
+    _err(INVALID, b, h, w, t, lse, dl, dweight=Fake((100, 16), stride=(32, 1)))
+    _err(DTYPE, b, h, w, t, lse, dl, dweight=Fake((100, 16), torch.float16))
+    _err(INVALID, b, h, w, t, lse, dl, accumulate=True)
+    _err(INVALID, b, h, w, t, lse, dl, dweight=False, accumulate=True)
+
+
+def test_loss_entry_points_refuse():
+    p = ctypes.c_void_p(256)
+    size = M.lm_loss_workspace_size
+    need_f, need_b = size(4, 10, 8, "bf16", False), size(4, 10, 8, "bf16")
+    assert 0 < need_f <= need_b
+    assert size(0, 10, 8, "bf16") == 0 and size(4, 0, 8, "bf16") == 0
+    assert size(4, 65535 * 128 + 1, 8, "bf16") == 0
+    # the gradient of the logits of one piece, not of all, is held
+    assert size(8192, 163840, 7168, "bf16") < 8192 * 163840 * 2 // 2
+
+    def fwd(h=p, ld=8, w=p, dt=1, t=p, t64=1, n=4, vocab=10, dim=8, loss=p, lse=p, ws=p,
+            nb=need_f):
+        return _rc("lm_loss_forward", h, ld, w, dt, t, t64, n, vocab, dim, loss, lse, ws, nb, None)
+
+    assert fwd(dt=2) == DTYPE and fwd(n=-1) == SHAPE and fwd(vocab=0) == SHAPE
+    assert fwd(dim=0, ld=0) == SHAPE and fwd(ld=7) == SHAPE
+    assert fwd(vocab=65535 * 128 + 1) == M.MUON_ERR_UNSUPPORTED
+    for k in ("h", "w", "t", "loss", "lse"):
+        assert fwd(**{k: None}) == INVALID
+    assert fwd(ws=None) == WS and fwd(nb=need_f - 1) == WS and fwd(ws=ctypes.c_void_p(8)) == WS
+    assert fwd(n=0, h=None, ws=None, nb=0) == M.MUON_OK
+
+    def bwd(h=p, ld=8, w=p, dt=1, t=p, t64=1, n=4, vocab=10, dim=8, lse=p, dl=p, dh=p, dhd=1,
+            ldh=8, dw=p, dwd=0, acc=0, ws=p, nb=need_b):
+        return _rc("lm_loss_backward", h, ld, w, dt, t, t64, n, vocab, dim, lse, dl, dh, dhd, ldh,
+                   dw, dwd, acc, ws, nb, None)
+
+    assert bwd(dt=2) == DTYPE and bwd(dhd=2) == DTYPE and bwd(dwd=-1) == DTYPE
+    assert bwd(ldh=7) == SHAPE and bwd(ld=7) == SHAPE and bwd(n=1 << 26) == SHAPE
+    for k in ("h", "w", "t", "lse", "dl"):
+        assert bwd(**{k: None}) == INVALID
+    assert bwd(ws=None) == WS and bwd(nb=need_b - 1) == WS and bwd(ws=ctypes.c_void_p(8)) == WS
+    assert bwd(dh=None, dw=None, ws=None, nb=0) == M.MUON_OK
+    assert bwd(n=0, dw=None) == M.MUON_OK and bwd(n=0, acc=1) == M.MUON_OK
+
+
+def test_expert_binding_checks():
+    x, w, o = Fake((40, 16)), Fake((5, 16, 24)), Fake((6,), torch.int32)
+    f = M.expert_matmul
+    _err(SHAPE, f, x, Fake((80, 24)), o)
+    _err(INVALID, f, x, Fake((5, 16, 24), stride=(400, 24, 1)), o)
+    _err(SHAPE, f, Fake((40, 24)), w, o)
+    _err(SHAPE, f, x, w, o, trans=True)
+    _err(SHAPE, f, Fake((640,)), w, o)
+    _err(SHAPE, f, None, w, o)
+    _err(DTYPE, f, Fake((40, 16), torch.float32), w, o)
+    _err(DTYPE, f, x, w, Fake((6,), I64))
+    _err(SHAPE, f, x, w, Fake((5,), torch.int32))
+    _err(INVALID, f, x, w, torch.zeros(6, dtype=torch.int32))
+    _err(SHAPE, f, x, w, o, out=Fake((40, 16)))
+    _err(INVALID, f, x, w, o, out=Fake((40, 24), stride=(1, 40)))
+    _err(DTYPE, f, x, w, o, out=Fake((40, 24)), out_dtype="fp32")
+    _err(INVALID, f, Fake((40, 16), dev="cuda:1"), w, o)
+    g, dw = M.expert_wgrad, Fake((5, 16, 24), torch.float32)
+    b = Fake((40, 24))
+    _err(SHAPE, g, x, Fake((39, 24)), o, dw)
+    _err(SHAPE, g, b, x, o, dw)
+    _err(DTYPE, g, x, Fake((40, 24), torch.float32), o, dw)
+    _err(DTYPE, g, x, b, o, Fake((5, 16, 24), torch.float16))
+    _err(SHAPE, g, x, b, o, Fake((80, 24)))
+    _err(SHAPE, g, x, b, Fake((5,), torch.int32), dw)
+    _err(INVALID, g, x, b, o, None)
+    _err(SHAPE, g, None, b, o, dw)
+
+
+def test_expert_entry_points_refuse():
+    p = ctypes.c_void_p(256)
+
+    def mm(x=p, ldx=16, w=p, dt=1, off=p, e=5, rows=40, k=16, n=24, tr=0, y=p, yd=1, ldy=24):
+        return _rc("expert_matmul", x, ldx, w, dt, off, e, rows, k, n, tr, y, yd, ldy, None)
+
+    assert mm(dt=2) == DTYPE and mm(yd=5) == DTYPE
+    assert mm(e=0) == SHAPE and mm(e=4097) == SHAPE and mm(rows=-1) == SHAPE
+    assert mm(rows=1 << 26) == SHAPE and mm(k=0) == SHAPE and mm(n=0) == SHAPE
+    assert mm(k=(1 << 22) + 1, ldx=1 << 23) == SHAPE and mm(ldx=15) == SHAPE and mm(ldy=23) == SHAPE
+    for k in ("x", "w", "off", "y"):
+        assert mm(**{k: None}) == INVALID
+    assert mm(rows=0, x=None, y=None) == M.MUON_OK
+
+    def wg(a=p, lda=16, b=p, ldb=24, dt=1, off=p, e=5, rows=40, m=16, n=24, dw=p, dwd=0, acc=0):
+        return _rc("expert_wgrad", a, lda, b, ldb, dt, off, e, rows, m, n, dw, dwd, acc, None)
+
+    assert wg(dt=2) == DTYPE and wg(dwd=2) == DTYPE and wg(lda=15) == SHAPE and wg(ldb=23) == SHAPE
+    assert wg(e=0) == SHAPE and wg(rows=1 << 26) == SHAPE and wg(m=0) == SHAPE
+    for k in ("a", "b", "off", "dw"):
+        assert wg(**{k: None}) == INVALID
+    assert wg(rows=0, a=None, b=None, acc=1) == M.MUON_OK
