@@ -83,14 +83,6 @@ __global__ __launch_bounds__(kThreads) void k_embed_fwd(const TT* __restrict__ t
 constexpr int kMaxBits = 9;
 constexpr int kMaxBins = 1 << kMaxBits;
 
-// Orders a wave's LDS accesses before and after it (the lanes of a wave run
-// in step and its LDS accesses complete in order).
-__device__ __forceinline__ void wave_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 // lanes of the wave (among `active`) whose digit equals this lane's
 __device__ __forceinline__ uint64_t match_digit(uint32_t d, int bits, uint64_t active) {
   uint64_t m = active;

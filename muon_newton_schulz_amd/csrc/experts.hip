@@ -63,22 +63,21 @@ struct MatmulArgs {
 
 // QKS: W_e is [K][N] (y = x W_e); else [N][K] (y = x W_e^T).
 template <typename Core, typename T, bool QKS, typename TO>
-__global__ __launch_bounds__(kThreads) void k_expert_matmul(MatmulArgs a) {
-  __shared__ __attribute__((aligned(16))) char smem[Core::kLdsBytes];
-  const RowTile rt = find_row_tile(a.off, a.experts, a.rows, Core::BM, blockIdx.x);
+__global__ __launch_bounds__(kThreads, Core::kWaves) void k_expert_matmul(MatmulArgs a, int nx,
+                                                                        int ny) {
+  int x, y;
+  if (!tile_of(blockIdx.x, nx, ny, x, y)) return;
+  const RowTile rt = find_row_tile(a.off, a.experts, a.rows, Core::BM, x);
   if (rt.e < 0) return;
-  const int i0 = rt.tile * Core::BM, j0 = blockIdx.y * Core::BN;
+  const int i0 = rt.tile * Core::BM, j0 = y * Core::BN;
   const int64_t row0 = static_cast<int64_t>(rt.lo) + i0;
   const T* P = static_cast<const T*>(a.x) + row0 * a.ldx;
   const T* W = static_cast<const T*>(a.w) + static_cast<int64_t>(rt.e) * a.K * a.N;
   f32x16_t acc[Core::NJ][Core::MI];
-  if (QKS) Core::run(P, a.ldx, rt.n - i0, W + j0, a.N, a.N - j0, a.K, acc, smem);
-  else Core::run(P, a.ldx, rt.n - i0, W + static_cast<int64_t>(j0) * a.K, a.K, a.N - j0, a.K, acc,
-                 smem);
+  if (QKS) Core::run(P, a.ldx, rt.n - i0, W + j0, a.N, a.N - j0, a.K, acc);
+  else Core::run(P, a.ldx, rt.n - i0, W + static_cast<int64_t>(j0) * a.K, a.K, a.N - j0, a.K, acc);
   TO* Y = static_cast<TO*>(a.y) + row0 * a.ldy + j0;
-  each_quad<Core>(acc, [&](int i, int j, f32x4_t v) {
-    if (i < rt.n - i0) store_quad(Y + i * a.ldy + j, a.N - j0 - j, v, false);
-  });
+  Core::write(acc, Y, a.ldy, static_cast<const TO*>(nullptr), 0, rt.n - i0, a.N - j0);
 }
 
 struct WgradArgs {
@@ -91,46 +90,65 @@ struct WgradArgs {
 };
 
 template <typename Core, typename T, typename TO>
-__global__ __launch_bounds__(kThreads) void k_expert_wgrad(WgradArgs g) {
-  __shared__ __attribute__((aligned(16))) char smem[Core::kLdsBytes];
-  const int e = blockIdx.z, i0 = blockIdx.x * Core::BM, j0 = blockIdx.y * Core::BN;
+__global__ __launch_bounds__(kThreads, Core::kWaves) void k_expert_wgrad(WgradArgs g, int nx,
+                                                                       int ny) {
+  int x, y;
+  if (!tile_of(blockIdx.x, static_cast<int64_t>(nx) * g.experts, ny, x, y)) return;
+  const int e = x / nx, i0 = x % nx * Core::BM, j0 = y * Core::BN;
   int lo, n;
   group_rows(g.off, e, g.rows, lo, n);
   if (n == 0 && g.accumulate) return;
   f32x16_t acc[Core::NJ][Core::MI];
   Core::run(static_cast<const T*>(g.a) + lo * g.lda + i0, g.lda, g.M - i0,
-            static_cast<const T*>(g.b) + lo * g.ldb + j0, g.ldb, g.N - j0, n, acc, smem);
+            static_cast<const T*>(g.b) + lo * g.ldb + j0, g.ldb, g.N - j0, n, acc);
   TO* C = static_cast<TO*>(g.dw) + static_cast<int64_t>(e) * g.M * g.N +
           static_cast<int64_t>(i0) * g.N + j0;
-  each_quad<Core>(acc, [&](int i, int j, f32x4_t v) {
-    if (i < g.M - i0)
-      store_quad(C + static_cast<int64_t>(i) * g.N + j, g.N - j0 - j, v, g.accumulate != 0);
-  });
+  Core::write(acc, C, g.N, g.accumulate ? C : static_cast<const TO*>(nullptr), g.N, g.M - i0,
+              g.N - j0);
 }
 
 // -------------------------------------------------------------------- host
 
 constexpr int kMaxExperts = 4096;
 
+template <typename Core, typename T, bool QKS, typename TO>
+void launch_matmul(const MatmulArgs& a, hipStream_t s) {
+  const int nx = a.rows / Core::BM + std::min(a.experts, a.rows);
+  const int ny = (a.N + Core::BN - 1) / Core::BN;
+  hipLaunchKernelGGL((k_expert_matmul<Core, T, QKS, TO>),
+                     dim3(static_cast<unsigned>(grid_blocks(nx, ny))), dim3(kThreads), 0, s, a, nx,
+                     ny);
+}
+template <typename Core, typename T, typename TO>
+void launch_wgrad(const WgradArgs& g, hipStream_t s) {
+  const int nx = (g.M + Core::BM - 1) / Core::BM, ny = (g.N + Core::BN - 1) / Core::BN;
+  hipLaunchKernelGGL((k_expert_wgrad<Core, T, TO>),
+                     dim3(static_cast<unsigned>(grid_blocks(static_cast<int64_t>(nx) * g.experts, ny))),
+                     dim3(kThreads), 0, s, g, nx, ny);
+}
+
 template <typename T, typename TO>
 void run_matmul(const MatmulArgs& a, bool trans, hipStream_t s) {
-  using NT = AnyCore<T, false, false>;
-  using NN = AnyCore<T, false, true>;
-  const dim3 grid(static_cast<unsigned>(a.rows / NT::BM + std::min(a.experts, a.rows)),
-                  static_cast<unsigned>((a.N + NT::BN - 1) / NT::BN));
-  if (trans)
-    hipLaunchKernelGGL((k_expert_matmul<NT, T, false, TO>), grid, dim3(kThreads), 0, s, a);
-  else
-    hipLaunchKernelGGL((k_expert_matmul<NN, T, true, TO>), grid, dim3(kThreads), 0, s, a);
+  if constexpr (sizeof(T) == 2) {
+    if (on_grid(a.x, a.ldx, a.K) && on_grid(a.w, a.N, a.K) && on_grid(a.y, a.ldy, a.N)) {
+      if (trans) launch_matmul<DmaCore<false, false, 256, 256, 2, 32, 4>, T, false, TO>(a, s);
+      else launch_matmul<DmaCore<false, true, 256, 256, 2, 32, 4>, T, true, TO>(a, s);
+      return;
+    }
+  }
+  if (trans) launch_matmul<AnyCore<T, false, false>, T, false, TO>(a, s);
+  else launch_matmul<AnyCore<T, false, true>, T, true, TO>(a, s);
 }
 
 template <typename T, typename TO>
 void run_wgrad(const WgradArgs& g, hipStream_t s) {
-  using TN = AnyCore<T, true, true>;
-  const dim3 grid(static_cast<unsigned>((g.M + TN::BM - 1) / TN::BM),
-                  static_cast<unsigned>((g.N + TN::BN - 1) / TN::BN),
-                  static_cast<unsigned>(g.experts));
-  hipLaunchKernelGGL((k_expert_wgrad<TN, T, TO>), grid, dim3(kThreads), 0, s, g);
+  if constexpr (sizeof(T) == 2) {
+    if (on_grid(g.a, g.lda, g.M) && on_grid(g.b, g.ldb, g.N) && on_grid(g.dw, g.N, g.M)) {
+      launch_wgrad<DmaCore<true, true, 256, 256, 2, 32, 4>, T, TO>(g, s);
+      return;
+    }
+  }
+  launch_wgrad<AnyCore<T, true, true>, T, TO>(g, s);
 }
 
 int check_group(int64_t rows, int32_t experts, int64_t k, int64_t n) {

@@ -68,18 +68,19 @@ struct StatsArgs {
 // values of a row, joined with the lane that holds the row's other columns
 // (lane ^ 32), then with the waves beside it.
 template <typename Core, typename T>
-__global__ __launch_bounds__(kThreads) void k_loss_stats(StatsArgs a) {
-  __shared__ __attribute__((aligned(16))) char smem[Core::kLdsBytes];
-  const int i0 = blockIdx.x * Core::BM;
-  const int64_t v0 = static_cast<int64_t>(blockIdx.y) * Core::BN;
+__global__ __launch_bounds__(kThreads, Core::kWaves) void k_loss_stats(StatsArgs a, int nx, int ny) {
+  int x, y;
+  if (!tile_of(blockIdx.x, nx, ny, x, y)) return;
+  const int i0 = x * Core::BM;
+  const int64_t v0 = static_cast<int64_t>(y) * Core::BN;
   const int jn = static_cast<int>(a.vocab - v0 < Core::BN ? a.vocab - v0 : Core::BN);
   f32x16_t acc[Core::NJ][Core::MI];
   Core::run(static_cast<const T*>(a.h) + i0 * a.ldh, a.ldh, a.n - i0,
-            static_cast<const T*>(a.w) + v0 * a.dim, a.dim, jn, a.dim, acc, smem);
+            static_cast<const T*>(a.w) + v0 * a.dim, a.dim, jn, a.dim, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wi = wave % Core::WM, wj = wave / Core::WM;
   const int jw = wj * 32 * Core::NJ + 4 * (lane >> 5);
-  float* red = reinterpret_cast<float*>(smem);  // [WN][BM][2]
+  float* red = reinterpret_cast<float*>(Core::lds());  // [WN][BM][2]
   static_assert(Core::WN * Core::BM * 8 <= Core::kLdsBytes, "the waves' row statistics");
   __syncthreads();
 #pragma unroll
@@ -119,7 +120,7 @@ __global__ __launch_bounds__(kThreads) void k_loss_stats(StatsArgs a) {
 #pragma unroll
     for (int w = 1; w < Core::WN; ++w)
       join_stats(m, s, red[(w * Core::BM + i) * 2], red[(w * Core::BM + i) * 2 + 1]);
-    const int64_t o = static_cast<int64_t>(blockIdx.y) * a.n + i0 + i;
+    const int64_t o = static_cast<int64_t>(y) * a.n + i0 + i;
     a.tile_m[o] = m;
     a.tile_s[o] = s;
   }
@@ -165,13 +166,14 @@ struct GradArgs {
 
 // g of the piece, in the operands' type.
 template <typename Core, typename T>
-__global__ __launch_bounds__(kThreads) void k_loss_g(GradArgs a) {
-  __shared__ __attribute__((aligned(16))) char smem[Core::kLdsBytes];
-  const int i0 = blockIdx.x * Core::BM, j0 = blockIdx.y * Core::BN;
+__global__ __launch_bounds__(kThreads, Core::kWaves) void k_loss_g(GradArgs a, int nx, int ny) {
+  int x, y;
+  if (!tile_of(blockIdx.x, nx, ny, x, y)) return;
+  const int i0 = x * Core::BM, j0 = y * Core::BN;
   f32x16_t acc[Core::NJ][Core::MI];
   Core::run(static_cast<const T*>(a.h) + i0 * a.ldh, a.ldh, a.n - i0,
             static_cast<const T*>(a.w) + static_cast<int64_t>(j0) * a.dim, a.dim, a.len - j0,
-            a.dim, acc, smem);
+            a.dim, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int iw = (wave % Core::WM) * 32 * Core::MI + (lane & 31);
   float lse[Core::MI], dl[Core::MI];
@@ -187,20 +189,25 @@ __global__ __launch_bounds__(kThreads) void k_loss_g(GradArgs a) {
       dl[bi] = a.dloss[t];
     }
   }
-  T* G = static_cast<T*>(a.g) + i0 * a.ldg + j0;
-  each_quad<Core>(acc, [&](int i, int j, f32x4_t v) {
-    const int bi = (i - iw) >> 5;
-    if (i0 + i < a.n) {
-      f32x4_t o;
+  // A row without a target has no loss, whatever dloss holds there.  On the
+  // grid the columns from the piece's end to ldg are stored as zeros, which
+  // the sums over the vocabulary read.
+  const int jw = (wave / Core::WM) * 32 * Core::NJ + 4 * (lane >> 5);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float p = exp_of<T>(v[e] - lse[bi]);
-        // a row without a target has no loss, whatever dloss holds there
-        o[e] = tgt[bi] < 0 ? 0.0f : (tgt[bi] == a.v0 + j0 + j + e ? p - 1.0f : p) * dl[bi];
+  for (int bi = 0; bi < Core::MI; ++bi) {
+    const int64_t at = tgt[bi] - a.v0 - j0 - jw;  // the target's column from this lane's first
+    const int left = tgt[bi] < 0 ? 0 : a.len - j0 - jw;
+#pragma unroll
+    for (int bj = 0; bj < Core::NJ; ++bj)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const float p = exp_of<T>(acc[bj][bi][v] - lse[bi]);
+        const int j = 32 * bj + 8 * (v >> 2) + (v & 3);
+        acc[bj][bi][v] = j < left ? (at == j ? p - 1.0f : p) * dl[bi] : 0.0f;
       }
-      store_quad(G + i * a.ldg + j, a.len - j0 - j, o, false);
-    }
-  });
+  }
+  Core::write(acc, static_cast<T*>(a.g) + i0 * a.ldg + j0, a.ldg, static_cast<const T*>(nullptr),
+              0, a.n - i0, Core::kGrid ? static_cast<int>(a.ldg) - j0 : a.len - j0);
 }
 
 struct DhArgs {
@@ -214,33 +221,24 @@ struct DhArgs {
 
 // dh (+)= g W of the piece; split s takes its share of the piece's rows.
 template <typename Core, typename T, typename TO>
-__global__ __launch_bounds__(kThreads) void k_loss_dh(DhArgs a) {
-  __shared__ __attribute__((aligned(16))) char smem[Core::kLdsBytes];
-  const int i0 = blockIdx.x * Core::BM, j0 = blockIdx.y * Core::BN, s = blockIdx.z;
+__global__ __launch_bounds__(kThreads, Core::kWaves) void k_loss_dh(DhArgs a, int nx, int ny) {
+  int x, y;
+  if (!tile_of(blockIdx.x, nx, static_cast<int64_t>(ny) * a.splits, x, y)) return;
+  const int s = y / ny, i0 = x * Core::BM, j0 = y % ny * Core::BN;
   // shares in whole steps of 64 rows
   const int share = ((a.len + a.splits - 1) / a.splits + 63) / 64 * 64;
   const int k0 = min(s * share, a.len), kn = min(share, a.len - k0);
   f32x16_t acc[Core::NJ][Core::MI];
   Core::run(static_cast<const T*>(a.g) + i0 * a.ldg + k0, a.ldg, a.n - i0,
             static_cast<const T*>(a.w) + static_cast<int64_t>(k0) * a.dim + j0, a.dim,
-            a.dim - j0, kn, acc, smem);
+            a.dim - j0, kn, acc);
   float* D = a.part + (static_cast<int64_t>(s) * a.n + i0) * a.dim + j0;
-  TO* O = a.out ? static_cast<TO*>(a.out) + i0 * a.ld_out + j0 : nullptr;
-  each_quad<Core>(acc, [&](int i, int j, f32x4_t v) {
-    const int left = a.dim - j0 - j;
-    if (i0 + i >= a.n || left <= 0) return;
-    float* d = D + static_cast<int64_t>(i) * a.dim + j;
-    if (O == nullptr) {
-      store_quad(d, left, v, !a.first);
-      return;
-    }
-    if (!a.first) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (e < left) v[e] += d[e];
-    }
-    store_quad(O + i * a.ld_out + j, left, v, false);
-  });
+  const float* old = a.first ? nullptr : D;
+  const int rows = a.n - i0, cols = a.dim - j0;
+  if (a.out == nullptr)
+    Core::write(acc, D, a.dim, old, a.dim, rows, cols);
+  else
+    Core::write(acc, static_cast<TO*>(a.out) + i0 * a.ld_out + j0, a.ld_out, old, a.dim, rows, cols);
 }
 
 // dhidden = sum of the splits, in order.
@@ -266,17 +264,16 @@ struct DwArgs {
 };
 
 template <typename Core, typename T, typename TO>
-__global__ __launch_bounds__(kThreads) void k_loss_dw(DwArgs a) {
-  __shared__ __attribute__((aligned(16))) char smem[Core::kLdsBytes];
-  const int i0 = blockIdx.x * Core::BM, j0 = blockIdx.y * Core::BN;
+__global__ __launch_bounds__(kThreads, Core::kWaves) void k_loss_dw(DwArgs a, int nx, int ny) {
+  int x, y;
+  if (!tile_of(blockIdx.x, nx, ny, x, y)) return;
+  const int i0 = x * Core::BM, j0 = y * Core::BN;
   f32x16_t acc[Core::NJ][Core::MI];
   Core::run(static_cast<const T*>(a.g) + i0, a.ldg, a.len - i0, static_cast<const T*>(a.h) + j0,
-            a.ldh, a.dim - j0, a.n, acc, smem);
+            a.ldh, a.dim - j0, a.n, acc);
   TO* C = static_cast<TO*>(a.dw) + static_cast<int64_t>(i0) * a.dim + j0;
-  each_quad<Core>(acc, [&](int i, int j, f32x4_t v) {
-    if (i < a.len - i0)
-      store_quad(C + static_cast<int64_t>(i) * a.dim + j, a.dim - j0 - j, v, a.accumulate != 0);
-  });
+  Core::write(acc, C, a.dim, a.accumulate ? C : static_cast<const TO*>(nullptr), a.dim, a.len - i0,
+              a.dim - j0);
 }
 
 template <typename T>
@@ -346,35 +343,69 @@ LossWs loss_ws(int64_t n, int64_t vocab, int64_t dim, int32_t dtype, bool backwa
   return w;
 }
 
+// bf16 operands on the 16-byte grid take the DMA core (grid), others the
+// core for any operands.
+template <typename Core, typename T>
+int launch_stats(const StatsArgs& a, hipStream_t s) {
+  const int nx = static_cast<int>(ceil_div(a.n, Core::BM));
+  const int ny = static_cast<int>(ceil_div(a.vocab, Core::BN));
+  hipLaunchKernelGGL((k_loss_stats<Core, T>), dim3(static_cast<unsigned>(grid_blocks(nx, ny))),
+                     dim3(kThreads), 0, s, a, nx, ny);
+  return ny;
+}
+// returns the number of tiles along the vocabulary
 template <typename T>
-void run_stats(const StatsArgs& a, int64_t v_tiles, hipStream_t s) {
-  using NT = AnyCore<T, false, false>;
-  const dim3 grid(static_cast<unsigned>(ceil_div(a.n, NT::BM)), static_cast<unsigned>(v_tiles));
-  hipLaunchKernelGGL((k_loss_stats<NT, T>), grid, dim3(kThreads), 0, s, a);
+int run_stats(const StatsArgs& a, bool grid, hipStream_t s) {
+  if constexpr (sizeof(T) == 2) {
+    if (grid) return launch_stats<DmaCore<false, false, 256, 256, 2, 32, 4>, T>(a, s);
+  }
+  return launch_stats<AnyCore<T, false, false>, T>(a, s);
 }
 
+template <typename Core, typename T>
+void launch_g(const GradArgs& a, hipStream_t s) {
+  const int nx = static_cast<int>(ceil_div(a.n, Core::BM));
+  const int ny = static_cast<int>(ceil_div(a.len, Core::BN));
+  hipLaunchKernelGGL((k_loss_g<Core, T>), dim3(static_cast<unsigned>(grid_blocks(nx, ny))),
+                     dim3(kThreads), 0, s, a, nx, ny);
+}
 template <typename T>
-void run_g(const GradArgs& a, hipStream_t s) {
-  using NT = AnyCore<T, false, false>;
-  const dim3 grid(static_cast<unsigned>(ceil_div(a.n, NT::BM)),
-                  static_cast<unsigned>(ceil_div(a.len, NT::BN)));
-  hipLaunchKernelGGL((k_loss_g<NT, T>), grid, dim3(kThreads), 0, s, a);
+void run_g(const GradArgs& a, bool grid, hipStream_t s) {
+  if constexpr (sizeof(T) == 2) {
+    if (grid) return launch_g<DmaCore<false, false, 256, 256, 2, 32, 4>, T>(a, s);
+  }
+  launch_g<AnyCore<T, false, false>, T>(a, s);
 }
 
+template <typename Core, typename T, typename TO>
+void launch_dh(const DhArgs& a, hipStream_t s) {
+  const int nx = static_cast<int>(ceil_div(a.n, Core::BM));
+  const int ny = static_cast<int>(ceil_div(a.dim, Core::BN));
+  hipLaunchKernelGGL((k_loss_dh<Core, T, TO>),
+                     dim3(static_cast<unsigned>(grid_blocks(nx, static_cast<int64_t>(ny) * a.splits))),
+                     dim3(kThreads), 0, s, a, nx, ny);
+}
 template <typename T, typename TO>
-void run_dh(const DhArgs& a, hipStream_t s) {
-  using NN = AnyCore<T, false, true>;
-  const dim3 grid(static_cast<unsigned>(ceil_div(a.n, NN::BM)),
-                  static_cast<unsigned>(ceil_div(a.dim, NN::BN)), a.splits);
-  hipLaunchKernelGGL((k_loss_dh<NN, T, TO>), grid, dim3(kThreads), 0, s, a);
+void run_dh(const DhArgs& a, bool grid, hipStream_t s) {
+  if constexpr (sizeof(T) == 2) {
+    if (grid) return launch_dh<DmaCore<false, true, 256, 256, 2, 32, 4>, T, TO>(a, s);
+  }
+  launch_dh<AnyCore<T, false, true>, T, TO>(a, s);
 }
 
+template <typename Core, typename T, typename TO>
+void launch_dw(const DwArgs& a, hipStream_t s) {
+  const int nx = static_cast<int>(ceil_div(a.len, Core::BM));
+  const int ny = static_cast<int>(ceil_div(a.dim, Core::BN));
+  hipLaunchKernelGGL((k_loss_dw<Core, T, TO>), dim3(static_cast<unsigned>(grid_blocks(nx, ny))),
+                     dim3(kThreads), 0, s, a, nx, ny);
+}
 template <typename T, typename TO>
-void run_dw(const DwArgs& a, hipStream_t s) {
-  using TN = AnyCore<T, true, true>;
-  const dim3 grid(static_cast<unsigned>(ceil_div(a.len, TN::BM)),
-                  static_cast<unsigned>(ceil_div(a.dim, TN::BN)));
-  hipLaunchKernelGGL((k_loss_dw<TN, T, TO>), grid, dim3(kThreads), 0, s, a);
+void run_dw(const DwArgs& a, bool grid, hipStream_t s) {
+  if constexpr (sizeof(T) == 2) {
+    if (grid) return launch_dw<DmaCore<true, true, 256, 256, 2, 32, 4>, T, TO>(a, s);
+  }
+  launch_dw<AnyCore<T, true, true>, T, TO>(a, s);
 }
 
 struct BackwardArgs {
@@ -390,23 +421,24 @@ template <typename T, typename TH, typename TW>
 void run_backward(const BackwardArgs& b, const LossWs& w, hipStream_t s) {
   T* g = reinterpret_cast<T*>(b.ws + w.g);
   float* part = reinterpret_cast<float*>(b.ws + w.part);
+  const bool grid = on_grid(b.h, b.ldh, b.dim) && on_grid(b.w, b.dim, b.dim);
   for (int64_t v0 = 0; v0 < b.vocab; v0 += w.piece) {
     const int len = static_cast<int>(std::min(w.piece, b.vocab - v0));
     const T* wp = static_cast<const T*>(b.w) + v0 * b.dim;
     run_g<T>(GradArgs{b.h, wp, b.targets, b.lse, b.dloss, g, b.ldh, w.ldg, b.vocab, v0,
                       static_cast<int>(b.n), static_cast<int>(b.dim), len, b.t64},
-             s);
+             grid, s);
     if (b.dh != nullptr) {
       const bool last = v0 + len == b.vocab;
       run_dh<T, TH>(DhArgs{g, wp, part, last && w.splits == 1 ? b.dh : nullptr, w.ldg, b.ld_dh,
                            static_cast<int>(b.n), static_cast<int>(b.dim), len, w.splits,
                            v0 == 0 ? 1 : 0},
-                    s);
+                    grid && on_grid(b.dh, b.ld_dh, b.dim), s);
     }
     if (b.dw != nullptr)
       run_dw<T, TW>(DwArgs{g, b.h, static_cast<TW*>(b.dw) + v0 * b.dim, w.ldg, b.ldh,
                            static_cast<int>(b.n), static_cast<int>(b.dim), len, b.accumulate},
-                    s);
+                    grid && on_grid(b.dw, b.dim, b.dim), s);
   }
   if (b.dh != nullptr && w.splits > 1)
     hipLaunchKernelGGL(k_loss_dh_join<TH>,
@@ -471,10 +503,11 @@ int lm_loss_forward(const void* hidden, int64_t ld_hidden, const void* weight, i
     const StatsArgs a{static_cast<const char*>(hidden) + static_cast<size_t>(r0 * ld_hidden) * sz,
                       weight, tg, tm, ts, at, ld_hidden, vocab, rows, static_cast<int>(dim),
                       targets_64 != 0};
-    if (dtype == MUON_DTYPE_BF16) run_stats<uint16_t>(a, w.v_tiles, stream);
-    else run_stats<float>(a, w.v_tiles, stream);
+    const bool grid = on_grid(a.h, ld_hidden, dim) && on_grid(weight, dim, dim);
+    const int v_tiles = static_cast<int>(dtype == MUON_DTYPE_BF16 ? run_stats<uint16_t>(a, grid, stream)
+                                                                 : run_stats<float>(a, grid, stream));
     hipLaunchKernelGGL(k_loss_join, dim3(static_cast<unsigned>(ceil_div(rows, 64))),
-                       dim3(kThreads), 0, stream, tm, ts, at, static_cast<int>(w.v_tiles), rows,
+                       dim3(kThreads), 0, stream, tm, ts, at, v_tiles, rows,
                        tg, targets_64 != 0, vocab, loss + r0, lse + r0);
   }
   return check_launch("vocabulary loss launch");

@@ -22,6 +22,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
 }
 
+// Orders a wave's LDS accesses before and after it (the lanes of a wave run
+// in step and its LDS accesses complete in order).
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Storage types: float, or uint16_t holding a bf16 pattern.
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(uint16_t x) { return bf16_to_f32(x); }
@@ -65,6 +73,12 @@ inline int check_token_sizes(int64_t n, int64_t vocab, int64_t dim) {
     return set_error(MUON_ERR_BAD_SHAPE, "vocab must be in [1, 2^31 - 2]");
   if (dim < 1 || dim > kMaxDim) return set_error(MUON_ERR_BAD_SHAPE, "dim must be in [1, 2^24]");
   return MUON_OK;
+}
+// On the 16-byte grid, for every type: base, row stride and row length.  The
+// row stride also keeps a tile's lane offsets within 32 bits.
+inline bool on_grid(const void* p, int64_t ld, int64_t cols) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0 && cols % 8 == 0 &&
+         ld <= (1 << 22);
 }
 inline size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 

@@ -15,6 +15,8 @@
 // so a lane holds four consecutive columns of one row.
 #pragma once
 
+#include <type_traits>
+
 #include "train_common.h"
 
 namespace muon {
@@ -51,6 +53,43 @@ __device__ __forceinline__ void each_quad(f32x16_t (&acc)[Core::NJ][Core::MI], F
       }
 }
 
+// Four consecutive columns of a row, `left` >= 1 of which exist.
+template <typename TO>
+__device__ __forceinline__ void store_quad(TO* p, int left, f32x4_t v) {
+  if (left >= 4) {
+    if constexpr (sizeof(TO) == 4) {
+      __builtin_memcpy(p, &v, 16);
+    } else {
+      const u32x2_t w = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+      __builtin_memcpy(p, &w, 8);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+      if (e < left) from_f32(v[e], p + e);
+  }
+}
+
+// Order of the tiles of an nx x ny grid over a launch of grid_blocks(nx, ny)
+// workgroups.  Workgroups go to the 8 XCDs in turn, so workgroup b takes
+// tile (b % 8) per + b / 8: each XCD works through a contiguous part of the
+// list, and its 32 CUs share operands in its L2.  The list runs through
+// bands of kBand row tiles, column by column.
+constexpr int kXcds = 8, kBand = 8;
+__device__ __forceinline__ bool tile_of(int64_t b, int64_t nx, int64_t ny, int& x, int& y) {
+  const int64_t total = nx * ny, per = (total + kXcds - 1) / kXcds;
+  const int64_t t = b % kXcds * per + b / kXcds;
+  if (t >= total) return false;
+  const int64_t band = t / (kBand * ny), r = t - band * kBand * ny;
+  const int64_t h = nx - band * kBand < kBand ? nx - band * kBand : kBand;
+  x = static_cast<int>(band * kBand + r % h);
+  y = static_cast<int>(r / h);
+  return true;
+}
+inline int64_t grid_blocks(int64_t nx, int64_t ny) {
+  return (nx * ny + kXcds - 1) / kXcds * kXcds;
+}
+
 // 8 k (bf16) or 4 k (fp32) of a 16-wide (8-wide) k step from LDS:
 // transposed read of a K-strided tile.  Within each group of 16 lanes, lane
 // l receives element l % 4 of the 8-byte blocks addressed by lanes
@@ -84,6 +123,12 @@ struct AnyCore {
   static constexpr int kOperandBytes = 128 * SC * static_cast<int>(sizeof(T));  // >= CK * SS
   static_assert(CK * SS <= 128 * SC, "a K-strided tile fits the K-contiguous one's space");
   static constexpr int kLdsBytes = 4 * kOperandBytes;
+  static constexpr int kWaves = 2;  // per SIMD, at least
+  static constexpr bool kGrid = false;
+  static __device__ __forceinline__ char* lds() {
+    __shared__ __attribute__((aligned(16))) char mem[kLdsBytes];
+    return mem;
+  }
 
   template <bool KS>
   static __device__ __forceinline__ u32x4_t piece(const T* p, int64_t ld, int n, int K, int k0,
@@ -147,7 +192,8 @@ struct AnyCore {
 
   static __device__ __forceinline__ void run(const T* P, int64_t ldp, int pn, const T* Q,
                                              int64_t ldq, int qn, int K,
-                                             f32x16_t (&acc)[NJ][MI], char* smem) {
+                                             f32x16_t (&acc)[NJ][MI]) {
+    char* smem = lds();
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     const int wi = wave % WM, wj = wave / WM;
     u32x4_t pr[2], qr[2];
@@ -205,35 +251,389 @@ struct AnyCore {
       __syncthreads();
     }
   }
+
+  // C[i][j] = acc (+ add[i][j]) for i < rows, j < cols.  add may be C.
+  template <typename TO, typename TA>
+  static __device__ __forceinline__ void write(f32x16_t (&acc)[NJ][MI], TO* C, int64_t ldc,
+                                               const TA* add, int64_t lda, int rows, int cols) {
+    each_quad<AnyCore>(acc, [&](int i, int j, f32x4_t v) {
+      if (i >= rows || j >= cols) return;
+      if (add != nullptr) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (j + e < cols) v[e] += to_f32(add[i * lda + j + e]);
+      }
+      store_quad(C + i * ldc + j, cols - j, v);
+    });
+  }
 };
 
-// Four consecutive columns of a row, `left` of which exist.
-template <typename TO>
-__device__ __forceinline__ void store_quad(TO* p, int left, f32x4_t v, bool add) {
-  if (left <= 0) return;
-  if (left >= 4) {
-    if constexpr (sizeof(TO) == 4) {
-      if (add) {
-        f32x4_t o;
-        __builtin_memcpy(&o, p, 16);
-        v += o;
-      }
-      __builtin_memcpy(p, &v, 16);
-    } else {
-      if (add) {
-        u32x2_t o;
-        __builtin_memcpy(&o, p, 8);
-        v += f32x4_t{__uint_as_float(o[0] << 16), __uint_as_float(o[0] & 0xffff0000u),
-                     __uint_as_float(o[1] << 16), __uint_as_float(o[1] & 0xffff0000u)};
-      }
-      const u32x2_t w = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-      __builtin_memcpy(p, &w, 8);
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 3; ++e)
-      if (e < left) from_f32(add ? to_f32(p[e]) + v[e] : v[e], p + e);
+// ------------------------------------------------------- aligned bf16 tiles
+//
+// The core for bf16 operands on the 16-byte grid (base, row stride and row
+// length multiples of 8 elements): operand tiles go from memory to LDS by
+// DMA (global_load_lds, 16 bytes a lane, no registers), through NS slots of
+// BK k each, NS - 1 stages in flight.
+//   K-contiguous tile [R rows][BK]: 16-byte chunk c of row r at position
+//     c ^ ((r >> 1) & 7) (BK = 64) or c ^ ((r >> 2) & 3) (BK = 32), so that
+//     16 consecutive rows' 16-byte reads cover the 64 banks once;
+//   K-strided tile [BK][R columns]: 32-column block q of row k at
+//     q ^ (k & 3) (R >= 128) or q ^ ((k >> 1) & 1) (R = 64), the same for
+//     the transposed reads of four k rows.
+// Rows of P and Q past pn, qn are read from the last row there is (their
+// results are not used); k past K come from a page of zeros.  Where K is not
+// a multiple of 8, a K-contiguous operand's rows hold zeros up to the next.
+//
+// Each slot is a __shared__ array of its own: the compiler tracks the DMA
+// into each separately, and its waits before LDS reads let the newer stages
+// stay in flight.
+
+// 16 bytes per lane, memory -> LDS; lane l's data lands at lds + 16 l.  The
+// source is a wave-uniform base plus a 32-bit lane offset.
+__device__ __forceinline__ void dma16(const char* base, uint32_t voff, char* lds) {
+  typedef __attribute__((address_space(1))) void* gbl_t;
+  typedef __attribute__((address_space(3))) void* lds_t;
+  // one scalar: the address is matched as SGPR base + VGPR offset
+  const uint64_t b = reinterpret_cast<uint64_t>(base);
+  const uint64_t sbase =
+      static_cast<uint64_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b >> 32))) << 32 |
+      static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b)));
+  __builtin_amdgcn_global_load_lds((gbl_t)(reinterpret_cast<const char*>(sbase) + voff),
+                                   (lds_t)lds, 16, 0, 0);
+}
+// the same from an address per lane
+__device__ __forceinline__ void dma16_at(const char* p, char* lds) {
+  typedef __attribute__((address_space(1))) void* gbl_t;
+  typedef __attribute__((address_space(3))) void* lds_t;
+  __builtin_amdgcn_global_load_lds((gbl_t)(p), (lds_t)lds, 16, 0, 0);
+}
+
+// Waits until at most VM vector memory instructions (which complete in
+// order) and no LDS reads of this wave are outstanding.
+template <int VM>
+__device__ __forceinline__ void wait_counts() {
+  static_assert(VM < 64, "vmcnt has 6 bits");
+  // vmcnt 3:0 and 15:14, expcnt 6:4 (not waited for), lgkmcnt 11:8
+  __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | 0x70);
+}
+
+static __device__ const u32x4_t kZeroPage[1] = {{0, 0, 0, 0}};
+
+template <int N>
+using Int = std::integral_constant<int, N>;
+// f(Int<I>{}), ..., f(Int<N - 1>{})
+template <int I, int N, typename F>
+__device__ __forceinline__ void static_for(F&& f) {
+  if constexpr (I < N) {
+    f(Int<I>{});
+    static_for<I + 1, N>(f);
   }
 }
+
+template <bool PKS, bool QKS, int BM_, int BN_, int WM_, int BK_, int NS_>
+struct DmaCore {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = 4 / WM_, BK = BK_, NS = NS_;
+  static constexpr int MI = BM / (32 * WM), NJ = BN / (32 * WN), SK = BK / 16;
+  static constexpr int PB = BM * BK * 2, QB = BN * BK * 2;  // bytes of a stage's tiles
+  static constexpr int NP = PB / 4096, NQ = QB / 4096;      // DMA per wave and stage
+  static constexpr int kSlotBytes = PB + QB;
+  static constexpr int kLdsBytes = kSlotBytes;  // of lds()
+  static constexpr bool kGrid = true;  // rows on the 16-byte grid
+  // waves per SIMD: what the LDS allows of workgroups per CU
+  static constexpr int kWaves = 160 * 1024 / (NS * kSlotBytes) < 3 ? 160 * 1024 / (NS * kSlotBytes) : 3;
+  static_assert(BK == 32 || BK == 64, "");
+  static_assert(PB % 4096 == 0 && QB % 4096 == 0, "whole DMA instructions for four waves");
+
+  template <int S>
+  static __device__ __forceinline__ char* slot() {
+    __shared__ __attribute__((aligned(1024))) char mem[kSlotBytes];
+    return mem;
+  }
+  static __device__ __forceinline__ char* lds() { return slot<0>(); }
+
+  // One operand: R rows (or columns), lane offsets of this wave's DMA.
+  template <bool KS, int R>
+  struct Operand {
+    static constexpr int N = R * BK * 2 / 4096;
+    const char* base;  // of stage 0
+    int64_t step;      // bytes from one stage to the next
+    uint32_t off[N];
+    // first k, within a stage, of the 16 bytes lane `lane` copies in the
+    // tile's i-th KiB
+    static __device__ __forceinline__ int k_of(int i, int lane) {
+      if constexpr (KS) {
+        constexpr int LR = R / 8;
+        return i * (64 / LR) + lane / LR;
+      } else {
+        constexpr int LR = BK / 8;
+        const int r = i * (64 / LR) + lane / LR;
+        return 8 * ((lane % LR) ^ (BK == 64 ? (r >> 1) & 7 : (r >> 2) & 3));
+      }
+    }
+    __device__ __forceinline__ void init(const uint16_t* p, int64_t ld, int n, int wave, int lane) {
+      base = reinterpret_cast<const char*>(p);
+      step = KS ? ld * BK * 2 : BK * 2;
+#pragma unroll
+      for (int d = 0; d < N; ++d) {
+        const int i = wave * N + d;
+        const int k = k_of(i, lane);
+        if constexpr (KS) {
+          constexpr int LR = R / 8;
+          const int sw = R >= 128 ? k & 3 : R == 64 ? (k >> 1) & 1 : 0;
+          const int c = 8 * ((lane % LR) ^ (sw << 2));
+          off[d] = static_cast<uint32_t>((k * ld + (c < n ? c : 0)) * 2);
+        } else {
+          const int r = i * (512 / BK) + lane / (BK / 8);
+          off[d] = static_cast<uint32_t>(((r < n ? r : n - 1) * ld + k) * 2);
+        }
+      }
+    }
+    // piece D of the stage that starts at k = kf BK and holds kleft k; the
+    // rest of it is zero
+    template <int D>
+    __device__ __forceinline__ void issue_tail(int64_t kf, char* tile, int wave, int lane,
+                                               int kleft) const {
+      const char* p = k_of(wave * N + D, lane) < kleft ? base + kf * step + off[D]
+                                   : reinterpret_cast<const char*>(kZeroPage);
+      dma16_at(p, tile + (wave * N + D) * 1024);
+    }
+  };
+
+  // LDS byte offset of this lane's part of the fragment of block b, k step
+  // g: K-contiguous one 16-byte read; K-strided two transposed reads, the
+  // second 4 k rows on.
+  template <bool KS, int R>
+  static __device__ __forceinline__ bf16x8_t frag(const char* tile, int row0, int b, int g,
+                                                  int lane) {
+    if constexpr (KS) {
+      const int s = lane & 15, kk = s >> 2;  // k % 4 of the row this lane addresses
+      const int q = (row0 >> 5) + b;
+      const int sw = R >= 128 ? kk : R == 64 ? kk >> 1 : 0;
+      const int kr = 8 * (lane >> 5) + kk;
+      const char* a = tile + (kr * R + ((q ^ sw) << 5) + 16 * ((lane >> 4) & 1) + 4 * (s & 3)) * 2 +
+                      g * 16 * R * 2;
+      const s16x4_t lo = lds_read_tr(reinterpret_cast<const uint16_t*>(a));
+      const s16x4_t hi = lds_read_tr(reinterpret_cast<const uint16_t*>(a + 4 * R * 2));
+      return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      const int r = row0 + (lane & 31);  // blocks are 32 rows: the same swizzle
+      const int sw = BK == 64 ? (r >> 1) & 7 : (r >> 2) & 3;
+      const int c = (2 * g + (lane >> 5)) ^ sw;
+      return *reinterpret_cast<const bf16x8_t*>(tile + (r * BK + 8 * c) * 2 + b * 32 * BK * 2);
+    }
+  }
+
+  struct Frags {
+    bf16x8_t p[MI], q[NJ];
+  };
+
+  static __device__ __forceinline__ void run(const uint16_t* P, int64_t ldp, int pn,
+                                             const uint16_t* Q, int64_t ldq, int qn, int K,
+                                             f32x16_t (&acc)[NJ][MI]) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int ri = (wave % WM) * 32 * MI, rj = (wave / WM) * 32 * NJ;
+    zero_acc(acc);
+    if (K <= 0) return;
+    Operand<PKS, BM> po;
+    Operand<QKS, BN> qo;
+    po.init(P, ldp, pn, wave, lane);
+    qo.init(Q, ldq, qn, wave, lane);
+    // stage 0 is the sum's ragged end, if it has one; the others are whole
+    const int kleft = K % BK, nk = K / BK + (kleft != 0);
+    const int shift = kleft != 0 ? -1 : 0;  // stage kt >= 1 - shift starts at k = (kt + shift) BK
+
+    // DMA instruction D (P's first) of stage kt
+    auto issue1 = [&](int kt, auto slot_c, auto d_c) {
+      char* tile = slot<decltype(slot_c)::value>();
+      constexpr int d = decltype(d_c)::value;
+      if constexpr (d < NP)
+        dma16(po.base + (kt + shift) * po.step, po.off[d], tile + (wave * NP + d) * 1024);
+      else
+        dma16(qo.base + (kt + shift) * qo.step, qo.off[d - NP],
+              tile + PB + (wave * NQ + d - NP) * 1024);
+    };
+    auto issue = [&](int kt, auto slot_c) {
+      static_for<0, NP + NQ>([&](auto d_c) { issue1(kt, slot_c, d_c); });
+    };
+    // this wave's DMA of a stage has landed when at most the newer stages'
+    // is outstanding; behind the barrier, everybody's has
+    constexpr int DPS = NP + NQ;
+    auto landed = [&](int newer) {
+      if (NS > 3 && newer >= 2) wait_counts<2 * DPS>();
+      else if (NS > 2 && newer >= 1) wait_counts<DPS>();
+      else wait_counts<0>();
+    };
+
+    __syncthreads();  // the slots are free (a tile before this one, an epilogue)
+    if (kleft != 0) {
+      const int64_t kf = K / BK;
+      static_for<0, NP>([&](auto d_c) {
+        constexpr int d = decltype(d_c)::value;
+        po.template issue_tail<d>(kf, slot<0>(), wave, lane, kleft);
+      });
+      static_for<0, NQ>([&](auto d_c) {
+        constexpr int d = decltype(d_c)::value;
+        qo.template issue_tail<d>(kf, slot<0>() + PB, wave, lane, kleft);
+      });
+    } else {
+      issue(0, Int<0>{});
+    }
+    static_for<1, NS>([&](auto s) {
+      if (decltype(s)::value < nk) issue(decltype(s)::value, s);
+    });
+    if (nk >= NS) wait_counts<(NS - 1) * DPS>();
+    else wait_counts<0>();
+    __builtin_amdgcn_s_barrier();
+
+    Frags f[2];
+    auto read = [&](Frags& fr, auto slot_c, int g, auto r_c) {
+      constexpr int r = decltype(r_c)::value;
+      const char* tile = slot<decltype(slot_c)::value>();
+      if constexpr (r < MI) fr.p[r] = frag<PKS, BM>(tile, ri, r, g, lane);
+      else fr.q[r - MI] = frag<QKS, BN>(tile + PB, rj, r - MI, g, lane);
+    };
+    static_for<0, MI + NJ>([&](auto r) { read(f[0], Int<0>{}, 0, r); });
+
+    // One stage: the matrix instructions of a k step run while the next
+    // step's fragments are read.  Before the last step every wave has its
+    // fragments of this stage and waits for the next stage's data; behind
+    // the barrier the next stage is whole and this stage's slot is free, and
+    // stage kt + NS goes into it.  STEADY: there is such a stage.
+    auto stage = [&](int kt, auto slot_c, auto steady_c) {
+      constexpr int S = decltype(slot_c)::value;
+      constexpr bool STEADY = decltype(steady_c)::value;
+      static_for<0, SK>([&](auto g_c) {
+        constexpr int g = decltype(g_c)::value;
+        constexpr bool last = g == SK - 1;
+        Frags& cur = f[g & 1];
+        Frags& nxt = f[(g + 1) & 1];
+        if constexpr (last) {
+          if constexpr (STEADY) wait_counts<(NS - 2) * DPS>();
+          else landed(nk - 2 - kt);
+          __builtin_amdgcn_s_barrier();
+          if constexpr (!STEADY) {
+            if (kt + NS < nk) issue(kt + NS, slot_c);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        static_for<0, MI * NJ>([&](auto m_c) {
+          constexpr int m = decltype(m_c)::value;
+          acc[m / MI][m % MI] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+              cur.q[m / MI], cur.p[m % MI], acc[m / MI][m % MI], 0, 0, 0);
+          // (behind the last stage the reads find old data, which is not used)
+          constexpr int RM = MI * NJ < MI + NJ ? MI * NJ : MI + NJ;
+          if constexpr (m < RM)
+            static_for<m * (MI + NJ) / RM, (m + 1) * (MI + NJ) / RM>([&](auto r_c) {
+              if constexpr (!last) read(nxt, slot_c, g + 1, r_c);
+              else read(nxt, Int<(S + 1) % NS>{}, 0, r_c);
+            });
+          // the refill's DMA spread over the step's second part
+          if constexpr (last && STEADY) {
+            constexpr int M0 = MI + NJ < MI * NJ ? MI + NJ : 0, MS = MI * NJ - M0;
+            if constexpr (m >= M0)
+              static_for<(m - M0) * DPS / MS, (m - M0 + 1) * DPS / MS>(
+                  [&](auto d_c) { issue1(kt + NS, slot_c, d_c); });
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        });
+      });
+    };
+    static_assert(SK % 2 == 0, "fragment buffers alternate evenly over a stage");
+    int kt = 0;
+    for (; kt + 2 * NS <= nk; kt += NS)
+      static_for<0, NS>([&](auto s) { stage(kt + decltype(s)::value, s, std::true_type{}); });
+    for (; kt < nk; kt += NS)
+      static_for<0, NS>([&](auto s) {
+        if (kt + decltype(s)::value < nk)
+          stage(kt + decltype(s)::value, s, std::false_type{});
+      });
+  }
+
+  // C[i][j] = acc (+ add[i][j]) for i < rows, j < cols.  add may be C.  The
+  // rows of C and add are on the 16-byte grid and cols is a multiple of 8.
+  // Each wave turns its accumulators into rows in LDS (16-byte chunk c of row
+  // i at c ^ i, in the low bits) and stores 16 bytes a lane along the rows:
+  // values already in the storage type, or fp32 where something is added.
+  template <typename TO, typename TA>
+  static __device__ __forceinline__ void write(f32x16_t (&acc)[NJ][MI], TO* C, int64_t ldc,
+                                               const TA* add, int64_t lda, int rows, int cols) {
+    __syncthreads();  // no wave reads operands any more
+    if (sizeof(TO) == 2 && add == nullptr) rows_out<TO, TA, true>(acc, C, ldc, add, lda, rows, cols);
+    else rows_out<TO, TA, false>(acc, C, ldc, add, lda, rows, cols);
+  }
+
+  // HALF: staged as bf16, else as fp32
+  template <typename TO, typename TA, bool HALF>
+  static __device__ __forceinline__ void rows_out(f32x16_t (&acc)[NJ][MI], TO* C, int64_t ldc,
+                                                  const TA* add, int64_t lda, int rows, int cols) {
+    constexpr int ES = HALF ? 2 : 4;
+    constexpr int RB = NJ * 32 * ES < 256 ? NJ * 32 * ES : 256;  // bytes of a staged row
+    constexpr int CW = RB / ES, JB = CW / 32;                    // its columns, blocks of 32
+    constexpr int NCH = RB / 16, SH = NCH == 16 ? 0 : NCH == 8 ? 1 : 2;
+    constexpr int REGION = 32 * MI * RB, PER = kSlotBytes / REGION;
+    static_assert(PER >= 1 && PER * NS >= 4, "a region for each wave");
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    char* S = slot<0>();
+    static_for<1, NS>([&](auto s) {
+      if (wave / PER == decltype(s)::value) S = slot<decltype(s)::value>();
+    });
+    S += wave % PER * REGION;
+    const int i0 = (wave % WM) * 32 * MI, j0 = (wave / WM) * 32 * NJ;
+    const int fr = lane & 31, hl = lane >> 5;
+    auto chunk = [&](int i, int c) { return S + i * RB + ((c ^ ((i >> SH) & (NCH - 1))) << 4); };
+#pragma unroll
+    for (int h = 0; h < NJ / JB; ++h) {
+#pragma unroll
+      for (int b = 0; b < JB; ++b)
+#pragma unroll
+        for (int bi = 0; bi < MI; ++bi)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const f32x16_t& a = acc[h * JB + b][bi];
+            const int i = 32 * bi + fr;
+            if constexpr (HALF) {
+              *reinterpret_cast<u32x2_t*>(chunk(i, 4 * b + q) + 8 * hl) =
+                  u32x2_t{pack_bf16(a[4 * q], a[4 * q + 1]), pack_bf16(a[4 * q + 2], a[4 * q + 3])};
+            } else {
+              *reinterpret_cast<f32x4_t*>(chunk(i, 8 * b + 2 * q + hl)) =
+                  f32x4_t{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
+            }
+          }
+      // the wave's own region: its LDS accesses complete in order
+      wave_sync();
+      constexpr int LC = ES == 2 || sizeof(TO) == 4 ? NCH : NCH / 2;  // lanes to a row
+      constexpr int LR = 64 / LC;                                     // rows at a time
+      const int c = lane % LC, j = j0 + h * CW + c * (CW / LC);
+      if (j < cols) {
+#pragma unroll 8
+        for (int r = lane / LC; r < 32 * MI; r += LR) {
+          const int i = i0 + r;
+          if (i >= rows) break;
+          if constexpr (HALF) {
+            *reinterpret_cast<u32x4_t*>(C + i * ldc + j) = *reinterpret_cast<u32x4_t*>(chunk(r, c));
+          } else if constexpr (sizeof(TO) == 4) {
+            f32x4_t v = *reinterpret_cast<f32x4_t*>(chunk(r, c));
+            if (add != nullptr) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[e] += to_f32(add[i * lda + j + e]);
+            }
+            *reinterpret_cast<f32x4_t*>(C + i * ldc + j) = v;
+          } else {
+            float v[8], o[8];
+            __builtin_memcpy(v, chunk(r, 2 * c), 16);
+            __builtin_memcpy(v + 4, chunk(r, 2 * c + 1), 16);
+            load8(add + i * lda + j, o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += o[e];
+            store8(C + i * ldc + j, v);
+          }
+        }
+      }
+      wave_sync();
+    }
+  }
+};
 
 }  // namespace muon
