@@ -479,7 +479,7 @@ int muon_clip(const muon_clip_plan_t* plan, void* params, int32_t mode, float ta
  *     workspaces are 256-byte aligned, scratch only (contents on entry are
  *     ignored), and calls that overlap in time need one each.
  *   - Results do not depend on timing: repeated calls give the same bits.
- *   - 0 <= n < 2^26 positions, 1 <= vocab <= 2^31 - 2, 1 <= dim <= 2^24.  */
+ *   - 0 <= n < 2^26 positions, 1 <= vocab <= 2^31 - 2, 1 <= dim <= 2^22.  */
 
 /* out[t] = scale * table[ids[t]], t < n.  A position whose id lies outside
  * [0, vocab) (a padding id such as -1) reads nothing and gets zeros. */

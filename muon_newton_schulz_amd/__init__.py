@@ -205,14 +205,19 @@ def muon_last_error() -> str:
 
 # ---------------------------------------------------------------- marshalling
 
+_dtype_codes = {"fp32": MUON_DTYPE_FP32, "bf16": MUON_DTYPE_BF16, "fp16": MUON_DTYPE_FP16}
+
+
 def dtype_code(dt) -> int:
-    import torch
-    table = {"fp32": MUON_DTYPE_FP32, "bf16": MUON_DTYPE_BF16, "fp16": MUON_DTYPE_FP16,
-             torch.float32: MUON_DTYPE_FP32, torch.bfloat16: MUON_DTYPE_BF16,
-             torch.float16: MUON_DTYPE_FP16}
-    if dt not in table:
-        raise MuonError(MUON_ERR_BAD_DTYPE, f"unsupported dtype {dt}")
-    return table[dt]
+    code = _dtype_codes.get(dt)
+    if code is None:
+        import torch
+        _dtype_codes.update({torch.float32: MUON_DTYPE_FP32, torch.bfloat16: MUON_DTYPE_BF16,
+                             torch.float16: MUON_DTYPE_FP16})
+        code = _dtype_codes.get(dt)
+        if code is None:
+            raise MuonError(MUON_ERR_BAD_DTYPE, f"unsupported dtype {dt}")
+    return code
 
 
 def _mats_array(mats: Sequence[Tuple[int, int, int]]):
@@ -731,10 +736,13 @@ class _Launch:
     """Makes ``dev`` current, and ``stream`` (if given) the stream that torch
     allocates on, around one call; ``handle`` is the hipStream_t."""
 
+    __slots__ = ("handle", "_dev", "_stream")
+
     def __init__(self, dev, stream):
         import torch
-        self._dev = torch.cuda.device(dev)
-        self._stream = None
+        self._dev = self._stream = None
+        if dev.index != torch.cuda.current_device():
+            self._dev = torch.cuda.device(dev)
         if stream is None:
             self.handle = torch.cuda.current_stream(dev).cuda_stream
             return
@@ -747,7 +755,8 @@ class _Launch:
         self._stream = torch.cuda.stream(stream)
 
     def __enter__(self):
-        self._dev.__enter__()
+        if self._dev is not None:
+            self._dev.__enter__()
         if self._stream is not None:
             self._stream.__enter__()
         return self
@@ -755,7 +764,8 @@ class _Launch:
     def __exit__(self, *exc):
         if self._stream is not None:
             self._stream.__exit__(*exc)
-        self._dev.__exit__(*exc)
+        if self._dev is not None:
+            self._dev.__exit__(*exc)
 
 
 def _workspace(workspace, need: int, dev):

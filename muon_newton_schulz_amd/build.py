@@ -8,6 +8,8 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +21,7 @@ SOURCES = ["muon_abi.hip", "elementwise.hip", "ns_gemm.hip", "ns_f32.hip", "ns_s
 # its HBM stream rates
 PROGRAMS = [("mfma_ceiling", "mfma_ceiling.hip"), ("hbm_ceiling", "hbm_ceiling.hip")]
 
+JOBS = min(8, os.cpu_count() or 1)
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
@@ -52,11 +55,18 @@ def _hipcc(cmd, out, verbose):
 
 
 def build(verbose: bool = True) -> str:
-    srcs = [os.path.join(CSRC, s) for s in SOURCES]
-    _hipcc([HIPCC, *FLAGS, *srcs], LIB, verbose)
-    exe_flags = [f for f in FLAGS if f not in ("-fPIC", "-shared")]
-    for exe, src in PROGRAMS:
-        _hipcc([HIPCC, *exe_flags, os.path.join(CSRC, src)], os.path.join(PKG, exe), verbose)
+    # one object per source, compiled side by side, then one link
+    compile_flags = [f for f in FLAGS if f != "-shared"]
+    exe_flags = [f for f in compile_flags if f != "-fPIC"]
+    with tempfile.TemporaryDirectory() as tmp, ThreadPoolExecutor(JOBS) as pool:
+        objs = [os.path.join(tmp, s + ".o") for s in SOURCES]
+        jobs = [pool.submit(_hipcc, [HIPCC, *compile_flags, "-c", os.path.join(CSRC, s)], o, verbose)
+                for s, o in zip(SOURCES, objs)]
+        jobs += [pool.submit(_hipcc, [HIPCC, *exe_flags, os.path.join(CSRC, src)],
+                             os.path.join(PKG, exe), verbose) for exe, src in PROGRAMS]
+        for j in jobs:
+            j.result()
+        _hipcc([HIPCC, "--offload-arch=gfx950", "-fPIC", "-shared", *objs], LIB, verbose)
     return LIB
 
 

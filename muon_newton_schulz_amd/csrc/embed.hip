@@ -9,11 +9,16 @@
 //
 // The gradient sorts the positions by id (stable, so that every sum runs in
 // the order of the positions and repeated calls give the same bits), cuts
-// the sorted list into chunks of kChunk positions and sums each run of
+// the sorted list into chunks of 16 or 32 positions and sums each run of
 // equal ids inside a chunk in fp32 registers.  A run that lies inside its
 // chunk is finished there; a run that crosses a chunk border leaves one
 // fp32 partial row per chunk, which a second kernel adds in chunk order.
 // A frequent token therefore spreads over as many workgroups as a rare one.
+//
+// Rows that no position names are zeroed by workgroups of their own: the
+// first rows beside the sort, which leaves the GPU idle (whether named or
+// not), the rest beside the sums, when the sorted ids tell which they are.
+#include <algorithm>
 #include <cmath>
 
 #include "train_common.h"
@@ -74,14 +79,24 @@ __global__ __launch_bounds__(kThreads) void k_embed_fwd(const TT* __restrict__ t
 
 // -------------------------------------------------------------------- sort
 //
-// LSD radix sort of (key, position) by key, at most kMaxBits bits a pass.
-// key = id, or vocab for an id outside [0, vocab), which puts the positions
-// without a row last.  Stable: each wave owns a contiguous part of its
-// workgroup's keys and places 64 keys at a time, a key's rank among equal
-// digits of the 64 being the number of lower lanes that hold the digit.
+// Stable sort of (key, position) by key: key = id, or vocab for an id outside
+// [0, vocab), which puts the positions without a row last.
+//
+// Up to kRankN keys: a key's place is the number of keys that are smaller,
+// or equal and before it.  All pairs are compared, n^2 / 64 wave
+// instructions spread over the GPU, in one launch (8192 keys: 8 us; one
+// workgroup's radix sort in LDS took 26).
+// More: LSD radix sort, at most kMaxBits bits a pass, a histogram and a
+// scatter launch each.  Each wave owns a contiguous part of its workgroup's
+// keys and places 64 keys at a time, a key's rank among equal digits of the
+// 64 being the number of lower lanes that hold the digit.
 
 constexpr int kMaxBits = 9;
 constexpr int kMaxBins = 1 << kMaxBits;
+
+__device__ __forceinline__ uint32_t clip_key(int64_t v, int64_t vocab) {
+  return static_cast<uint32_t>(v >= 0 && v < vocab ? v : vocab);
+}
 
 // lanes of the wave (among `active`) whose digit equals this lane's
 __device__ __forceinline__ uint64_t match_digit(uint32_t d, int bits, uint64_t active) {
@@ -115,224 +130,230 @@ __device__ __forceinline__ void block_exclusive_scan(uint32_t* h, int n, uint32_
   __syncthreads();
 }
 
-// Zeroes the table gradient: the part of workgroup `b` of `nb`.
+// Zeroes n elements from g: the part of workgroup `b` of `nb`.
 template <typename TG>
-__device__ __forceinline__ void zero_part(TG* g, int64_t total, int64_t b, int64_t nb,
-                                          int threads) {
+__device__ __forceinline__ void zero_part(TG* g, int64_t n, int64_t b, int64_t nb, int threads) {
   // 16-byte stores on the aligned middle, the ragged ends by workgroup 0
   const int64_t per = 16 / sizeof(TG);
   const int64_t mis = static_cast<int64_t>((reinterpret_cast<uintptr_t>(g) & 15) / sizeof(TG));
   int64_t head = mis ? per - mis : 0;
-  if (head > total) head = total;
-  const int64_t n16 = (total - head) / per;
+  if (head > n) head = n;
+  const int64_t n16 = (n - head) / per;
   u32x4_t* v = reinterpret_cast<u32x4_t*>(g + head);
   for (int64_t i = b * threads + threadIdx.x; i < n16; i += nb * threads) v[i] = u32x4_t{0, 0, 0, 0};
   if (b == 0) {
     if (static_cast<int64_t>(threadIdx.x) < head) g[threadIdx.x] = TG{};
     const int64_t t = head + n16 * per + threadIdx.x;
-    if (t < total) g[t] = TG{};
+    if (t < n) g[t] = TG{};
+  }
+}
+// Zeroes the rows of [r0, r0 + 32) whose bit of `named` is clear and that
+// are below vocab: part `b` of `nb`.
+template <typename TG>
+__device__ __forceinline__ void zero_rows(TG* g, uint32_t named, int64_t r0, int64_t vocab,
+                                          int64_t dim, int b, int nb, int threads) {
+  const int rows = static_cast<int>(vocab - r0 < 32 ? vocab - r0 : 32);
+  for (int r = 0; r < rows;) {
+    if ((named >> r) & 1u) {
+      ++r;
+      continue;
+    }
+    int e = r + 1;
+    while (e < rows && !((named >> e) & 1u)) ++e;
+    zero_part(g + (r0 + r) * dim, (e - r) * dim, b, nb, threads);
+    r = e;
   }
 }
 
-// Up to kSmallN keys: one workgroup sorts them in LDS in one launch, while
-// the other workgroups of the launch zero the table gradient.
-constexpr int kSmallN = 8192;
-constexpr int kSmallThreads = 1024;
-constexpr int kSmallWaves = kSmallThreads / 64;
+// Zeroes the rows from v0 on that are not among the sorted keys.  Workgroup
+// b takes part b % parts of every so many-th group of 32 rows; lane l of
+// each wave looks row l of the group up.
+template <typename TG>
+__device__ __forceinline__ void zero_unnamed(TG* g, const uint32_t* keys, int64_t n, int64_t v0,
+                                             int64_t vocab, int64_t dim, int64_t b, int64_t nb,
+                                             int parts, int threads) {
+  const int lane = threadIdx.x & 63;
+  for (int64_t r0 = v0 + b / parts * 32; r0 < vocab; r0 += nb / parts * 32) {
+    bool named = false;
+    if (lane < 32 && r0 + lane < vocab) {
+      const uint32_t row = static_cast<uint32_t>(r0 + lane);
+      int64_t lo = 0, hi = n;
+      while (lo < hi) {
+        const int64_t mid = (lo + hi) >> 1;
+        if (keys[mid] < row) lo = mid + 1;
+        else hi = mid;
+      }
+      named = lo < n && keys[lo] == row;
+    }
+    zero_rows(g, static_cast<uint32_t>(__ballot(named)), r0, vocab, dim,
+              static_cast<int>(b % parts), parts, threads);
+  }
+}
 
+constexpr int kRankN = 16384;
+constexpr int kRankThreads = 1024;
+constexpr int kRankWaves = kRankThreads / 64;
+
+// Each workgroup places 64 keys, one a lane; its waves share the keys they
+// are compared with.  The workgroups from rank_blocks on zero the first
+// zero_n elements of the table gradient.
 template <typename ID, typename TG>
-__global__ __launch_bounds__(kSmallThreads) void k_sort_small(
-    const ID* __restrict__ ids, int n, int64_t vocab, int bits, int passes,
+__global__ __launch_bounds__(kRankThreads) void k_sort_rank(
+    const ID* __restrict__ ids, int n, int64_t vocab, int rank_blocks,
     uint32_t* __restrict__ keys_out, uint32_t* __restrict__ pos_out, TG* __restrict__ dtable,
-    int64_t total) {
-  __shared__ uint32_t key[2][kSmallN];
-  __shared__ uint16_t pos[2][kSmallN];
-  __shared__ uint32_t cnt[kSmallWaves][kMaxBins];
-  __shared__ uint32_t base[kMaxBins], tmp[kSmallWaves];
-  if (blockIdx.x > 0) {
-    zero_part(dtable, total, blockIdx.x - 1, gridDim.x - 1, kSmallThreads);
+    int64_t zero_n) {
+  __shared__ __attribute__((aligned(16))) uint32_t key[kRankN];
+  __shared__ uint32_t red[kRankWaves][64];
+  if (static_cast<int>(blockIdx.x) >= rank_blocks) {
+    zero_part(dtable, zero_n, blockIdx.x - rank_blocks, gridDim.x - rank_blocks, kRankThreads);
     return;
   }
-  const int t = threadIdx.x, lane = t & 63, w = t >> 6;
-  const uint32_t vocab32 = static_cast<uint32_t>(vocab);
-  for (int i = t; i < n; i += kSmallThreads) {
-    const int64_t v = static_cast<int64_t>(ids[i]);
-    key[0][i] = v >= 0 && v < vocab ? static_cast<uint32_t>(v) : vocab32;
-    pos[0][i] = static_cast<uint16_t>(i);
-  }
-  // contiguous part of each wave, in steps of 64
-  const int part = ((n + kSmallWaves - 1) / kSmallWaves + 63) / 64 * 64;
-  const int lo = w * part, hi = lo + part < n ? lo + part : n;
-  const int bins = 1 << bits;
-  const uint32_t mask = static_cast<uint32_t>(bins) - 1u;
-  int cur = 0;
-  for (int p = 0; p < passes; ++p) {
-    const int shift = p * bits;
-    for (int i = t; i < kSmallWaves * kMaxBins; i += kSmallThreads) cnt[0][i] = 0;
-    __syncthreads();
-    for (int i = lo + lane; i < hi; i += 64) atomicAdd(&cnt[w][(key[cur][i] >> shift) & mask], 1u);
-    __syncthreads();
-    for (int b = t; b < bins; b += kSmallThreads) {
-      uint32_t s = 0;
-      for (int k = 0; k < kSmallWaves; ++k) {
-        const uint32_t c = cnt[k][b];
-        cnt[k][b] = s;
-        s += c;
-      }
-      base[b] = s;
+  const int t = threadIdx.x, lane = t & 63;
+  const int w = __builtin_amdgcn_readfirstlane(t >> 6);
+  // padded to whole groups of 64 with a key above all others
+  const int np = (n + 63) / 64 * 64;
+  for (int i = t; i < np; i += kRankThreads)
+    key[i] = i < n ? clip_key(static_cast<int64_t>(ids[i]), vocab) : 0xffffffffu;
+  __syncthreads();
+  const int i0 = blockIdx.x * 64, i = i0 + lane;
+  const uint32_t ki = key[i];
+  uint32_t count = 0;
+  // keys of [lo, hi) below x, both multiples of 4
+  auto below = [&](int lo, int hi, uint32_t x) {
+    for (int j = lo; j < hi; j += 4) {
+      const uint4 k = *reinterpret_cast<const uint4*>(key + j);
+      count += k.x < x;
+      count += k.y < x;
+      count += k.z < x;
+      count += k.w < x;
     }
-    __syncthreads();
-    block_exclusive_scan<kSmallThreads>(base, bins, tmp);
-    for (int i0 = lo; i0 < hi; i0 += 64) {
-      const int i = i0 + lane;
-      const bool on = i < hi;
-      const uint32_t k = on ? key[cur][i] : 0u;
-      const uint32_t d = (k >> shift) & mask;
-      const uint64_t m = match_digit(d, bits, __ballot(on));
-      if (on) {
-        const uint32_t rank = __popcll(m & ((1ull << lane) - 1ull));
-        const uint32_t to = base[d] + cnt[w][d] + rank;
-        key[cur ^ 1][to] = k;
-        pos[cur ^ 1][to] = pos[cur][i];
-        // the last lane of the digit moves the wave's counter on
-        if ((m >> lane) == 1ull) cnt[w][d] += __popcll(m);
-      }
-      wave_sync();  // the wave's next 64 keys read the counters just moved
+  };
+  // this wave's part; equal keys count where they come before, so k <= ki,
+  // that is k < ki + 1, in the groups of 64 before this one (a position of
+  // the padding is not placed: its ki + 1 may wrap)
+  const int part = (np / 64 + kRankWaves - 1) / kRankWaves * 64;
+  const int lo = min(w * part, np), hi = min(lo + part, np);
+  below(lo, min(hi, i0), ki + 1u);
+  below(max(lo, i0 + 64), hi, ki);
+  if (lo <= i0 && i0 < hi)
+    for (int j = 0; j < 64; ++j) {
+      const uint32_t k = key[i0 + j];
+      count += k < ki || (k == ki && j < lane);
     }
-    __syncthreads();
-    cur ^= 1;
-  }
-  for (int i = t; i < n; i += kSmallThreads) {
-    keys_out[i] = key[cur][i];
-    pos_out[i] = pos[cur][i];
-  }
+  red[w][lane] = count;
+  __syncthreads();
+  if (w != 0 || i >= n) return;
+  uint32_t rank = 0;
+#pragma unroll
+  for (int k = 0; k < kRankWaves; ++k) rank += red[k][lane];
+  keys_out[rank] = ki;
+  pos_out[rank] = static_cast<uint32_t>(i);
 }
 
-// More keys: per pass a histogram per workgroup, a scan over all of them,
-// and a stable scatter.
+// Radix passes: at most kSortBlocks workgroups, so that each can add up the
+// others' histograms by itself; part: keys of a wave, a multiple of 64.
 constexpr int kSortThreads = 256;
 constexpr int kSortWaves = kSortThreads / 64;
-constexpr int kSortKeys = 4096;  // keys per workgroup
-constexpr int kWaveKeys = kSortKeys / kSortWaves;
+constexpr int kSortBlocks = 64;
 
-__device__ __forceinline__ uint32_t clip_key(int64_t v, int64_t vocab) {
-  return static_cast<uint32_t>(v >= 0 && v < vocab ? v : vocab);
-}
-
-// The first pass reads the ids themselves (FIRST); its launch has zero_blocks
-// more workgroups, which zero the table gradient.
+// The first pass reads the ids themselves (FIRST); its launch has more
+// workgroups, which zero the first zero_n elements of the table gradient.
 template <bool FIRST, typename ID, typename TG>
 __global__ __launch_bounds__(kSortThreads) void k_sort_hist(
     const ID* __restrict__ ids, const uint32_t* __restrict__ keys, int64_t n, int64_t vocab,
-    int shift, int bits, int n_blocks, uint32_t* __restrict__ hist, TG* __restrict__ dtable,
-    int64_t total) {
+    int shift, int bits, int n_blocks, int part, uint32_t* __restrict__ hist,
+    TG* __restrict__ dtable, int64_t zero_n) {
   if (FIRST && static_cast<int>(blockIdx.x) >= n_blocks) {
-    zero_part(dtable, total, blockIdx.x - n_blocks, gridDim.x - n_blocks, kSortThreads);
+    zero_part(dtable, zero_n, blockIdx.x - n_blocks, gridDim.x - n_blocks, kSortThreads);
     return;
   }
   __shared__ uint32_t cnt[kMaxBins];
   const int bins = 1 << bits;
   for (int b = threadIdx.x; b < bins; b += kSortThreads) cnt[b] = 0;
   __syncthreads();
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kSortKeys;
-  for (int k = threadIdx.x; k < kSortKeys; k += kSortThreads)
-    if (i0 + k < n) {
-      const uint32_t key = FIRST ? clip_key(static_cast<int64_t>(ids[i0 + k]), vocab) : keys[i0 + k];
-      atomicAdd(&cnt[(key >> shift) & (bins - 1)], 1u);
-    }
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * part * kSortWaves;
+  for (int k = threadIdx.x; k < part * kSortWaves && i0 + k < n; k += kSortThreads) {
+    const uint32_t key = FIRST ? clip_key(static_cast<int64_t>(ids[i0 + k]), vocab) : keys[i0 + k];
+    atomicAdd(&cnt[(key >> shift) & (bins - 1)], 1u);
+  }
   __syncthreads();
   for (int b = threadIdx.x; b < bins; b += kSortThreads)
-    hist[static_cast<int64_t>(b) * n_blocks + blockIdx.x] = cnt[b];
-}
-
-// exclusive scan of m entries in place, one workgroup
-__global__ __launch_bounds__(1024) void k_sort_scan(uint32_t* __restrict__ h, int64_t m) {
-  __shared__ uint32_t tmp[16];
-  __shared__ uint32_t carry_s;
-  const int t = threadIdx.x, lane = t & 63, w = t >> 6;
-  uint32_t carry = 0;
-  for (int64_t i0 = 0; i0 < m; i0 += 4096) {
-    const int64_t i = i0 + 4 * t;
-    uint32_t v[4], s = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[k] = i + k < m ? h[i + k] : 0;
-      s += v[k];
-    }
-    uint32_t sc = s;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const uint32_t u = __shfl_up(sc, o, 64);
-      if (lane >= o) sc += u;
-    }
-    if (lane == 63) tmp[w] = sc;
-    __syncthreads();
-    uint32_t base = carry;
-    for (int k = 0; k < w; ++k) base += tmp[k];
-    uint32_t ex = base + sc - s;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (i + k < m) h[i + k] = ex;
-      ex += v[k];
-    }
-    if (t == 1023) carry_s = base + sc;
-    __syncthreads();
-    carry = carry_s;
-  }
+    hist[static_cast<int64_t>(blockIdx.x) * bins + b] = cnt[b];
 }
 
 template <bool FIRST, typename ID>
 __global__ __launch_bounds__(kSortThreads) void k_sort_scatter(
     const ID* __restrict__ ids, const uint32_t* __restrict__ keys,
     const uint32_t* __restrict__ pos, int64_t n, int64_t vocab, int shift, int bits, int n_blocks,
-    const uint32_t* __restrict__ hist, uint32_t* __restrict__ keys_out,
+    int part, const uint32_t* __restrict__ hist, uint32_t* __restrict__ keys_out,
     uint32_t* __restrict__ pos_out) {
   __shared__ uint32_t cnt[kSortWaves][kMaxBins];
+  __shared__ uint32_t base[kMaxBins], tmp[kSortWaves];
   const int bins = 1 << bits;
   const uint32_t mask = static_cast<uint32_t>(bins) - 1u;
   const int t = threadIdx.x, lane = t & 63, w = t >> 6;
   for (int i = t; i < kSortWaves * kMaxBins; i += kSortThreads) cnt[0][i] = 0;
   __syncthreads();
-  const int64_t lo = static_cast<int64_t>(blockIdx.x) * kSortKeys + w * kWaveKeys;
-  uint32_t k[kWaveKeys / 64];
+  const int64_t lo = (static_cast<int64_t>(blockIdx.x) * kSortWaves + w) * part;
+  const int64_t hi = lo + part < n ? lo + part : n;
+  auto key_at = [&](int64_t i) {
+    return FIRST ? clip_key(static_cast<int64_t>(ids[i]), vocab) : keys[i];
+  };
+  for (int64_t i = lo + lane; i < hi; i += 64) atomicAdd(&cnt[w][(key_at(i) >> shift) & mask], 1u);
+  // a digit's first place: all keys with lower digits, then this digit's in
+  // the workgroups before this one, then in this one's waves before
+  uint32_t before[kMaxBins / kSortThreads];
 #pragma unroll
-  for (int r = 0; r < kWaveKeys / 64; ++r) {
-    const int64_t i = lo + r * 64 + lane;
-    k[r] = 0;
-    if (i < n) {
-      k[r] = FIRST ? clip_key(static_cast<int64_t>(ids[i]), vocab) : keys[i];
-      atomicAdd(&cnt[w][(k[r] >> shift) & mask], 1u);
+  for (int u = 0; u < kMaxBins / kSortThreads; ++u) {
+    const int b = t + u * kSortThreads;
+    before[u] = 0;
+    if (b < bins) {
+      uint32_t all = 0;
+#pragma unroll 8
+      for (int k = 0; k < n_blocks; ++k) {
+        const uint32_t c = hist[static_cast<int64_t>(k) * bins + b];
+        all += c;
+        if (k < static_cast<int>(blockIdx.x)) before[u] += c;
+      }
+      base[b] = all;
     }
   }
   __syncthreads();
-  for (int b = t; b < bins; b += kSortThreads) {
-    uint32_t s = hist[static_cast<int64_t>(b) * n_blocks + blockIdx.x];
-    for (int j = 0; j < kSortWaves; ++j) {
-      const uint32_t c = cnt[j][b];
-      cnt[j][b] = s;
-      s += c;
+  block_exclusive_scan<kSortThreads>(base, bins, tmp);
+#pragma unroll
+  for (int u = 0; u < kMaxBins / kSortThreads; ++u) {
+    const int b = t + u * kSortThreads;
+    if (b < bins) {
+      uint32_t s = base[b] + before[u];
+      for (int j = 0; j < kSortWaves; ++j) {
+        const uint32_t c = cnt[j][b];
+        cnt[j][b] = s;
+        s += c;
+      }
     }
   }
   __syncthreads();
-#pragma unroll
-  for (int r = 0; r < kWaveKeys / 64; ++r) {
-    const int64_t i = lo + r * 64 + lane;
-    const bool on = i < n;
-    const uint32_t d = (k[r] >> shift) & mask;
+  for (int64_t i0 = lo; i0 < hi; i0 += 64) {
+    const int64_t i = i0 + lane;
+    const bool on = i < hi;
+    const uint32_t k = on ? key_at(i) : 0u;
+    const uint32_t d = (k >> shift) & mask;
     const uint64_t m = match_digit(d, bits, __ballot(on));
     if (on) {
       const uint32_t to = cnt[w][d] + __popcll(m & ((1ull << lane) - 1ull));
-      keys_out[to] = k[r];
+      keys_out[to] = k;
       pos_out[to] = FIRST ? static_cast<uint32_t>(i) : pos[i];
+      // the last lane of the digit moves the wave's counter on
       if ((m >> lane) == 1ull) cnt[w][d] += __popcll(m);
     }
-    wave_sync();
+    wave_sync();  // the wave's next 64 keys read the counters just moved
   }
 }
 
 // -------------------------------------------------------------------- sums
 
-constexpr int kChunk = 32;
+constexpr int kSumThreads = 128;
+constexpr int kSumCols = kSumThreads * 8;
 
 // The row of a finished run: scale * sum, plus the old row when
 // accumulating; cols columns (1..8) from c.
@@ -366,15 +387,23 @@ __device__ __forceinline__ float* partial_row(float* parts, int64_t chunk, int s
   return parts + (2 * chunk + slot) * dim_p;
 }
 
+// The workgroups from sum_blocks on zero the unnamed rows from zero_v0 on.
 template <typename TD, typename TG>
-__global__ __launch_bounds__(kThreads) void k_embed_runs(
+__global__ __launch_bounds__(kSumThreads) void k_embed_runs(
     const TD* __restrict__ dout, int64_t ld, const uint32_t* __restrict__ keys,
     const uint32_t* __restrict__ pos, int64_t n, int64_t vocab, int64_t dim, int64_t dim_p,
-    float scale, int accumulate, TG* __restrict__ dtable, float* __restrict__ parts) {
-  const int64_t chunk = blockIdx.x;
-  const int64_t s0 = chunk * kChunk;
-  const int len = static_cast<int>(n - s0 < kChunk ? n - s0 : kChunk);
-  const int64_t c = static_cast<int64_t>(blockIdx.y) * kCols + threadIdx.x * 8;
+    int chunk_len, float scale, int accumulate, TG* __restrict__ dtable,
+    float* __restrict__ parts, int64_t sum_blocks, int slices, int64_t zero_v0,
+    int zero_parts) {
+  if (static_cast<int64_t>(blockIdx.x) >= sum_blocks) {
+    zero_unnamed(dtable, keys, n, zero_v0, vocab, dim, blockIdx.x - sum_blocks,
+                 gridDim.x - sum_blocks, zero_parts, kSumThreads);
+    return;
+  }
+  const int64_t chunk = blockIdx.x / slices;
+  const int64_t s0 = chunk * chunk_len;
+  const int len = static_cast<int>(n - s0 < chunk_len ? n - s0 : chunk_len);
+  const int64_t c = static_cast<int64_t>(blockIdx.x % slices) * kSumCols + threadIdx.x * 8;
   if (c >= dim) return;
   const int cols = static_cast<int>(dim - c < 8 ? dim - c : 8);
   const uint32_t none = static_cast<uint32_t>(vocab);
@@ -431,17 +460,18 @@ __global__ __launch_bounds__(kThreads) void k_embed_runs(
 // Adds the partial rows of the run that starts in this chunk and crosses
 // its end, in chunk order.
 template <typename TG>
-__global__ __launch_bounds__(kThreads) void k_embed_join(
-    const uint32_t* __restrict__ keys, int64_t n, int64_t n_chunks, int64_t vocab, int64_t dim,
-    int64_t dim_p, float scale, int accumulate, TG* __restrict__ dtable, float* parts) {
-  const int64_t chunk = blockIdx.x;
-  const int64_t end = (chunk + 1) * kChunk;
+__global__ __launch_bounds__(kSumThreads) void k_embed_join(
+    const uint32_t* __restrict__ keys, int64_t n, int64_t vocab, int64_t dim, int64_t dim_p,
+    int chunk_len, float scale, int accumulate, TG* __restrict__ dtable, float* parts,
+    int slices) {
+  const int64_t chunk = blockIdx.x / slices;
+  const int64_t end = (chunk + 1) * chunk_len;
   if (end >= n) return;
   const uint32_t key = keys[end - 1];
   if (key == static_cast<uint32_t>(vocab) || keys[end] != key) return;
   // the run started in an earlier chunk: that chunk joins it
-  if (chunk > 0 && keys[end - kChunk] == key && keys[end - kChunk - 1] == key) return;
-  const int64_t c = static_cast<int64_t>(blockIdx.y) * kCols + threadIdx.x * 8;
+  if (chunk > 0 && keys[end - chunk_len] == key && keys[end - chunk_len - 1] == key) return;
+  const int64_t c = static_cast<int64_t>(blockIdx.x % slices) * kSumCols + threadIdx.x * 8;
   if (c >= dim) return;
   // the last chunk that the run reaches: first position whose key exceeds it
   int64_t lo = end, hi = n;
@@ -450,16 +480,17 @@ __global__ __launch_bounds__(kThreads) void k_embed_join(
     if (keys[mid] <= key) lo = mid + 1;
     else hi = mid;
   }
-  const int64_t last = (lo - 1) / kChunk;
+  const int64_t last = (lo - 1) / chunk_len;
   float acc[8];
   load8(partial_row(parts, chunk, 1, dim_p) + c, acc);
   int64_t k = chunk + 1;
-  for (; k + 3 <= last; k += 4) {
-    float x[4][8];
+  constexpr int U = 8;
+  for (; k + U - 1 <= last; k += U) {
+    float x[U][8];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) load8(partial_row(parts, k + u, 0, dim_p) + c, x[u]);
+    for (int u = 0; u < U; ++u) load8(partial_row(parts, k + u, 0, dim_p) + c, x[u]);
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
+    for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int e = 0; e < 8; ++e) acc[e] += x[u][e];
   }
@@ -473,6 +504,91 @@ __global__ __launch_bounds__(kThreads) void k_embed_join(
             static_cast<int>(dim - c < 8 ? dim - c : 8), scale, accumulate);
 }
 
+// ------------------------------------------------------------ few positions
+//
+// Up to kDirectN positions need no sort: the workgroup of a position compares
+// its id with all others and, if it is the first to name its row, adds the
+// row's positions up in order.  Other workgroups zero the rows that nobody
+// names, whose bits they gather from the ids.  One launch instead of three:
+// 512 positions into 32000 x 2048 take 26 us, 700 take 30, where the sort's
+// three launches take 31; 1024 take 39 and 32.
+constexpr int kDirectN = 640;
+constexpr int kDirectRows = 4096;  // rows of a zeroing workgroup at most
+
+template <typename TD, typename TG, typename ID>
+__global__ __launch_bounds__(kSumThreads) void k_embed_direct(
+    const TD* __restrict__ dout, int64_t ld, const ID* __restrict__ ids, int n, int64_t vocab,
+    int64_t dim, float scale, int accumulate, TG* __restrict__ dtable, int sum_blocks, int slices,
+    int zero_len, int zero_parts) {
+  const int t = threadIdx.x, lane = t & 63, w = t >> 6;
+  if (static_cast<int>(blockIdx.x) >= sum_blocks) {
+    // rows [r0, r0 + zero_len), a multiple of 32
+    __shared__ uint32_t bits[kDirectRows / 32];
+    const int b = blockIdx.x - sum_blocks;
+    const int64_t r0 = static_cast<int64_t>(b / zero_parts) * zero_len;
+    for (int i = t; i < zero_len / 32; i += kSumThreads) bits[i] = 0u;
+    __syncthreads();
+    for (int i = t; i < n; i += kSumThreads) {
+      const int64_t v = static_cast<int64_t>(ids[i]) - r0;
+      if (v >= 0 && v < zero_len) atomicOr(&bits[v >> 5], 1u << (v & 31));
+    }
+    __syncthreads();
+    for (int i = 0; i < zero_len / 32 && r0 + 32 * i < vocab; ++i)
+      zero_rows(dtable, bits[i], r0 + 32 * i, vocab, dim, b % zero_parts, zero_parts, kSumThreads);
+    return;
+  }
+  __shared__ uint64_t same[kDirectN / 64];
+  const int at = blockIdx.x / slices;
+  const int64_t id = static_cast<int64_t>(ids[at]);
+  if (id < 0 || id >= vocab) return;
+  const int words = (n + 63) / 64;
+  for (int k = w; k < words; k += kSumThreads / 64) {
+    const int i = 64 * k + lane;
+    const uint64_t m = __ballot(i < n && static_cast<int64_t>(ids[i]) == id);
+    if (lane == 0) same[k] = m;
+  }
+  __syncthreads();
+  // a position before this one names the row: that one's workgroup adds up
+  for (int k = 0; k < at / 64; ++k)
+    if (same[k] != 0) return;
+  if ((same[at / 64] & ((1ull << (at % 64)) - 1ull)) != 0) return;
+  const int64_t c = static_cast<int64_t>(blockIdx.x % slices) * kSumCols + t * 8;
+  if (c >= dim) return;
+  const int cols = static_cast<int>(dim - c < 8 ? dim - c : 8);
+  float acc[8] = {};
+  constexpr int U = 8;
+  int k = at / 64;
+  uint64_t m = same[k];
+  bool more = true;
+  while (more) {
+    float x[U][8];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[u][e] = 0.0f;
+      while (m == 0 && k + 1 < words) m = same[++k];
+      more = m != 0;
+      if (!more) continue;
+      const int i = 64 * k + __ffsll(static_cast<unsigned long long>(m)) - 1;
+      m &= m - 1;
+      const TD* p = dout + i * ld + c;
+      if (cols == 8) {
+        load8(p, x[u]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (e < cols) x[u][e] = to_f32(p[e]);
+      }
+    }
+    // (the slots left over add zeros)
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] += x[u][e];
+  }
+  write_row(dtable + id * dim + c, acc, cols, scale, accumulate);
+}
+
 // -------------------------------------------------------------------- host
 
 int key_bits(int64_t vocab) {
@@ -483,12 +599,21 @@ int key_bits(int64_t vocab) {
 
 struct EmbedWs {
   size_t keys[2], pos[2], hist, parts, total;
-  int64_t blocks, chunks, dim_p;
+  int64_t chunks, dim_p;
+  int blocks, part;  // radix workgroups, keys of a wave
+  int chunk_len, slices;
 };
 EmbedWs embed_ws(int64_t n, int64_t dim) {
   EmbedWs w{};
-  w.blocks = (n + kSortKeys - 1) / kSortKeys;
-  w.chunks = (n + kChunk - 1) / kChunk;
+  const int64_t groups = (n + 63) / 64;  // of 64 keys; at least 4 a wave
+  w.part = static_cast<int>(std::max<int64_t>(4, (groups + kSortBlocks * kSortWaves - 1) /
+                                                     (kSortBlocks * kSortWaves)) * 64);
+  w.blocks = static_cast<int>((n + w.part * kSortWaves - 1) / (w.part * kSortWaves));
+  w.slices = static_cast<int>((dim + kSumCols - 1) / kSumCols);
+  // 32 positions a chunk, or 16 where that leaves too few workgroups for the
+  // 256 CUs to hide the loads' latency (8191 x 2048: 21 us against 16)
+  w.chunk_len = (n + 31) / 32 * w.slices >= 4096 ? 32 : 16;
+  w.chunks = (n + w.chunk_len - 1) / w.chunk_len;
   w.dim_p = (dim + 7) / 8 * 8;
   size_t o = 0;
   for (int k = 0; k < 2; ++k) {
@@ -522,78 +647,111 @@ void run_fwd(const void* table, const void* ids, int64_t n, int64_t vocab, int64
                      scale, static_cast<TO*>(out), ld);
 }
 
-// workgroups that zero the table gradient beside the sort: enough to reach
-// the write rate, few enough that each has several stores
-int zero_blocks(int64_t total, size_t size, int threads) {
-  const int64_t pieces = (total * static_cast<int64_t>(size) + 16 * threads * 4 - 1) / (16 * threads * 4);
-  return static_cast<int>(pieces < 4096 ? (pieces < 1 ? 1 : pieces) : 4096);
+// Workgroups that zero `bytes`: enough to reach the write rate, few enough
+// that each has several stores.
+int zero_blocks(int64_t bytes, int threads) {
+  const int64_t pieces = (bytes + 64 * threads - 1) / (64 * threads);
+  return static_cast<int>(pieces < 4096 ? pieces : 4096);
 }
+// Workgroups to a group of rows that are zeroed, for 2048 in all.
+int zero_parts(int64_t groups) {
+  return groups <= 0 ? 1 : static_cast<int>(std::max<int64_t>(1, 2048 / groups));
+}
+// Bytes zeroed beside the sort: about what its time allows.
+constexpr int64_t kZeroWithRank = 32 << 20, kZeroWithRadix = 64 << 20;
 
-template <typename ID, typename TG>
-void run_sort(const void* ids_v, int64_t n, int64_t vocab, const EmbedWs& w, char* ws,
-              void* dtable, int64_t total, bool zero, hipStream_t s, int* cur_out) {
-  const ID* ids = static_cast<const ID*>(ids_v);
-  uint32_t* keys[2] = {reinterpret_cast<uint32_t*>(ws + w.keys[0]),
-                       reinterpret_cast<uint32_t*>(ws + w.keys[1])};
-  uint32_t* pos[2] = {reinterpret_cast<uint32_t*>(ws + w.pos[0]),
-                      reinterpret_cast<uint32_t*>(ws + w.pos[1])};
-  uint32_t* hist = reinterpret_cast<uint32_t*>(ws + w.hist);
-  const int all = key_bits(vocab);
-  const int passes = (all + kMaxBits - 1) / kMaxBits;
-  const int bits = (all + passes - 1) / passes;
-  TG* dt = static_cast<TG*>(dtable);
-  if (n <= kSmallN) {
-    const int zb = zero ? zero_blocks(total, sizeof(TG), kSmallThreads) : 0;
-    hipLaunchKernelGGL((k_sort_small<ID, TG>), dim3(1 + zb), dim3(kSmallThreads), 0, s, ids,
-                       static_cast<int>(n), vocab, bits, passes, keys[0], pos[0], dt, total);
-    *cur_out = 0;
+struct BackwardArgs {
+  const void *dout, *ids;
+  int64_t ld, n, vocab, dim;
+  float scale;
+  void* dtable;
+  int accumulate;
+  char* ws;
+};
+
+template <typename TD, typename TG, typename ID>
+void run_backward(const BackwardArgs& a, const EmbedWs& w, hipStream_t s) {
+  const ID* ids = static_cast<const ID*>(a.ids);
+  TG* dt = static_cast<TG*>(a.dtable);
+  const int64_t n = a.n, vocab = a.vocab;
+  if (n > 0 && n <= kDirectN) {
+    const int sum_blocks = static_cast<int>(n) * w.slices;
+    // groups of rows for the zeroing workgroups: 32, more for a table of very
+    // many rows; several workgroups to a group where there are few
+    const int64_t len = std::min<int64_t>(kDirectRows, ((vocab + 4095) / 4096 + 31) / 32 * 32);
+    const int64_t groups = a.accumulate ? 0 : (vocab + len - 1) / len;
+    const int parts = zero_parts(groups);
+    hipLaunchKernelGGL((k_embed_direct<TD, TG, ID>),
+                       dim3(static_cast<unsigned>(sum_blocks + groups * parts)), dim3(kSumThreads),
+                       0, s, static_cast<const TD*>(a.dout), a.ld, ids, static_cast<int>(n), vocab,
+                       a.dim, a.scale, a.accumulate, dt, sum_blocks, w.slices,
+                       static_cast<int>(len), parts);
     return;
   }
-  const int nb = static_cast<int>(w.blocks);
-  int cur = 0;
-  for (int p = 0; p < passes; ++p) {
-    const int shift = p * bits;
-    if (p == 0) {
-      const int zb = zero ? zero_blocks(total, sizeof(TG), kSortThreads) : 0;
-      hipLaunchKernelGGL((k_sort_hist<true, ID, TG>), dim3(nb + zb), dim3(kSortThreads), 0, s,
-                         ids, nullptr, n, vocab, shift, bits, nb, hist, dt, total);
-    } else {
-      hipLaunchKernelGGL((k_sort_hist<false, ID, TG>), dim3(nb), dim3(kSortThreads), 0, s, ids,
-                         keys[cur], n, vocab, shift, bits, nb, hist, dt, total);
-    }
-    hipLaunchKernelGGL(k_sort_scan, dim3(1), dim3(1024), 0, s, hist,
-                       static_cast<int64_t>(nb) << bits);
-    if (p == 0)
-      hipLaunchKernelGGL((k_sort_scatter<true, ID>), dim3(nb), dim3(kSortThreads), 0, s, ids,
-                         nullptr, nullptr, n, vocab, shift, bits, nb, hist, keys[cur ^ 1],
-                         pos[cur ^ 1]);
-    else
-      hipLaunchKernelGGL((k_sort_scatter<false, ID>), dim3(nb), dim3(kSortThreads), 0, s, ids,
-                         keys[cur], pos[cur], n, vocab, shift, bits, nb, hist, keys[cur ^ 1],
-                         pos[cur ^ 1]);
-    cur ^= 1;
+  // rows [0, zero_v0) are zeroed before the sums
+  const int64_t row_bytes = a.dim * static_cast<int64_t>(sizeof(TG));
+  int64_t zero_v0 = a.accumulate ? vocab : (n <= kRankN ? kZeroWithRank : kZeroWithRadix) / row_bytes;
+  if (zero_v0 > vocab || n == 0) zero_v0 = vocab;
+  const int64_t zero_n = a.accumulate ? 0 : zero_v0 * a.dim;
+  const int64_t zero_bytes = zero_n * static_cast<int64_t>(sizeof(TG));
+  if (n == 0) {
+    hipLaunchKernelGGL((k_sort_rank<ID, TG>), dim3(zero_blocks(zero_bytes, kRankThreads)),
+                       dim3(kRankThreads), 0, s, ids, 0, vocab, 0, nullptr, nullptr, dt, zero_n);
+    return;
   }
-  *cur_out = cur;
+  uint32_t* keys[2] = {reinterpret_cast<uint32_t*>(a.ws + w.keys[0]),
+                       reinterpret_cast<uint32_t*>(a.ws + w.keys[1])};
+  uint32_t* pos[2] = {reinterpret_cast<uint32_t*>(a.ws + w.pos[0]),
+                      reinterpret_cast<uint32_t*>(a.ws + w.pos[1])};
+  uint32_t* hist = reinterpret_cast<uint32_t*>(a.ws + w.hist);
+  int cur = 0;
+  if (n <= kRankN) {
+    const int rb = static_cast<int>((n + 63) / 64);
+    hipLaunchKernelGGL((k_sort_rank<ID, TG>), dim3(rb + zero_blocks(zero_bytes, kRankThreads)),
+                       dim3(kRankThreads), 0, s, ids, static_cast<int>(n), vocab, rb, keys[0],
+                       pos[0], dt, zero_n);
+  } else {
+    const int all = key_bits(vocab);
+    const int passes = (all + kMaxBits - 1) / kMaxBits;
+    const int bits = (all + passes - 1) / passes;
+    const dim3 grid(w.blocks), block(kSortThreads);
+    for (int p = 0; p < passes; ++p) {
+      const int shift = p * bits;
+      if (p == 0) {
+        hipLaunchKernelGGL((k_sort_hist<true, ID, TG>),
+                           dim3(w.blocks + zero_blocks(zero_bytes, kSortThreads)), block, 0, s, ids,
+                           nullptr, n, vocab, shift, bits, w.blocks, w.part, hist, dt, zero_n);
+        hipLaunchKernelGGL((k_sort_scatter<true, ID>), grid, block, 0, s, ids, nullptr, nullptr, n,
+                           vocab, shift, bits, w.blocks, w.part, hist, keys[1], pos[1]);
+      } else {
+        hipLaunchKernelGGL((k_sort_hist<false, ID, TG>), grid, block, 0, s, ids, keys[cur], n,
+                           vocab, shift, bits, w.blocks, w.part, hist, dt, int64_t{0});
+        hipLaunchKernelGGL((k_sort_scatter<false, ID>), grid, block, 0, s, ids, keys[cur],
+                           pos[cur], n, vocab, shift, bits, w.blocks, w.part, hist, keys[cur ^ 1],
+                           pos[cur ^ 1]);
+      }
+      cur ^= 1;
+    }
+  }
+  const int64_t sum_blocks = w.chunks * w.slices;
+  const int64_t groups = (vocab - zero_v0 + 31) / 32;
+  const int zparts = zero_parts(groups);
+  const int64_t zb = std::min<int64_t>(groups, 4096) * zparts;
+  float* parts = reinterpret_cast<float*>(a.ws + w.parts);
+  hipLaunchKernelGGL((k_embed_runs<TD, TG>), dim3(static_cast<unsigned>(sum_blocks + zb)),
+                     dim3(kSumThreads), 0, s, static_cast<const TD*>(a.dout), a.ld, keys[cur],
+                     pos[cur], n, vocab, a.dim, w.dim_p, w.chunk_len, a.scale, a.accumulate, dt,
+                     parts, sum_blocks, w.slices, zero_v0, zparts);
+  if (w.chunks > 1)
+    hipLaunchKernelGGL(k_embed_join<TG>, dim3(static_cast<unsigned>(sum_blocks)),
+                       dim3(kSumThreads), 0, s, keys[cur], n, vocab, a.dim, w.dim_p, w.chunk_len,
+                       a.scale, a.accumulate, dt, parts, w.slices);
 }
 
-template <typename TG>
-void run_sums(const void* dout, int32_t dout_dtype, int64_t ld, const uint32_t* keys,
-              const uint32_t* pos, int64_t n, int64_t vocab, int64_t dim, const EmbedWs& w,
-              float scale, int accumulate, void* dtable, float* parts, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(w.chunks),
-                  static_cast<unsigned>((dim + kCols - 1) / kCols));
-  TG* dt = static_cast<TG*>(dtable);
-  if (dout_dtype == MUON_DTYPE_BF16)
-    hipLaunchKernelGGL((k_embed_runs<uint16_t, TG>), grid, dim3(kThreads), 0, s,
-                       static_cast<const uint16_t*>(dout), ld, keys, pos, n, vocab, dim, w.dim_p,
-                       scale, accumulate, dt, parts);
-  else
-    hipLaunchKernelGGL((k_embed_runs<float, TG>), grid, dim3(kThreads), 0, s,
-                       static_cast<const float*>(dout), ld, keys, pos, n, vocab, dim, w.dim_p,
-                       scale, accumulate, dt, parts);
-  if (w.chunks > 1)
-    hipLaunchKernelGGL(k_embed_join<TG>, grid, dim3(kThreads), 0, s, keys, n, w.chunks, vocab,
-                       dim, w.dim_p, scale, accumulate, dt, parts);
+template <typename TD, typename TG>
+void run_backward(const BackwardArgs& a, const EmbedWs& w, bool ids_64, hipStream_t s) {
+  if (ids_64) run_backward<TD, TG, int64_t>(a, w, s);
+  else run_backward<TD, TG, int32_t>(a, w, s);
 }
 
 }  // namespace
@@ -652,27 +810,13 @@ int embed_backward(const void* dout, int32_t dout_dtype, int64_t ld_dout, const 
     return set_error(MUON_ERR_WORKSPACE_TOO_SMALL,
                      "embed_backward needs " + std::to_string(w.total) +
                          " bytes of workspace, 256-byte aligned");
-  char* ws = static_cast<char*>(workspace);
-  const int64_t total = vocab * dim;
-  const bool gb = dtable_dtype == MUON_DTYPE_BF16;
-  int cur = 0;
-  const bool zero = accumulate == 0;
-  if (ids_64) {
-    if (gb) run_sort<int64_t, uint16_t>(ids, n, vocab, w, ws, dtable, total, zero, stream, &cur);
-    else run_sort<int64_t, float>(ids, n, vocab, w, ws, dtable, total, zero, stream, &cur);
-  } else {
-    if (gb) run_sort<int32_t, uint16_t>(ids, n, vocab, w, ws, dtable, total, zero, stream, &cur);
-    else run_sort<int32_t, float>(ids, n, vocab, w, ws, dtable, total, zero, stream, &cur);
-  }
-  if (n > 0) {
-    const uint32_t* keys = reinterpret_cast<const uint32_t*>(ws + w.keys[cur]);
-    const uint32_t* pos = reinterpret_cast<const uint32_t*>(ws + w.pos[cur]);
-    float* parts = reinterpret_cast<float*>(ws + w.parts);
-    if (gb) run_sums<uint16_t>(dout, dout_dtype, ld_dout, keys, pos, n, vocab, dim, w, scale,
-                               accumulate, dtable, parts, stream);
-    else run_sums<float>(dout, dout_dtype, ld_dout, keys, pos, n, vocab, dim, w, scale,
-                         accumulate, dtable, parts, stream);
-  }
+  const BackwardArgs a{dout, ids, ld_dout, n, vocab, dim, scale, dtable, accumulate != 0,
+                       static_cast<char*>(workspace)};
+  const bool db = dout_dtype == MUON_DTYPE_BF16, gb = dtable_dtype == MUON_DTYPE_BF16;
+  if (db && gb) run_backward<uint16_t, uint16_t>(a, w, ids_64 != 0, stream);
+  else if (db) run_backward<uint16_t, float>(a, w, ids_64 != 0, stream);
+  else if (gb) run_backward<float, uint16_t>(a, w, ids_64 != 0, stream);
+  else run_backward<float, float>(a, w, ids_64 != 0, stream);
   return check_launch("embedding gradient launch");
 }
 

@@ -127,12 +127,31 @@ void launch_wgrad(const WgradArgs& g, hipStream_t s) {
                      dim3(kThreads), 0, s, g, nx, ny);
 }
 
+// Row tiles of the groups, whose sizes the host does not know: rows spread
+// evenly, and half a tile lost at each group's end.
+double group_tiles(int rows, int experts, int bm) {
+  const double groups = std::min(rows, experts), r = rows / groups;
+  return groups * (r <= bm ? 1.0 : r / bm + 0.5);
+}
+
+template <bool QKS, typename TO>
+void run_matmul_grid(const MatmulArgs& a, hipStream_t s) {
+  const Shape shape = pick_shape(QKS ? kShapeNN : kShapeNT, [&](int bm) {
+    return group_tiles(a.rows, a.experts, bm);
+  }, a.N, a.K);
+  using T = uint16_t;
+  if (shape == kLarge) launch_matmul<LargeCore<false, QKS>, T, QKS, TO>(a, s);
+  else if (shape == kHalf) launch_matmul<HalfCore<false, QKS>, T, QKS, TO>(a, s);
+  else if (shape == kMedium) launch_matmul<MediumCore<false, QKS>, T, QKS, TO>(a, s);
+  else launch_matmul<ThinCore<false, QKS>, T, QKS, TO>(a, s);
+}
+
 template <typename T, typename TO>
 void run_matmul(const MatmulArgs& a, bool trans, hipStream_t s) {
   if constexpr (sizeof(T) == 2) {
     if (on_grid(a.x, a.ldx, a.K) && on_grid(a.w, a.N, a.K) && on_grid(a.y, a.ldy, a.N)) {
-      if (trans) launch_matmul<DmaCore<false, false, 256, 256, 2, 32, 4>, T, false, TO>(a, s);
-      else launch_matmul<DmaCore<false, true, 256, 256, 2, 32, 4>, T, true, TO>(a, s);
+      if (trans) run_matmul_grid<false, TO>(a, s);
+      else run_matmul_grid<true, TO>(a, s);
       return;
     }
   }
@@ -144,7 +163,12 @@ template <typename T, typename TO>
 void run_wgrad(const WgradArgs& g, hipStream_t s) {
   if constexpr (sizeof(T) == 2) {
     if (on_grid(g.a, g.lda, g.M) && on_grid(g.b, g.ldb, g.N) && on_grid(g.dw, g.N, g.M)) {
-      launch_wgrad<DmaCore<true, true, 256, 256, 2, 32, 4>, T, TO>(g, s);
+      const Shape shape = pick_shape(kShapeTN, [&](int bm) {
+        return static_cast<double>(g.experts) * ((g.M + bm - 1) / bm);
+      }, g.N, g.rows / g.experts);
+      if (shape == kLarge) launch_wgrad<LargeCore<true, true>, T, TO>(g, s);
+      else if (shape == kHalf) launch_wgrad<HalfCore<true, true>, T, TO>(g, s);
+      else launch_wgrad<MediumCore<true, true>, T, TO>(g, s);
       return;
     }
   }

@@ -83,37 +83,51 @@ __global__ __launch_bounds__(kThreads, Core::kWaves) void k_loss_stats(StatsArgs
   float* red = reinterpret_cast<float*>(Core::lds());  // [WN][BM][2]
   static_assert(Core::WN * Core::BM * 8 <= Core::kLdsBytes, "the waves' row statistics");
   __syncthreads();
+  // EDGE: the vocabulary ends inside the tile (the test stays out of the
+  // loops of the other tiles)
+  auto rows = [&](auto edge_c) {
+    constexpr bool EDGE = decltype(edge_c)::value;
 #pragma unroll
-  for (int bi = 0; bi < Core::MI; ++bi) {
-    const int i = wi * 32 * Core::MI + 32 * bi + (lane & 31);
-    const int64_t t = static_cast<int64_t>(i0) + i;
-    const bool row = t < a.n;
-    const int64_t tgt = row ? target_of(a.targets, a.t64, t, a.vocab) : -1;
-    float m = -INFINITY;
+    for (int bi = 0; bi < Core::MI; ++bi) {
+      const int i = wi * 32 * Core::MI + 32 * bi + (lane & 31);
+      const int64_t t = static_cast<int64_t>(i0) + i;
+      const int64_t tgt = t < a.n ? target_of(a.targets, a.t64, t, a.vocab) : -1;
+      // few lanes hold their row's target
+      const int64_t at64 = tgt - v0 - jw;
+      const int at = tgt >= 0 && at64 >= 0 && at64 < 32 * Core::NJ ? static_cast<int>(at64) : -1;
+      if (__ballot(at >= 0) != 0) {
 #pragma unroll
-    for (int bj = 0; bj < Core::NJ; ++bj)
+        for (int bj = 0; bj < Core::NJ; ++bj)
 #pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const int j = jw + 32 * bj + 8 * (v >> 2) + (v & 3);
-        if (j < jn) m = fmaxf(m, acc[bj][bi][v]);
-        if (tgt == v0 + j) a.at[t] = acc[bj][bi][v];
+          for (int v = 0; v < 16; ++v)
+            if (at == 32 * bj + 8 * (v >> 2) + (v & 3)) a.at[t] = acc[bj][bi][v];
       }
-    float s = 0.0f;
+      float m = -INFINITY;
 #pragma unroll
-    for (int bj = 0; bj < Core::NJ; ++bj)
+      for (int bj = 0; bj < Core::NJ; ++bj)
 #pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const int j = jw + 32 * bj + 8 * (v >> 2) + (v & 3);
-        const float x = acc[bj][bi][v];
-        if (j < jn && x != -INFINITY) s += exp_of<T>(x - m);
+        for (int v = 0; v < 16; ++v)
+          if (!EDGE || jw + 32 * bj + 8 * (v >> 2) + (v & 3) < jn) m = fmaxf(m, acc[bj][bi][v]);
+      // nothing above -inf: every term is exp(-inf) = 0
+      const float ms = m == -INFINITY ? 0.0f : m;
+      float s = 0.0f;
+#pragma unroll
+      for (int bj = 0; bj < Core::NJ; ++bj)
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+          if (!EDGE || jw + 32 * bj + 8 * (v >> 2) + (v & 3) < jn)
+            s += exp_of<T>(acc[bj][bi][v] - ms);
+      const float m2 = __shfl_xor(m, 32, 64), s2 = __shfl_xor(s, 32, 64);
+      if (lane < 32) {
+        join_stats(m, s, m2, s2);
+        red[(wj * Core::BM + i) * 2] = m;
+        red[(wj * Core::BM + i) * 2 + 1] = s;
       }
-    const float m2 = __shfl_xor(m, 32, 64), s2 = __shfl_xor(s, 32, 64);
-    if (lane < 32) {
-      join_stats(m, s, m2, s2);
-      red[(wj * Core::BM + i) * 2] = m;
-      red[(wj * Core::BM + i) * 2 + 1] = s;
+      __builtin_amdgcn_sched_barrier(0);  // one block of rows at a time: fewer live values
     }
-  }
+  };
+  if (jn < Core::BN) rows(std::true_type{});
+  else rows(std::false_type{});
   __syncthreads();
   for (int i = threadIdx.x; i < Core::BM && i0 + i < a.n; i += kThreads) {
     float m = red[2 * i], s = red[2 * i + 1];
@@ -126,28 +140,41 @@ __global__ __launch_bounds__(kThreads, Core::kWaves) void k_loss_stats(StatsArgs
   }
 }
 
-// Joins a row's tiles: lane l of the wave takes tiles l, l + 64, ... in
-// order, then the lanes are joined in a fixed tree.
+// Joins a row's tiles in a fixed order: thread (r, p) of a workgroup takes
+// tiles p, p + P, ... of row r, R rows x P parts, then the parts are joined in
+// order.  Rows run along the lanes, so loads of many rows are whole lines; few
+// rows take more parts.
+template <int R>
 __global__ __launch_bounds__(kThreads) void k_loss_join(const float* __restrict__ tile_m,
                                                         const float* __restrict__ tile_s,
                                                         const float* __restrict__ at, int tiles,
                                                         int n, const void* targets, int t64,
                                                         int64_t vocab, float* __restrict__ loss,
                                                         float* __restrict__ lse) {
-  // 64 rows x 4 parts of the tiles, so that loads run along rows
-  __shared__ float red[4][64][2];
-  const int r = threadIdx.x & 63, part = threadIdx.x >> 6;
-  const int t = blockIdx.x * 64 + r;
+  constexpr int P = kThreads / R;
+  __shared__ float red[P][R][2];
+  const int r = threadIdx.x % R, part = threadIdx.x / R;
+  const int t = blockIdx.x * R + r;
   float m = -INFINITY, s = 0.0f;
-  if (t < n)
-    for (int k = part; k < tiles; k += 4)
-      join_stats(m, s, tile_m[static_cast<int64_t>(k) * n + t],
-                 tile_s[static_cast<int64_t>(k) * n + t]);
+  if (t < n) {
+    constexpr int U = 8;
+    for (int k0 = part; k0 < tiles; k0 += U * P) {
+      float tm[U], ts[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int k = k0 + u * P;
+        tm[u] = k < tiles ? tile_m[static_cast<int64_t>(k) * n + t] : -INFINITY;
+        ts[u] = k < tiles ? tile_s[static_cast<int64_t>(k) * n + t] : 0.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) join_stats(m, s, tm[u], ts[u]);
+    }
+  }
   red[part][r][0] = m;
   red[part][r][1] = s;
   __syncthreads();
   if (part != 0 || t >= n) return;
-  for (int p = 1; p < 4; ++p) join_stats(m, s, red[p][r][0], red[p][r][1]);
+  for (int p = 1; p < P; ++p) join_stats(m, s, red[p][r][0], red[p][r][1]);
   const float l = m + logf(s);
   lse[t] = l;
   loss[t] = target_of(targets, t64, t, vocab) >= 0 ? l - at[t] : 0.0f;
@@ -193,18 +220,22 @@ __global__ __launch_bounds__(kThreads, Core::kWaves) void k_loss_g(GradArgs a, i
   // grid the columns from the piece's end to ldg are stored as zeros, which
   // the sums over the vocabulary read.
   const int jw = (wave / Core::WM) * 32 * Core::NJ + 4 * (lane >> 5);
+  const int len = a.len - j0 - jw;
 #pragma unroll
   for (int bi = 0; bi < Core::MI; ++bi) {
-    const int64_t at = tgt[bi] - a.v0 - j0 - jw;  // the target's column from this lane's first
-    const int left = tgt[bi] < 0 ? 0 : a.len - j0 - jw;
+    const bool row = tgt[bi] >= 0;
+    const int64_t at64 = tgt[bi] - a.v0 - j0 - jw;
+    const int at = row && at64 >= 0 && at64 < 32 * Core::NJ ? static_cast<int>(at64) : -1;
+    const int left = row ? len : 0;
 #pragma unroll
     for (int bj = 0; bj < Core::NJ; ++bj)
 #pragma unroll
       for (int v = 0; v < 16; ++v) {
-        const float p = exp_of<T>(acc[bj][bi][v] - lse[bi]);
         const int j = 32 * bj + 8 * (v >> 2) + (v & 3);
+        const float p = exp_of<T>(acc[bj][bi][v] - lse[bi]);
         acc[bj][bi][v] = j < left ? (at == j ? p - 1.0f : p) * dl[bi] : 0.0f;
       }
+    __builtin_amdgcn_sched_barrier(0);
   }
   Core::write(acc, static_cast<T*>(a.g) + i0 * a.ldg + j0, a.ldg, static_cast<const T*>(nullptr),
               0, a.n - i0, Core::kGrid ? static_cast<int>(a.ldg) - j0 : a.len - j0);
@@ -297,6 +328,14 @@ constexpr int64_t kMinPiece = 2048;
 constexpr int kMaxSplits = 16;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+auto row_tiles(int64_t rows) {
+  return [rows](int bm) { return static_cast<double>(ceil_div(rows, bm)); };
+}
+// dh: `splits` times the tiles, each with its share of the sum
+Shape dh_shape(int64_t n, int64_t dim, int splits, int64_t len) {
+  return pick_shape(kShapeNN, [&](int bm) { return static_cast<double>(ceil_div(n, bm) * splits); },
+                    dim, ceil_div(len, splits));
+}
 
 struct LossWs {
   int64_t stats_rows, v_tiles;          // forward
@@ -357,7 +396,13 @@ int launch_stats(const StatsArgs& a, hipStream_t s) {
 template <typename T>
 int run_stats(const StatsArgs& a, bool grid, hipStream_t s) {
   if constexpr (sizeof(T) == 2) {
-    if (grid) return launch_stats<DmaCore<false, false, 256, 256, 2, 32, 4>, T>(a, s);
+    if (grid) {
+      const Shape shape = pick_shape(kShapeNT, row_tiles(a.n), a.vocab, a.dim);
+      if (shape == kLarge) return launch_stats<LargeCore<false, false>, T>(a, s);
+      if (shape == kHalf) return launch_stats<HalfCore<false, false>, T>(a, s);
+      if (shape == kMedium) return launch_stats<MediumCore<false, false>, T>(a, s);
+      return launch_stats<ThinCore<false, false>, T>(a, s);
+    }
   }
   return launch_stats<AnyCore<T, false, false>, T>(a, s);
 }
@@ -372,7 +417,13 @@ void launch_g(const GradArgs& a, hipStream_t s) {
 template <typename T>
 void run_g(const GradArgs& a, bool grid, hipStream_t s) {
   if constexpr (sizeof(T) == 2) {
-    if (grid) return launch_g<DmaCore<false, false, 256, 256, 2, 32, 4>, T>(a, s);
+    if (grid) {
+      const Shape shape = pick_shape(kShapeNT, row_tiles(a.n), a.len, a.dim);
+      if (shape == kLarge) return launch_g<LargeCore<false, false>, T>(a, s);
+      if (shape == kHalf) return launch_g<HalfCore<false, false>, T>(a, s);
+      if (shape == kMedium) return launch_g<MediumCore<false, false>, T>(a, s);
+      return launch_g<ThinCore<false, false>, T>(a, s);
+    }
   }
   launch_g<AnyCore<T, false, false>, T>(a, s);
 }
@@ -388,7 +439,13 @@ void launch_dh(const DhArgs& a, hipStream_t s) {
 template <typename T, typename TO>
 void run_dh(const DhArgs& a, bool grid, hipStream_t s) {
   if constexpr (sizeof(T) == 2) {
-    if (grid) return launch_dh<DmaCore<false, true, 256, 256, 2, 32, 4>, T, TO>(a, s);
+    if (grid) {
+      const Shape shape = dh_shape(a.n, a.dim, a.splits, a.len);
+      if (shape == kLarge) return launch_dh<LargeCore<false, true>, T, TO>(a, s);
+      if (shape == kHalf) return launch_dh<HalfCore<false, true>, T, TO>(a, s);
+      if (shape == kMedium) return launch_dh<MediumCore<false, true>, T, TO>(a, s);
+      return launch_dh<ThinCore<false, true>, T, TO>(a, s);
+    }
   }
   launch_dh<AnyCore<T, false, true>, T, TO>(a, s);
 }
@@ -403,7 +460,12 @@ void launch_dw(const DwArgs& a, hipStream_t s) {
 template <typename T, typename TO>
 void run_dw(const DwArgs& a, bool grid, hipStream_t s) {
   if constexpr (sizeof(T) == 2) {
-    if (grid) return launch_dw<DmaCore<true, true, 256, 256, 2, 32, 4>, T, TO>(a, s);
+    if (grid) {
+      const Shape shape = pick_shape(kShapeTN, row_tiles(a.len), a.dim, a.n);
+      if (shape == kLarge) return launch_dw<LargeCore<true, true>, T, TO>(a, s);
+      if (shape == kHalf) return launch_dw<HalfCore<true, true>, T, TO>(a, s);
+      return launch_dw<MediumCore<true, true>, T, TO>(a, s);
+    }
   }
   launch_dw<AnyCore<T, true, true>, T, TO>(a, s);
 }
@@ -506,9 +568,10 @@ int lm_loss_forward(const void* hidden, int64_t ld_hidden, const void* weight, i
     const bool grid = on_grid(a.h, ld_hidden, dim) && on_grid(weight, dim, dim);
     const int v_tiles = static_cast<int>(dtype == MUON_DTYPE_BF16 ? run_stats<uint16_t>(a, grid, stream)
                                                                  : run_stats<float>(a, grid, stream));
-    hipLaunchKernelGGL(k_loss_join, dim3(static_cast<unsigned>(ceil_div(rows, 64))),
-                       dim3(kThreads), 0, stream, tm, ts, at, v_tiles, rows,
-                       tg, targets_64 != 0, vocab, loss + r0, lse + r0);
+    // 16 rows a workgroup: 16 parts, and enough workgroups from 4096 rows on
+    hipLaunchKernelGGL(k_loss_join<16>, dim3(static_cast<unsigned>(ceil_div(rows, 16))),
+                       dim3(kThreads), 0, stream, tm, ts, at, v_tiles, rows, tg, targets_64 != 0,
+                       vocab, loss + r0, lse + r0);
   }
   return check_launch("vocabulary loss launch");
 }

@@ -65,13 +65,13 @@ inline size_t train_dtype_size(int32_t d) { return d == MUON_DTYPE_FP32 ? 4 : 2;
 // position at most) stay below 2^32.
 constexpr int64_t kMaxTokens = (static_cast<int64_t>(1) << 26) - 1;
 constexpr int64_t kMaxVocab = (static_cast<int64_t>(1) << 31) - 2;
-constexpr int64_t kMaxDim = static_cast<int64_t>(1) << 24;
+constexpr int64_t kMaxDim = static_cast<int64_t>(1) << 22;
 
 inline int check_token_sizes(int64_t n, int64_t vocab, int64_t dim) {
   if (n < 0 || n > kMaxTokens) return set_error(MUON_ERR_BAD_SHAPE, "n must be in [0, 2^26)");
   if (vocab < 1 || vocab > kMaxVocab)
     return set_error(MUON_ERR_BAD_SHAPE, "vocab must be in [1, 2^31 - 2]");
-  if (dim < 1 || dim > kMaxDim) return set_error(MUON_ERR_BAD_SHAPE, "dim must be in [1, 2^24]");
+  if (dim < 1 || dim > kMaxDim) return set_error(MUON_ERR_BAD_SHAPE, "dim must be in [1, 2^22]");
   return MUON_OK;
 }
 // On the 16-byte grid, for every type: base, row stride and row length.  The

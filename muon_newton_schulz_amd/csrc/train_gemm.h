@@ -15,6 +15,7 @@
 // so a lane holds four consecutive columns of one row.
 #pragma once
 
+#include <cmath>
 #include <type_traits>
 
 #include "train_common.h"
@@ -460,9 +461,10 @@ struct DmaCore {
     // is outstanding; behind the barrier, everybody's has
     constexpr int DPS = NP + NQ;
     auto landed = [&](int newer) {
-      if (NS > 3 && newer >= 2) wait_counts<2 * DPS>();
-      else if (NS > 2 && newer >= 1) wait_counts<DPS>();
-      else wait_counts<0>();
+      static_for<0, NS - 1>([&](auto i_c) {
+        constexpr int i = decltype(i_c)::value;
+        if (i == NS - 2 ? newer >= i : i == 0 ? newer <= 0 : newer == i) wait_counts<i * DPS>();
+      });
     };
 
     __syncthreads();  // the slots are free (a tile before this one, an epilogue)
@@ -563,12 +565,18 @@ struct DmaCore {
     else rows_out<TO, TA, false>(acc, C, ldc, add, lda, rows, cols);
   }
 
+  // Bytes of a staged row: up to 256, as many as leave each wave a region.
+  static constexpr int stage_row(int bytes) {
+    int rb = bytes < 256 ? bytes : 256;
+    while (kSlotBytes / (32 * MI * rb) * NS < 4) rb /= 2;
+    return rb;
+  }
   // HALF: staged as bf16, else as fp32
   template <typename TO, typename TA, bool HALF>
   static __device__ __forceinline__ void rows_out(f32x16_t (&acc)[NJ][MI], TO* C, int64_t ldc,
                                                   const TA* add, int64_t lda, int rows, int cols) {
     constexpr int ES = HALF ? 2 : 4;
-    constexpr int RB = NJ * 32 * ES < 256 ? NJ * 32 * ES : 256;  // bytes of a staged row
+    constexpr int RB = stage_row(NJ * 32 * ES);                  // bytes of a staged row
     constexpr int CW = RB / ES, JB = CW / 32;                    // its columns, blocks of 32
     constexpr int NCH = RB / 16, SH = NCH == 16 ? 0 : NCH == 8 ? 1 : 2;
     constexpr int REGION = 32 * MI * RB, PER = kSlotBytes / REGION;
@@ -635,5 +643,65 @@ struct DmaCore {
     }
   }
 };
+
+// The tile shapes.  Large: the least operand traffic for a flop (512 rows and
+// columns of operands for 256 x 256 results), one workgroup to a CU, so
+// nothing hides its prologue and epilogue.  Half and Medium: two workgroups
+// to a CU.  Thin: a deep ring for streaming Q past a few rows of P.
+// K-contiguous operands take 64 k a stage, whole 128-byte lines; K-strided
+// ones always read whole lines and take 32, which doubles the stages in
+// flight.  Large NN (one of each) measured 2323 us with 32 k and 2473 with
+// 64 (65536 rows, 128 experts of 7168 x 2048).
+template <bool PKS, bool QKS>
+using LargeCore = DmaCore<PKS, QKS, 256, 256, 2, (PKS || QKS) ? 32 : 64, (PKS || QKS) ? 4 : 2>;
+template <bool PKS, bool QKS>
+using HalfCore = DmaCore<PKS, QKS, 128, 256, 2, 32, 3>;
+template <bool PKS, bool QKS>
+using MediumCore = DmaCore<PKS, QKS, 128, 128, 2, 64, 2>;
+template <bool PKS, bool QKS>
+using ThinCore = DmaCore<PKS, QKS, 32, 128, 1, 64, 6>;
+
+// Which of them: the least estimated time on 256 CUs.  A workgroup's time is
+// stage x K / 64 + fixed microseconds, as many share a CU as fit it; tiles
+// beyond one a place take their share of a round more, and the last round
+// is on average partly empty.  The constants are fits to measured products
+// (8 to 65536 rows, 8 to 128 experts, sides 1024 to 7168): the estimate
+// ranks the shapes right or within 10% there.
+struct ShapeCost {
+  int bm, bn, per_cu;
+  double stage, fixed;
+};
+inline double shape_time(const ShapeCost& c, double row_tiles, int64_t cols, int64_t k) {
+  const double tiles = row_tiles * static_cast<double>((cols + c.bn - 1) / c.bn);
+  double stage = c.stage, rounds = 1.0;
+  if (tiles <= 256.0) {
+    stage /= c.per_cu;  // alone on its CU
+  } else if (tiles > 256.0 * c.per_cu) {
+    const double r = tiles / (256.0 * c.per_cu);
+    rounds = r < 8.0 ? std::ceil(r) : r + 0.5;
+  }
+  return rounds * (static_cast<double>(k) / 64.0 * stage + c.fixed);
+}
+enum Shape { kLarge, kHalf, kMedium, kThin };
+constexpr ShapeCost kShapeNT[] = {{256, 256, 1, 1.75, 11.0}, {128, 256, 2, 2.45, 4.0},
+                                  {128, 128, 2, 1.13, 3.0}, {32, 128, 1, 0.70, 2.0}};
+constexpr ShapeCost kShapeNN[] = {{256, 256, 1, 1.79, 12.0}, {128, 256, 2, 2.15, 3.0},
+                                  {128, 128, 2, 1.13, 3.0}, {32, 128, 1, 0.70, 2.0}};
+constexpr ShapeCost kShapeTN[] = {{256, 256, 1, 1.65, 9.0}, {128, 256, 2, 2.10, 4.2},
+                                  {128, 128, 2, 1.10, 3.2}};
+// rows(bm): row tiles of bm rows
+template <int N, typename R>
+Shape pick_shape(const ShapeCost (&c)[N], R&& rows, int64_t cols, int64_t k) {
+  int best = 0;
+  double t = 0.0;
+  for (int i = 0; i < N; ++i) {
+    const double e = shape_time(c[i], rows(c[i].bm), cols, k);
+    if (i == 0 || e < t) {
+      best = i;
+      t = e;
+    }
+  }
+  return static_cast<Shape>(best);
+}
 
 }  // namespace muon

@@ -103,6 +103,12 @@ def test_lookup_of_non_finite_rows_and_offsets_past_32_bits(gpu):
     (20000, 512, 64, "bf16", "bf16", torch.int32, "uniform", False, 0, 0),
     (12289, 511, 40, "bf16", "bf16", torch.int64, "uniform", False, 5, 0),
     (30000, 300000, 24, "bf16", "fp32", torch.int64, "uniform", False, 0, 0),
+    (1500, 300000, 24, "bf16", "fp32", torch.int64, "uniform", False, 1, 0),
+    (2048, 40, 1032, "bf16", "bf16", torch.int32, "zipf", False, 0, 0),
+    (2049, 700, 520, "bf16", "bf16", torch.int32, "zipf", True, 0, 0),
+    (16384, 32000, 72, "bf16", "bf16", torch.int64, "zipf", False, 0, 0),
+    (16385, 163840, 8, "fp32", "bf16", torch.int64, "uniform", False, 0, 0),
+    (70000, 1000003, 16, "bf16", "bf16", torch.int64, "zipf", False, 0, 0),
     (9000, 5, 2056, "bf16", "bf16", torch.int64, "same", False, 0, 8),
 ])
 def test_gradient(gpu, n, vocab, dim, dd, gd, idt, kind, acc, off, pad):
