@@ -23,12 +23,13 @@ __device__ __forceinline__ void group_rows(const int32_t* off, int e, int rows, 
 }
 
 struct RowTile {
-  int e, lo, n, tile;  // expert, its first row and row count, tile within it; e < 0: none
+  int e, lo, n, tile;  // expert, its first row and row count, tile within it
 };
-// The t-th row tile of the grouped list, each group cut into tiles of bm
-// rows.  Every wave scans the offsets, 64 experts at a time.
-__device__ __forceinline__ RowTile find_row_tile(const int32_t* off, int experts, int rows, int bm,
-                                                 int t) {
+// Row tiles of all groups, each cut into tiles of bm rows; with find also the
+// t-th of them.  Every wave scans the offsets, 64 experts at a time.
+template <bool FIND>
+__device__ __forceinline__ int scan_row_tiles(const int32_t* off, int experts, int rows, int bm,
+                                              int t, RowTile* out) {
   const int lane = threadIdx.x & 63;
   int base = 0;
   for (int e0 = 0; e0 < experts; e0 += 64) {
@@ -41,15 +42,21 @@ __device__ __forceinline__ RowTile find_row_tile(const int32_t* off, int experts
       const int u = __shfl_up(s, o, 64);
       if (lane >= o) s += u;
     }
-    const uint64_t over = __ballot(base + s > t);
-    if (over != 0) {
-      const int l = __ffsll(static_cast<unsigned long long>(over)) - 1;
-      return RowTile{e0 + l, __shfl(lo, l, 64), __shfl(n, l, 64),
-                     t - base - __shfl(s - tiles, l, 64)};
+    if constexpr (FIND) {
+      const uint64_t over = __ballot(base + s > t);
+      if (over != 0) {
+        // uniform values, in scalar registers
+        const int l = __ffsll(static_cast<unsigned long long>(over)) - 1;
+        out->e = e0 + l;
+        out->lo = __builtin_amdgcn_readlane(lo, l);
+        out->n = __builtin_amdgcn_readlane(n, l);
+        out->tile = t - base - __builtin_amdgcn_readlane(s - tiles, l);
+        return 0;
+      }
     }
-    base += __shfl(s, 63, 64);
+    base += __builtin_amdgcn_readlane(s, 63);
   }
-  return RowTile{-1, 0, 0, 0};
+  return base;
 }
 
 struct MatmulArgs {
@@ -61,23 +68,38 @@ struct MatmulArgs {
   int experts, rows, K, N;
 };
 
-// QKS: W_e is [K][N] (y = x W_e); else [N][K] (y = x W_e^T).
+// QKS: W_e is [K][N] (y = x W_e); else [N][K] (y = x W_e^T).  The launch has
+// as many workgroups as any sizes can need; they share the tiles that the
+// offsets give.
+template <typename T>
+struct MatmulTile : TileArgs<T> {
+  int64_t row0;
+  int j0;
+};
 template <typename Core, typename T, bool QKS, typename TO>
-__global__ __launch_bounds__(kThreads, Core::kWaves) void k_expert_matmul(MatmulArgs a, int nx,
-                                                                        int ny) {
+__global__ __launch_bounds__(kThreads, Core::kWaves) void k_expert_matmul(MatmulArgs a, int ny) {
+  using W = MatmulTile<T>;
+  const int nx = scan_row_tiles<false>(a.off, a.experts, a.rows, Core::BM, 0, nullptr);
   int x, y;
-  if (!tile_of(blockIdx.x, nx, ny, x, y)) return;
-  const RowTile rt = find_row_tile(a.off, a.experts, a.rows, Core::BM, x);
-  if (rt.e < 0) return;
-  const int i0 = rt.tile * Core::BM, j0 = y * Core::BN;
-  const int64_t row0 = static_cast<int64_t>(rt.lo) + i0;
-  const T* P = static_cast<const T*>(a.x) + row0 * a.ldx;
-  const T* W = static_cast<const T*>(a.w) + static_cast<int64_t>(rt.e) * a.K * a.N;
+  if (!my_tile(nx, ny, x, y)) return;
+  W w;
+  RowTile rt;
+  scan_row_tiles<true>(a.off, a.experts, a.rows, Core::BM, x, &rt);
+  const int i0 = rt.tile * Core::BM;
+  w.j0 = y * Core::BN;
+  w.row0 = static_cast<int64_t>(rt.lo) + i0;
+  w.P = static_cast<const T*>(a.x) + w.row0 * a.ldx;
+  w.ldp = a.ldx;
+  w.pn = rt.n - i0;
+  w.Q = static_cast<const T*>(a.w) + static_cast<int64_t>(rt.e) * a.K * a.N +
+        (QKS ? w.j0 : static_cast<int64_t>(w.j0) * a.K);
+  w.ldq = QKS ? a.N : a.K;
+  w.qn = a.N - w.j0;
+  w.K = a.K;
   f32x16_t acc[Core::NJ][Core::MI];
-  if (QKS) Core::run(P, a.ldx, rt.n - i0, W + j0, a.N, a.N - j0, a.K, acc);
-  else Core::run(P, a.ldx, rt.n - i0, W + static_cast<int64_t>(j0) * a.K, a.K, a.N - j0, a.K, acc);
-  TO* Y = static_cast<TO*>(a.y) + row0 * a.ldy + j0;
-  Core::write(acc, Y, a.ldy, static_cast<const TO*>(nullptr), 0, rt.n - i0, a.N - j0);
+  Core::run(w, acc);
+  Core::write(acc, static_cast<TO*>(a.y) + w.row0 * a.ldy + w.j0, a.ldy,
+              static_cast<const TO*>(nullptr), 0, w.pn, w.qn);
 }
 
 struct WgradArgs {
@@ -89,22 +111,34 @@ struct WgradArgs {
   int experts, rows, M, N, accumulate;
 };
 
+template <typename T>
+struct WgradTile : TileArgs<T> {
+  int64_t out;
+};
 template <typename Core, typename T, typename TO>
 __global__ __launch_bounds__(kThreads, Core::kWaves) void k_expert_wgrad(WgradArgs g, int nx,
                                                                        int ny) {
+  using W = WgradTile<T>;
   int x, y;
-  if (!tile_of(blockIdx.x, static_cast<int64_t>(nx) * g.experts, ny, x, y)) return;
+  if (!my_tile(static_cast<int64_t>(nx) * g.experts, ny, x, y)) return;
+  W w;
   const int e = x / nx, i0 = x % nx * Core::BM, j0 = y * Core::BN;
   int lo, n;
   group_rows(g.off, e, g.rows, lo, n);
   if (n == 0 && g.accumulate) return;
+  w.P = static_cast<const T*>(g.a) + lo * g.lda + i0;
+  w.ldp = g.lda;
+  w.pn = g.M - i0;
+  w.Q = static_cast<const T*>(g.b) + lo * g.ldb + j0;
+  w.ldq = g.ldb;
+  w.qn = g.N - j0;
+  w.K = n;
+  w.out = (static_cast<int64_t>(e) * g.M + i0) * g.N + j0;
   f32x16_t acc[Core::NJ][Core::MI];
-  Core::run(static_cast<const T*>(g.a) + lo * g.lda + i0, g.lda, g.M - i0,
-            static_cast<const T*>(g.b) + lo * g.ldb + j0, g.ldb, g.N - j0, n, acc);
-  TO* C = static_cast<TO*>(g.dw) + static_cast<int64_t>(e) * g.M * g.N +
-          static_cast<int64_t>(i0) * g.N + j0;
-  Core::write(acc, C, g.N, g.accumulate ? C : static_cast<const TO*>(nullptr), g.N, g.M - i0,
-              g.N - j0);
+  Core::run(w, acc);
+  TO* C = static_cast<TO*>(g.dw) + w.out;
+  Core::write(acc, C, g.N, g.accumulate ? C : static_cast<const TO*>(nullptr), g.N, w.pn,
+              w.qn);
 }
 
 // -------------------------------------------------------------------- host
@@ -116,14 +150,13 @@ void launch_matmul(const MatmulArgs& a, hipStream_t s) {
   const int nx = a.rows / Core::BM + std::min(a.experts, a.rows);
   const int ny = (a.N + Core::BN - 1) / Core::BN;
   hipLaunchKernelGGL((k_expert_matmul<Core, T, QKS, TO>),
-                     dim3(static_cast<unsigned>(grid_blocks(nx, ny))), dim3(kThreads), 0, s, a, nx,
-                     ny);
+                     dim3(tile_blocks(nx, ny)), dim3(kThreads), 0, s, a, ny);
 }
 template <typename Core, typename T, typename TO>
 void launch_wgrad(const WgradArgs& g, hipStream_t s) {
   const int nx = (g.M + Core::BM - 1) / Core::BM, ny = (g.N + Core::BN - 1) / Core::BN;
   hipLaunchKernelGGL((k_expert_wgrad<Core, T, TO>),
-                     dim3(static_cast<unsigned>(grid_blocks(static_cast<int64_t>(nx) * g.experts, ny))),
+                     dim3(tile_blocks(static_cast<int64_t>(nx) * g.experts, ny)),
                      dim3(kThreads), 0, s, g, nx, ny);
 }
 
@@ -131,7 +164,7 @@ void launch_wgrad(const WgradArgs& g, hipStream_t s) {
 // evenly, and half a tile lost at each group's end.
 double group_tiles(int rows, int experts, int bm) {
   const double groups = std::min(rows, experts), r = rows / groups;
-  return groups * (r <= bm ? 1.0 : r / bm + 0.5);
+  return groups * (r <= bm / 2 ? 1.0 : r / bm + 0.6);
 }
 
 template <bool QKS, typename TO>
@@ -155,24 +188,32 @@ void run_matmul(const MatmulArgs& a, bool trans, hipStream_t s) {
       return;
     }
   }
-  if (trans) launch_matmul<AnyCore<T, false, false>, T, false, TO>(a, s);
-  else launch_matmul<AnyCore<T, false, true>, T, true, TO>(a, s);
+  const bool large = pick_any_large<T>(
+      [&](int bm) { return group_tiles(a.rows, a.experts, bm); }, a.N, a.K);
+  if (trans) {
+    if (large) launch_matmul<AnyCore<T, false, false, 128>, T, false, TO>(a, s);
+    else launch_matmul<AnyCore<T, false, false, 64>, T, false, TO>(a, s);
+  } else {
+    if (large) launch_matmul<AnyCore<T, false, true, 128>, T, true, TO>(a, s);
+    else launch_matmul<AnyCore<T, false, true, 64>, T, true, TO>(a, s);
+  }
 }
 
 template <typename T, typename TO>
 void run_wgrad(const WgradArgs& g, hipStream_t s) {
+  auto tiles = [&](int bm) { return static_cast<double>(g.experts) * ((g.M + bm - 1) / bm); };
+  const int64_t k = g.rows / g.experts;
   if constexpr (sizeof(T) == 2) {
     if (on_grid(g.a, g.lda, g.M) && on_grid(g.b, g.ldb, g.N) && on_grid(g.dw, g.N, g.M)) {
-      const Shape shape = pick_shape(kShapeTN, [&](int bm) {
-        return static_cast<double>(g.experts) * ((g.M + bm - 1) / bm);
-      }, g.N, g.rows / g.experts);
+      const Shape shape = pick_shape(kShapeTN, tiles, g.N, k);
       if (shape == kLarge) launch_wgrad<LargeCore<true, true>, T, TO>(g, s);
       else if (shape == kHalf) launch_wgrad<HalfCore<true, true>, T, TO>(g, s);
       else launch_wgrad<MediumCore<true, true>, T, TO>(g, s);
       return;
     }
   }
-  launch_wgrad<AnyCore<T, true, true>, T, TO>(g, s);
+  if (pick_any_large<T>(tiles, g.N, k)) launch_wgrad<AnyCore<T, true, true, 128>, T, TO>(g, s);
+  else launch_wgrad<AnyCore<T, true, true, 64>, T, TO>(g, s);
 }
 
 int check_group(int64_t rows, int32_t experts, int64_t k, int64_t n) {

@@ -35,6 +35,16 @@ __device__ __forceinline__ void zero_acc(f32x16_t (&acc)[NJ][MI]) {
       for (int v = 0; v < 16; ++v) acc[a][b][v] = 0.0f;
 }
 
+template <int NJ, int MI>
+__device__ __forceinline__ void scale_acc(f32x16_t (&acc)[NJ][MI], float c) {
+#pragma unroll
+  for (int a = 0; a < NJ; ++a)
+#pragma unroll
+    for (int b = 0; b < MI; ++b)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[a][b][v] *= c;
+}
+
 // Calls f(i, j, value) for every group of four columns of this thread.
 template <typename Core, typename F>
 __device__ __forceinline__ void each_quad(f32x16_t (&acc)[Core::NJ][Core::MI], F&& f) {
@@ -71,24 +81,47 @@ __device__ __forceinline__ void store_quad(TO* p, int left, f32x4_t v) {
   }
 }
 
-// Order of the tiles of an nx x ny grid over a launch of grid_blocks(nx, ny)
-// workgroups.  Workgroups go to the 8 XCDs in turn, so workgroup b takes
-// tile (b % 8) per + b / 8: each XCD works through a contiguous part of the
-// list, and its 32 CUs share operands in its L2.  The list runs through
-// bands of kBand row tiles, column by column.
+// Tile t of an nx x ny grid of tiles: bands of kBand row tiles, column by
+// column.  Workgroups go to the 8 XCDs in turn, so workgroup b works in the
+// (b % 8)-th eighth of this list: the 32 CUs of an XCD run neighbouring
+// tiles and share operands in their L2.
 constexpr int kXcds = 8, kBand = 8;
-__device__ __forceinline__ bool tile_of(int64_t b, int64_t nx, int64_t ny, int& x, int& y) {
-  const int64_t total = nx * ny, per = (total + kXcds - 1) / kXcds;
-  const int64_t t = b % kXcds * per + b / kXcds;
-  if (t >= total) return false;
+__device__ __forceinline__ void tile_at(int64_t t, int64_t nx, int64_t ny, int& x, int& y) {
   const int64_t band = t / (kBand * ny), r = t - band * kBand * ny;
   const int64_t h = nx - band * kBand < kBand ? nx - band * kBand : kBand;
   x = static_cast<int>(band * kBand + r % h);
   y = static_cast<int>(r / h);
+}
+
+// Waits for this wave's LDS accesses and then for the workgroup.  Unlike
+// __syncthreads it leaves vector memory instructions (DMA, stores) in
+// flight.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// One tile's operands; K <= 0 gives zeros.
+template <typename T>
+struct TileArgs {
+  const T *P, *Q;
+  int64_t ldp, ldq;
+  int pn, qn, K;
+};
+
+// The tile of this workgroup among nx x ny (tile_at), if it has one.  A launch
+// of tile_blocks(nx, ny) workgroups covers them all.
+__device__ __forceinline__ bool my_tile(int64_t nx, int64_t ny, int& x, int& y) {
+  const int64_t total = nx * ny, per = (total + kXcds - 1) / kXcds;
+  const int64_t k = blockIdx.x / kXcds, t = blockIdx.x % kXcds * per + k;
+  if (k >= per || t >= total) return false;
+  tile_at(t, nx, ny, x, y);
   return true;
 }
-inline int64_t grid_blocks(int64_t nx, int64_t ny) {
-  return (nx * ny + kXcds - 1) / kXcds * kXcds;
+inline unsigned tile_blocks(int64_t nx, int64_t ny) {
+  return static_cast<unsigned>((nx * ny + kXcds - 1) / kXcds * kXcds);
 }
 
 // 8 k (bf16) or 4 k (fp32) of a 16-wide (8-wide) k step from LDS:
@@ -102,30 +135,34 @@ __device__ __forceinline__ s16x4_t lds_read_tr(const uint16_t* p) {
 
 // ------------------------------------------------------------ any operands
 //
-// The core for operands off the 16-byte grid, and for fp32: 128x128 tiles,
-// 64 bytes of k at a time (32 bf16, 16 fp32) through registers into
+// The core for operands off the 16-byte grid, and for fp32: 128x128 or 64x64
+// tiles, 64 bytes of k at a time (32 bf16, 16 fp32) through registers into
 // double-buffered LDS, the next step's loads in flight during the current
 // step's matrix instructions.  Loads need no alignment; a piece of 16 bytes
 // that crosses the end of a row (or of the tile's columns) is read element
 // by element, so nothing outside the operands is touched.
 // fp32 runs on v_mfma_f32_32x32x2_f32: lane l of instruction s of a group
-// of 8 k supplies k = 4 (l / 32) + s, for both operands.
-template <typename T, bool PKS, bool QKS>
+// of 8 k supplies k = 4 (l / 32) + s, for both operands.  Its sums restart
+// every kFlush steps (256 k) and are added up beside them, so that rounding
+// grows with the square root of 256 and of K / 256 instead of that of K.
+template <typename T, bool PKS, bool QKS, int B>
 struct AnyCore {
-  static constexpr int BM = 128, BN = 128, MI = 2, NJ = 2, WM = 2, WN = 2;
+  static constexpr int BM = B, BN = B, MI = B / 64, NJ = B / 64, WM = 2, WN = 2;
   static constexpr bool F32 = sizeof(T) == 4;
   static constexpr int E = 16 / sizeof(T);   // elements per 16-byte piece
   static constexpr int CK = 4 * E;           // k per step
+  static constexpr int H = B / 64;           // pieces of an operand per thread
   // LDS strides in elements.  K-contiguous rows of 64 bytes are padded to
   // 80, so that 16-byte reads of consecutive rows spread over the banks;
-  // K-strided rows of 128 columns by 8 elements, so that the k rows the two
+  // K-strided rows of B columns by 8 elements, so that the k rows the two
   // lane halves read differ by half the banks.
-  static constexpr int SC = CK + E, SS = 128 + 8;
-  static constexpr int kOperandBytes = 128 * SC * static_cast<int>(sizeof(T));  // >= CK * SS
-  static_assert(CK * SS <= 128 * SC, "a K-strided tile fits the K-contiguous one's space");
+  static constexpr int SC = CK + E, SS = B + 8;
+  static constexpr int kOperandBytes =
+      (B * SC > CK * SS ? B * SC : CK * SS) * static_cast<int>(sizeof(T));
   static constexpr int kLdsBytes = 4 * kOperandBytes;
-  static constexpr int kWaves = 2;  // per SIMD, at least
+  static constexpr int kWaves = B == 128 ? 2 : 4;  // per SIMD, at least
   static constexpr bool kGrid = false;
+  static constexpr int kFlush = 16;
   static __device__ __forceinline__ char* lds() {
     __shared__ __attribute__((aligned(16))) char mem[kLdsBytes];
     return mem;
@@ -137,7 +174,7 @@ struct AnyCore {
     int r, k, left;
     const T* a;
     if (KS) {
-      constexpr int PR = 128 / E;
+      constexpr int PR = B / E;
       k = k0 + pc / PR;
       r = (pc % PR) * E;
       left = k < K ? n - r : 0;
@@ -161,7 +198,7 @@ struct AnyCore {
   }
   template <bool KS>
   static __device__ __forceinline__ T* lds_piece(T* s, int pc) {
-    constexpr int PR = 128 / E;
+    constexpr int PR = B / E;
     return KS ? s + (pc / PR) * SS + (pc % PR) * E : s + (pc >> 2) * SC + (pc & 3) * E;
   }
   // operand fragment of 32-row block at row b, k step g (16 bf16, 8 fp32)
@@ -191,16 +228,17 @@ struct AnyCore {
     }
   }
 
-  static __device__ __forceinline__ void run(const T* P, int64_t ldp, int pn, const T* Q,
-                                             int64_t ldq, int qn, int K,
-                                             f32x16_t (&acc)[NJ][MI]) {
+  static __device__ __forceinline__ void run(const TileArgs<T>& w, f32x16_t (&acc)[NJ][MI]) {
+    const T *P = w.P, *Q = w.Q;
+    const int64_t ldp = w.ldp, ldq = w.ldq;
+    const int pn = w.pn, qn = w.qn, K = w.K;
     char* smem = lds();
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     const int wi = wave % WM, wj = wave / WM;
-    u32x4_t pr[2], qr[2];
+    u32x4_t pr[H], qr[H];
     auto load = [&](int k0) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < H; ++h) {
         pr[h] = piece<PKS>(P, ldp, pn, K, k0, t + 256 * h);
         qr[h] = piece<QKS>(Q, ldq, qn, K, k0, t + 256 * h);
       }
@@ -210,46 +248,60 @@ struct AnyCore {
     };
     auto store = [&](int b) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < H; ++h) {
         *reinterpret_cast<u32x4_t*>(lds_piece<PKS>(buf(b, 0), t + 256 * h)) = pr[h];
         *reinterpret_cast<u32x4_t*>(lds_piece<QKS>(buf(b, 1), t + 256 * h)) = qr[h];
       }
     };
     zero_acc(acc);
+    if (K <= 0) return;
     const int steps = (K + CK - 1) / CK;
-    if (steps == 0) return;
     load(0);
     store(0);
     __syncthreads();
-    for (int c = 0; c < steps; ++c) {
-      const int b = c & 1;
-      if (c + 1 < steps) load((c + 1) * CK);
-      const T* ps = buf(b, 0);
-      const T* qs = buf(b, 1);
+    auto span = [&](f32x16_t (&d)[NJ][MI], int c0, int c1) {
+      for (int c = c0; c < c1; ++c) {
+        const int b = c & 1;
+        if (c + 1 < steps) load((c + 1) * CK);
+        const T* ps = buf(b, 0);
+        const T* qs = buf(b, 1);
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        decltype(frag<PKS>(ps, 0, 0, 0)) p[MI];
-        decltype(frag<QKS>(qs, 0, 0, 0)) q[NJ];
+        for (int g = 0; g < 2; ++g) {
+          decltype(frag<PKS>(ps, 0, 0, 0)) p[MI];
+          decltype(frag<QKS>(qs, 0, 0, 0)) q[NJ];
 #pragma unroll
-        for (int i = 0; i < MI; ++i) p[i] = frag<PKS>(ps, wi * 64 + 32 * i, g, lane);
+          for (int i = 0; i < MI; ++i) p[i] = frag<PKS>(ps, wi * 32 * MI + 32 * i, g, lane);
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) q[j] = frag<QKS>(qs, wj * 64 + 32 * j, g, lane);
+          for (int j = 0; j < NJ; ++j) q[j] = frag<QKS>(qs, wj * 32 * NJ + 32 * j, g, lane);
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+              if constexpr (F32) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  d[j][i] = __builtin_amdgcn_mfma_f32_32x32x2f32(q[j][e], p[i][e], d[j][i], 0, 0, 0);
+              } else {
+                d[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(q[j], p[i], d[j][i], 0, 0, 0);
+              }
+            }
+        }
+        if (c + 1 < steps) store(b ^ 1);
+        __syncthreads();
+      }
+    };
+    if constexpr (F32) {
+      for (int c0 = 0; c0 < steps; c0 += kFlush) {
+        f32x16_t part[NJ][MI];
+        zero_acc(part);
+        span(part, c0, min(c0 + kFlush, steps));
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
-          for (int i = 0; i < MI; ++i) {
-            if constexpr (F32) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x2f32(q[j][e], p[i][e], acc[j][i], 0, 0, 0);
-            } else {
-              acc[j][i] =
-                  __builtin_amdgcn_mfma_f32_32x32x16_bf16(q[j], p[i], acc[j][i], 0, 0, 0);
-            }
-          }
+          for (int i = 0; i < MI; ++i) acc[j][i] += part[j][i];
       }
-      if (c + 1 < steps) store(b ^ 1);
-      __syncthreads();
+    } else {
+      span(acc, 0, steps);
     }
   }
 
@@ -318,7 +370,23 @@ __device__ __forceinline__ void wait_counts() {
   __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | 0x70);
 }
 
+// Workgroup barrier of the operand pipeline; the waits before it are the
+// callers'.
+__device__ __forceinline__ void pipe_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 static __device__ const u32x4_t kZeroPage[1] = {{0, 0, 0, 0}};
+
+// The lane id, hidden from the optimiser: what is derived from it is computed
+// where it is used instead of being kept in registers from tile to tile.
+__device__ __forceinline__ int opaque_lane() {
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  return lane;
+}
 
 template <int N>
 using Int = std::integral_constant<int, N>;
@@ -338,8 +406,8 @@ struct DmaCore {
   static constexpr int PB = BM * BK * 2, QB = BN * BK * 2;  // bytes of a stage's tiles
   static constexpr int NP = PB / 4096, NQ = QB / 4096;      // DMA per wave and stage
   static constexpr int kSlotBytes = PB + QB;
-  static constexpr int kLdsBytes = kSlotBytes;  // of lds()
   static constexpr bool kGrid = true;  // rows on the 16-byte grid
+  static constexpr int kLdsBytes = kSlotBytes;  // of lds()
   // waves per SIMD: what the LDS allows of workgroups per CU
   static constexpr int kWaves = 160 * 1024 / (NS * kSlotBytes) < 3 ? 160 * 1024 / (NS * kSlotBytes) : 3;
   static_assert(BK == 32 || BK == 64, "");
@@ -350,6 +418,7 @@ struct DmaCore {
     __shared__ __attribute__((aligned(1024))) char mem[kSlotBytes];
     return mem;
   }
+  // scratch for a result
   static __device__ __forceinline__ char* lds() { return slot<0>(); }
 
   // One operand: R rows (or columns), lane offsets of this wave's DMA.
@@ -428,23 +497,25 @@ struct DmaCore {
     bf16x8_t p[MI], q[NJ];
   };
 
-  static __device__ __forceinline__ void run(const uint16_t* P, int64_t ldp, int pn,
-                                             const uint16_t* Q, int64_t ldq, int qn, int K,
+  static constexpr int DPS = NP + NQ;  // a wave's DMA instructions per stage
+
+  static __device__ __forceinline__ void run(const TileArgs<uint16_t>& w,
                                              f32x16_t (&acc)[NJ][MI]) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int ri = (wave % WM) * 32 * MI, rj = (wave / WM) * 32 * NJ;
     zero_acc(acc);
-    if (K <= 0) return;
+    if (w.K <= 0) return;
     Operand<PKS, BM> po;
     Operand<QKS, BN> qo;
-    po.init(P, ldp, pn, wave, lane);
-    qo.init(Q, ldq, qn, wave, lane);
-    // stage 0 is the sum's ragged end, if it has one; the others are whole
-    const int kleft = K % BK, nk = K / BK + (kleft != 0);
-    const int shift = kleft != 0 ? -1 : 0;  // stage kt >= 1 - shift starts at k = (kt + shift) BK
+    po.init(w.P, w.ldp, w.pn, wave, lane);
+    qo.init(w.Q, w.ldq, w.qn, wave, lane);
+    // stage 0 is the sum's ragged end, if it has one; the others are whole,
+    // and stage kt starts at k = (kt + shift) BK
+    const int kleft = w.K % BK, nk = w.K / BK + (kleft != 0);
+    const int shift = kleft != 0 ? -1 : 0;
 
-    // DMA instruction D (P's first) of stage kt
+    // DMA instruction D (P's first) of a whole stage
     auto issue1 = [&](int kt, auto slot_c, auto d_c) {
       char* tile = slot<decltype(slot_c)::value>();
       constexpr int d = decltype(d_c)::value;
@@ -455,11 +526,10 @@ struct DmaCore {
               tile + PB + (wave * NQ + d - NP) * 1024);
     };
     auto issue = [&](int kt, auto slot_c) {
-      static_for<0, NP + NQ>([&](auto d_c) { issue1(kt, slot_c, d_c); });
+      static_for<0, DPS>([&](auto d_c) { issue1(kt, slot_c, d_c); });
     };
-    // this wave's DMA of a stage has landed when at most the newer stages'
-    // is outstanding; behind the barrier, everybody's has
-    constexpr int DPS = NP + NQ;
+    // This wave's DMA of a stage has landed when at most that of the newer
+    // stages is outstanding; behind the barrier, everybody's has.
     auto landed = [&](int newer) {
       static_for<0, NS - 1>([&](auto i_c) {
         constexpr int i = decltype(i_c)::value;
@@ -467,16 +537,13 @@ struct DmaCore {
       });
     };
 
-    __syncthreads();  // the slots are free (a tile before this one, an epilogue)
     if (kleft != 0) {
-      const int64_t kf = K / BK;
-      static_for<0, NP>([&](auto d_c) {
-        constexpr int d = decltype(d_c)::value;
-        po.template issue_tail<d>(kf, slot<0>(), wave, lane, kleft);
+      const int64_t kf = w.K / BK;
+      static_for<0, NP>([&](auto d) {
+        po.template issue_tail<decltype(d)::value>(kf, slot<0>(), wave, lane, kleft);
       });
-      static_for<0, NQ>([&](auto d_c) {
-        constexpr int d = decltype(d_c)::value;
-        qo.template issue_tail<d>(kf, slot<0>() + PB, wave, lane, kleft);
+      static_for<0, NQ>([&](auto d) {
+        qo.template issue_tail<decltype(d)::value>(kf, slot<0>() + PB, wave, lane, kleft);
       });
     } else {
       issue(0, Int<0>{});
@@ -486,7 +553,7 @@ struct DmaCore {
     });
     if (nk >= NS) wait_counts<(NS - 1) * DPS>();
     else wait_counts<0>();
-    __builtin_amdgcn_s_barrier();
+    pipe_barrier();
 
     Frags f[2];
     auto read = [&](Frags& fr, auto slot_c, int g, auto r_c) {
@@ -513,7 +580,7 @@ struct DmaCore {
         if constexpr (last) {
           if constexpr (STEADY) wait_counts<(NS - 2) * DPS>();
           else landed(nk - 2 - kt);
-          __builtin_amdgcn_s_barrier();
+          pipe_barrier();
           if constexpr (!STEADY) {
             if (kt + NS < nk) issue(kt + NS, slot_c);
           }
@@ -560,12 +627,13 @@ struct DmaCore {
   template <typename TO, typename TA>
   static __device__ __forceinline__ void write(f32x16_t (&acc)[NJ][MI], TO* C, int64_t ldc,
                                                const TA* add, int64_t lda, int rows, int cols) {
-    __syncthreads();  // no wave reads operands any more
     if (sizeof(TO) == 2 && add == nullptr) rows_out<TO, TA, true>(acc, C, ldc, add, lda, rows, cols);
     else rows_out<TO, TA, false>(acc, C, ldc, add, lda, rows, cols);
   }
 
-  // Bytes of a staged row: up to 256, as many as leave each wave a region.
+  // Bytes of a staged row: up to 256, as many as leave each wave a region in
+  // the slots.  (Behind the last barrier of run() no wave reads operands any
+  // more, so the slots are free.)
   static constexpr int stage_row(int bytes) {
     int rb = bytes < 256 ? bytes : 256;
     while (kSlotBytes / (32 * MI * rb) * NS < 4) rb /= 2;
@@ -576,12 +644,12 @@ struct DmaCore {
   static __device__ __forceinline__ void rows_out(f32x16_t (&acc)[NJ][MI], TO* C, int64_t ldc,
                                                   const TA* add, int64_t lda, int rows, int cols) {
     constexpr int ES = HALF ? 2 : 4;
-    constexpr int RB = stage_row(NJ * 32 * ES);                  // bytes of a staged row
-    constexpr int CW = RB / ES, JB = CW / 32;                    // its columns, blocks of 32
+    constexpr int RB = stage_row(NJ * 32 * ES);
+    constexpr int CW = RB / ES, JB = CW / 32;  // columns of a staged row, blocks of 32
     constexpr int NCH = RB / 16, SH = NCH == 16 ? 0 : NCH == 8 ? 1 : 2;
     constexpr int REGION = 32 * MI * RB, PER = kSlotBytes / REGION;
-    static_assert(PER >= 1 && PER * NS >= 4, "a region for each wave");
-    const int lane = threadIdx.x & 63;
+    static_assert(PER >= 1 && PER * NS >= 4 && NJ % JB == 0, "a region for each wave");
+    const int lane = opaque_lane();
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     char* S = slot<0>();
     static_for<1, NS>([&](auto s) {
@@ -644,7 +712,7 @@ struct DmaCore {
   }
 };
 
-// The tile shapes.  Large: the least operand traffic for a flop (512 rows and
+// The tile shapes of the DMA core.  Large: the least operand traffic for a flop (512 rows and
 // columns of operands for 256 x 256 results), one workgroup to a CU, so
 // nothing hides its prologue and epilogue.  Half and Medium: two workgroups
 // to a CU.  Thin: a deep ring for streaming Q past a few rows of P.
@@ -661,34 +729,44 @@ using MediumCore = DmaCore<PKS, QKS, 128, 128, 2, 64, 2>;
 template <bool PKS, bool QKS>
 using ThinCore = DmaCore<PKS, QKS, 32, 128, 1, 64, 6>;
 
-// Which of them: the least estimated time on 256 CUs.  A workgroup's time is
-// stage x K / 64 + fixed microseconds, as many share a CU as fit it; tiles
-// beyond one a place take their share of a round more, and the last round
-// is on average partly empty.  The constants are fits to measured products
-// (8 to 65536 rows, 8 to 128 experts, sides 1024 to 7168): the estimate
-// ranks the shapes right or within 10% there.
+// Which of them: the least estimated time on 256 CUs.  A workgroup takes
+// stage x K / 64 + fixed microseconds, where the time of 64 k grows from
+// `alone` to `full` with the number of workgroups that share the GPU (matrix
+// cores of their CU, memory); tiles beyond one a place take further rounds,
+// whole ones while they are few.  The constants are fits to measured
+// products of 8 to 65536 rows, 1 to 128 experts, sides 1000 to 7168 and 32000
+// to 163840 vocabulary rows; some of what they rest on (us, shape by shape):
+//   8 rows x 64 experts 2048x1408 (NN): Thin 11.8, Medium 21.5, Half 24, Large 43
+//   700 rows x 20 experts 1280x1024 (NN): Medium 16.5, Half 18.2, Thin 20.5, Large 30
+//   8192 rows x 16 experts 1024x2048 (TN): Half 41.0, Medium 47.9, Large 48.2
+//   loss 1024 x 50048 x 1024 (NT): Medium 164, Large 198, Half 255
+//   loss 4096 x 163840 x 7168 (NT): Large 7900, Medium 9530, Half 10240
 struct ShapeCost {
   int bm, bn, per_cu;
-  double stage, fixed;
+  double alone, full, fixed;
 };
 inline double shape_time(const ShapeCost& c, double row_tiles, int64_t cols, int64_t k) {
   const double tiles = row_tiles * static_cast<double>((cols + c.bn - 1) / c.bn);
-  double stage = c.stage, rounds = 1.0;
-  if (tiles <= 256.0) {
-    stage /= c.per_cu;  // alone on its CU
-  } else if (tiles > 256.0 * c.per_cu) {
-    const double r = tiles / (256.0 * c.per_cu);
+  const double places = 256.0 * c.per_cu;
+  const double load = std::fmin(1.0, std::fmax(0.0, (tiles - 128.0) / (places - 128.0)));
+  double rounds = 1.0;
+  if (tiles > places) {
+    const double r = tiles / places;
     rounds = r < 8.0 ? std::ceil(r) : r + 0.5;
   }
+  const double stage = c.alone + (c.full - c.alone) * load;
   return rounds * (static_cast<double>(k) / 64.0 * stage + c.fixed);
 }
 enum Shape { kLarge, kHalf, kMedium, kThin };
-constexpr ShapeCost kShapeNT[] = {{256, 256, 1, 1.75, 11.0}, {128, 256, 2, 2.45, 4.0},
-                                  {128, 128, 2, 1.13, 3.0}, {32, 128, 1, 0.70, 2.0}};
-constexpr ShapeCost kShapeNN[] = {{256, 256, 1, 1.79, 12.0}, {128, 256, 2, 2.15, 3.0},
-                                  {128, 128, 2, 1.13, 3.0}, {32, 128, 1, 0.70, 2.0}};
-constexpr ShapeCost kShapeTN[] = {{256, 256, 1, 1.65, 9.0}, {128, 256, 2, 2.10, 4.2},
-                                  {128, 128, 2, 1.10, 3.2}};
+constexpr ShapeCost kShapeNT[] = {{256, 256, 1, 1.40, 1.72, 12.0}, {128, 256, 2, 1.40, 2.45, 4.0},
+                                  {128, 128, 2, 0.50, 1.12, 3.0}, {32, 128, 1, 0.30, 0.80, 2.0}};
+constexpr ShapeCost kShapeNN[] = {{256, 256, 1, 1.50, 1.79, 12.0}, {128, 256, 2, 1.10, 2.15, 3.0},
+                                  {128, 128, 2, 0.50, 1.13, 3.0}, {32, 128, 1, 0.30, 0.80, 2.0}};
+constexpr ShapeCost kShapeTN[] = {{256, 256, 1, 1.45, 1.65, 9.0}, {128, 256, 2, 1.05, 2.10, 4.2},
+                                  {128, 128, 2, 0.55, 1.10, 3.2}};
+// the core for any operands: 128 x 128, 64 x 64
+constexpr ShapeCost kShapeAnyBf16[] = {{128, 128, 2, 1.20, 1.85, 3.0}, {64, 64, 4, 0.70, 1.60, 2.0}};
+constexpr ShapeCost kShapeAnyFp32[] = {{128, 128, 2, 5.60, 9.40, 3.0}, {64, 64, 4, 2.40, 5.40, 2.0}};
 // rows(bm): row tiles of bm rows
 template <int N, typename R>
 Shape pick_shape(const ShapeCost (&c)[N], R&& rows, int64_t cols, int64_t k) {
@@ -702,6 +780,12 @@ Shape pick_shape(const ShapeCost (&c)[N], R&& rows, int64_t cols, int64_t k) {
     }
   }
   return static_cast<Shape>(best);
+}
+
+// Whether the core for any operands takes its 128x128 tiles.
+template <typename T, typename R>
+bool pick_any_large(R&& rows, int64_t cols, int64_t k) {
+  return pick_shape(sizeof(T) == 2 ? kShapeAnyBf16 : kShapeAnyFp32, rows, cols, k) == 0;
 }
 
 }  // namespace muon
