@@ -732,6 +732,14 @@ def _one_device(**tensors):
     return dev
 
 
+def _current_handle(dev) -> int:
+    """hipStream_t of the current stream of ``dev`` (the raw query where torch
+    has it: the Stream object costs more than the rest of a small call)."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(dev.index) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
 class _Launch:
     """Makes ``dev`` current, and ``stream`` (if given) the stream that torch
     allocates on, around one call; ``handle`` is the hipStream_t."""
@@ -744,7 +752,7 @@ class _Launch:
         if dev.index != torch.cuda.current_device():
             self._dev = torch.cuda.device(dev)
         if stream is None:
-            self.handle = torch.cuda.current_stream(dev).cuda_stream
+            self.handle = _current_handle(dev)
             return
         if isinstance(stream, int):
             stream = (torch.cuda.ExternalStream(stream, device=dev) if stream

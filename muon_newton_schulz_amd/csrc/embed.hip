@@ -84,8 +84,8 @@ __global__ __launch_bounds__(kThreads) void k_embed_fwd(const TT* __restrict__ t
 //
 // Up to kRankN keys: a key's place is the number of keys that are smaller,
 // or equal and before it.  All pairs are compared, n^2 / 64 wave
-// instructions spread over the GPU, in one launch (8192 keys: 8 us; one
-// workgroup's radix sort in LDS took 26).
+// instructions spread over the GPU, in one launch (one workgroup's radix
+// sort of 8192 keys in LDS took 26 us).
 // More: LSD radix sort, at most kMaxBits bits a pass, a histogram and a
 // scatter launch each.  Each wave owns a contiguous part of its workgroup's
 // keys and places 64 keys at a time, a key's rank among equal digits of the
@@ -220,6 +220,7 @@ __global__ __launch_bounds__(kRankThreads) void k_sort_rank(
   uint32_t count = 0;
   // keys of [lo, hi) below x, both multiples of 4
   auto below = [&](int lo, int hi, uint32_t x) {
+#pragma unroll 8
     for (int j = lo; j < hi; j += 4) {
       const uint4 k = *reinterpret_cast<const uint4*>(key + j);
       count += k.x < x;
@@ -657,8 +658,12 @@ int zero_blocks(int64_t bytes, int threads) {
 int zero_parts(int64_t groups) {
   return groups <= 0 ? 1 : static_cast<int>(std::max<int64_t>(1, 2048 / groups));
 }
-// Bytes zeroed beside the sort: about what its time allows.
-constexpr int64_t kZeroWithRank = 32 << 20, kZeroWithRadix = 64 << 20;
+// Bytes zeroed beside the sort: about what its time allows.  (4096 positions
+// into 32000 x 2048: 42 us with 32 MiB, 34 with 64, 36 with 128; 8191: 46, 46
+// and 39.)
+int64_t zero_with_sort(int64_t n) {
+  return std::min<int64_t>(int64_t{128} << 20, std::max<int64_t>(int64_t{32} << 20, n << 14));
+}
 
 struct BackwardArgs {
   const void *dout, *ids;
@@ -690,7 +695,7 @@ void run_backward(const BackwardArgs& a, const EmbedWs& w, hipStream_t s) {
   }
   // rows [0, zero_v0) are zeroed before the sums
   const int64_t row_bytes = a.dim * static_cast<int64_t>(sizeof(TG));
-  int64_t zero_v0 = a.accumulate ? vocab : (n <= kRankN ? kZeroWithRank : kZeroWithRadix) / row_bytes;
+  int64_t zero_v0 = a.accumulate ? vocab : zero_with_sort(n) / row_bytes;
   if (zero_v0 > vocab || n == 0) zero_v0 = vocab;
   const int64_t zero_n = a.accumulate ? 0 : zero_v0 * a.dim;
   const int64_t zero_bytes = zero_n * static_cast<int64_t>(sizeof(TG));
