@@ -191,11 +191,11 @@ void run_matmul(const MatmulArgs& a, bool trans, hipStream_t s) {
   const bool large = pick_any_large<T>(
       [&](int bm) { return group_tiles(a.rows, a.experts, bm); }, a.N, a.K);
   if (trans) {
-    if (large) launch_matmul<AnyCore<T, false, false, 128>, T, false, TO>(a, s);
-    else launch_matmul<AnyCore<T, false, false, 64>, T, false, TO>(a, s);
+    if (large) launch_matmul<OtherCore<T, false, false, 128>, T, false, TO>(a, s);
+    else launch_matmul<OtherCore<T, false, false, 64>, T, false, TO>(a, s);
   } else {
-    if (large) launch_matmul<AnyCore<T, false, true, 128>, T, true, TO>(a, s);
-    else launch_matmul<AnyCore<T, false, true, 64>, T, true, TO>(a, s);
+    if (large) launch_matmul<OtherCore<T, false, true, 128>, T, true, TO>(a, s);
+    else launch_matmul<OtherCore<T, false, true, 64>, T, true, TO>(a, s);
   }
 }
 
@@ -212,8 +212,8 @@ void run_wgrad(const WgradArgs& g, hipStream_t s) {
       return;
     }
   }
-  if (pick_any_large<T>(tiles, g.N, k)) launch_wgrad<AnyCore<T, true, true, 128>, T, TO>(g, s);
-  else launch_wgrad<AnyCore<T, true, true, 64>, T, TO>(g, s);
+  if (pick_any_large<T>(tiles, g.N, k)) launch_wgrad<OtherCore<T, true, true, 128>, T, TO>(g, s);
+  else launch_wgrad<OtherCore<T, true, true, 64>, T, TO>(g, s);
 }
 
 int check_group(int64_t rows, int32_t experts, int64_t k, int64_t n) {

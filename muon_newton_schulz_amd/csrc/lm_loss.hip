@@ -492,8 +492,8 @@ int run_stats(const StatsArgs& a, bool grid, hipStream_t s) {
     }
   }
   if (pick_any_large<T>(row_tiles(a.n), a.vocab, a.dim))
-    return launch_stats<AnyCore<T, false, false, 128>, T>(a, s);
-  return launch_stats<AnyCore<T, false, false, 64>, T>(a, s);
+    return launch_stats<OtherCore<T, false, false, 128>, T>(a, s);
+  return launch_stats<OtherCore<T, false, false, 64>, T>(a, s);
 }
 
 template <typename Core, typename T>
@@ -515,9 +515,9 @@ void run_g(const GradArgs& a, bool grid, hipStream_t s) {
     }
   }
   if (pick_any_large<T>(row_tiles(a.n), a.len, a.dim))
-    launch_g<AnyCore<T, false, false, 128>, T>(a, s);
+    launch_g<OtherCore<T, false, false, 128>, T>(a, s);
   else
-    launch_g<AnyCore<T, false, false, 64>, T>(a, s);
+    launch_g<OtherCore<T, false, false, 64>, T>(a, s);
 }
 
 template <typename Core, typename T, typename TO>
@@ -541,9 +541,9 @@ void run_dh(const DhArgs& a, bool grid, hipStream_t s) {
     }
   }
   if (pick_any_large<T>(dh_tiles(a.n, a.splits), a.dim, ceil_div(a.len, a.splits)))
-    launch_dh<AnyCore<T, false, true, 128>, T, TO>(a, s);
+    launch_dh<OtherCore<T, false, true, 128>, T, TO>(a, s);
   else
-    launch_dh<AnyCore<T, false, true, 64>, T, TO>(a, s);
+    launch_dh<OtherCore<T, false, true, 64>, T, TO>(a, s);
 }
 
 template <typename Core, typename T, typename TO>
@@ -564,9 +564,9 @@ void run_dw(const DwArgs& a, bool grid, hipStream_t s) {
     }
   }
   if (pick_any_large<T>(row_tiles(a.len), a.dim, a.n))
-    launch_dw<AnyCore<T, true, true, 128>, T, TO>(a, s);
+    launch_dw<OtherCore<T, true, true, 128>, T, TO>(a, s);
   else
-    launch_dw<AnyCore<T, true, true, 64>, T, TO>(a, s);
+    launch_dw<OtherCore<T, true, true, 64>, T, TO>(a, s);
 }
 
 struct BackwardArgs {

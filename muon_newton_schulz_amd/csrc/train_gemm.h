@@ -81,6 +81,22 @@ __device__ __forceinline__ void store_quad(TO* p, int left, f32x4_t v) {
   }
 }
 
+// C[i][j] = acc (+ add[i][j]) for i < rows, j < cols, no alignment needed.
+// add may be C.
+template <typename Core, typename TO, typename TA>
+__device__ __forceinline__ void write_quads(f32x16_t (&acc)[Core::NJ][Core::MI], TO* C, int64_t ldc,
+                                            const TA* add, int64_t lda, int rows, int cols) {
+  each_quad<Core>(acc, [&](int i, int j, f32x4_t v) {
+    if (i >= rows || j >= cols) return;
+    if (add != nullptr) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (j + e < cols) v[e] += to_f32(add[i * lda + j + e]);
+    }
+    store_quad(C + i * ldc + j, cols - j, v);
+  });
+}
+
 // Tile t of an nx x ny grid of tiles: bands of kBand row tiles, column by
 // column.  Workgroups go to the 8 XCDs in turn, so workgroup b works in the
 // (b % 8)-th eighth of this list: the 32 CUs of an XCD run neighbouring
@@ -133,6 +149,28 @@ __device__ __forceinline__ s16x4_t lds_read_tr(const uint16_t* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t)(p));
 }
 
+// 16 bytes of an operand tile of B rows (columns) by CK k: piece pc counts
+// along the memory's rows.  What lies past row n or k = K is zero.
+template <typename T, bool KS, int B, int CK>
+__device__ __forceinline__ u32x4_t load_piece(const T* p, int64_t ld, int n, int K, int k0, int pc) {
+  constexpr int E = 16 / sizeof(T);
+  constexpr int PR = (KS ? B : CK) / E;  // pieces to a row
+  const int row = pc / PR, col = pc % PR * E;
+  const int r = KS ? col : row, k = k0 + (KS ? row : col);
+  const int left = KS ? (k < K ? n - r : 0) : (r < n ? K - k : 0);
+  const T* a = p + static_cast<int64_t>(KS ? k : r) * ld + (KS ? r : k);
+  u32x4_t w = {0, 0, 0, 0};
+  if (left >= E) {
+    __builtin_memcpy(&w, a, 16);
+  } else if (left > 0) {
+    T x[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = e < left ? a[e] : T{};
+    __builtin_memcpy(&w, x, 16);
+  }
+  return w;
+}
+
 // ------------------------------------------------------------ any operands
 //
 // The core for operands off the 16-byte grid, and for fp32: 128x128 or 64x64
@@ -169,34 +207,6 @@ struct AnyCore {
   }
 
   template <bool KS>
-  static __device__ __forceinline__ u32x4_t piece(const T* p, int64_t ld, int n, int K, int k0,
-                                                  int pc) {
-    int r, k, left;
-    const T* a;
-    if (KS) {
-      constexpr int PR = B / E;
-      k = k0 + pc / PR;
-      r = (pc % PR) * E;
-      left = k < K ? n - r : 0;
-      a = p + static_cast<int64_t>(k) * ld + r;
-    } else {
-      r = pc >> 2;
-      k = k0 + (pc & 3) * E;
-      left = r < n ? K - k : 0;
-      a = p + static_cast<int64_t>(r) * ld + k;
-    }
-    u32x4_t w = {0, 0, 0, 0};
-    if (left >= E) {
-      __builtin_memcpy(&w, a, 16);
-    } else if (left > 0) {
-      T x[E];
-#pragma unroll
-      for (int e = 0; e < E; ++e) x[e] = e < left ? a[e] : T{};
-      __builtin_memcpy(&w, x, 16);
-    }
-    return w;
-  }
-  template <bool KS>
   static __device__ __forceinline__ T* lds_piece(T* s, int pc) {
     constexpr int PR = B / E;
     return KS ? s + (pc / PR) * SS + (pc % PR) * E : s + (pc >> 2) * SC + (pc & 3) * E;
@@ -229,18 +239,21 @@ struct AnyCore {
   }
 
   static __device__ __forceinline__ void run(const TileArgs<T>& w, f32x16_t (&acc)[NJ][MI]) {
+    run_in(w, acc, lds());
+  }
+  static __device__ __forceinline__ void run_in(const TileArgs<T>& w, f32x16_t (&acc)[NJ][MI],
+                                                char* smem) {
     const T *P = w.P, *Q = w.Q;
     const int64_t ldp = w.ldp, ldq = w.ldq;
     const int pn = w.pn, qn = w.qn, K = w.K;
-    char* smem = lds();
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     const int wi = wave % WM, wj = wave / WM;
     u32x4_t pr[H], qr[H];
     auto load = [&](int k0) {
 #pragma unroll
       for (int h = 0; h < H; ++h) {
-        pr[h] = piece<PKS>(P, ldp, pn, K, k0, t + 256 * h);
-        qr[h] = piece<QKS>(Q, ldq, qn, K, k0, t + 256 * h);
+        pr[h] = load_piece<T, PKS, B, CK>(P, ldp, pn, K, k0, t + 256 * h);
+        qr[h] = load_piece<T, QKS, B, CK>(Q, ldq, qn, K, k0, t + 256 * h);
       }
     };
     auto buf = [&](int b, int op) {
@@ -305,19 +318,146 @@ struct AnyCore {
     }
   }
 
-  // C[i][j] = acc (+ add[i][j]) for i < rows, j < cols.  add may be C.
   template <typename TO, typename TA>
   static __device__ __forceinline__ void write(f32x16_t (&acc)[NJ][MI], TO* C, int64_t ldc,
                                                const TA* add, int64_t lda, int rows, int cols) {
-    each_quad<AnyCore>(acc, [&](int i, int j, f32x4_t v) {
-      if (i >= rows || j >= cols) return;
-      if (add != nullptr) {
+    write_quads<AnyCore>(acc, C, ldc, add, lda, rows, cols);
+  }
+};
+
+// ------------------------------------------------------- fp32 in three bf16
+//
+// fp32 products on the bf16 matrix cores: an operand x is the sum of three
+// bf16 values, hi = bf16(x), mid = bf16(x - hi), lo = bf16(x - hi - mid),
+// exactly up to 2^-27 x, and of the nine products the six above 2^-26 of
+// the largest are added, smallest first, in fp32 (products of bf16 are
+// exact in fp32).  The result is as accurate as a sum of fp32 products
+// (Henry, Tang, Heinecke, "Leveraging the bfloat16 artificial intelligence
+// datatype for higher-precision computations", 2019).  Six bf16
+// instructions take 192 cycles for 16 k, the fp32 ones 512.
+// An operand that is not finite, or rounds to an infinite hi, makes its
+// results NaN here: a tile that holds a value that is not finite is computed
+// again on the fp32 instructions, and those values are taken from there.
+// 32 k a step; the operands are split on their way into LDS (single buffer;
+// two to four workgroups share a CU).  Sums restart every 256 k.
+template <bool PKS, bool QKS, int B>
+struct SplitCore {
+  using Exact = AnyCore<float, PKS, QKS, B>;
+  using Half = AnyCore<uint16_t, PKS, QKS, B>;  // its fragments and strides
+  static constexpr int BM = B, BN = B, MI = B / 64, NJ = B / 64, WM = 2, WN = 2, CK = 32;
+  static constexpr int H = B / 32;              // pieces of an operand per thread
+  static constexpr int kPlane = Half::kOperandBytes;
+  static constexpr int kLdsBytes = 6 * kPlane > Exact::kLdsBytes ? 6 * kPlane : Exact::kLdsBytes;
+  static constexpr int kWaves = B == 128 ? 2 : 4;
+  static constexpr bool kGrid = false;
+  static constexpr int kFlush = 8;
+  static __device__ __forceinline__ char* lds() {
+    __shared__ __attribute__((aligned(16))) char mem[kLdsBytes];
+    return mem;
+  }
+  // plane k (hi, mid, lo) of operand op
+  static __device__ __forceinline__ uint16_t* plane(int op, int k) {
+    return reinterpret_cast<uint16_t*>(lds() + (3 * op + k) * kPlane);
+  }
+  template <bool KS>
+  static __device__ __forceinline__ void split_store(int op, int pc, u32x4_t w) {
+    constexpr int PR = (KS ? B : CK) / 4;
+    const int o = pc / PR * (KS ? Half::SS : Half::SC) + pc % PR * 4;
+    const f32x4_t x = __builtin_bit_cast(f32x4_t, w);
+    f32x2_t a = {x[0], x[1]}, b = {x[2], x[3]};
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (j + e < cols) v[e] += to_f32(add[i * lda + j + e]);
+    for (int k = 0; k < 3; ++k) {
+      const u32x2_t h = {pack_bf16(a[0], a[1]), pack_bf16(b[0], b[1])};
+      *reinterpret_cast<u32x2_t*>(plane(op, k) + o) = h;
+      a[0] -= __uint_as_float(h[0] << 16);
+      a[1] -= __uint_as_float(h[0] & 0xffff0000u);
+      b[0] -= __uint_as_float(h[1] << 16);
+      b[1] -= __uint_as_float(h[1] & 0xffff0000u);
+    }
+  }
+
+  static __device__ __forceinline__ void run(const TileArgs<float>& w, f32x16_t (&acc)[NJ][MI]) {
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int wi = wave % WM, wj = wave / WM;
+    zero_acc(acc);
+    if (w.K <= 0) return;
+    u32x4_t pr[H], qr[H];
+    auto load = [&](int k0) {
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        pr[h] = load_piece<float, PKS, B, CK>(w.P, w.ldp, w.pn, w.K, k0, t + 256 * h);
+        qr[h] = load_piece<float, QKS, B, CK>(w.Q, w.ldq, w.qn, w.K, k0, t + 256 * h);
       }
-      store_quad(C + i * ldc + j, cols - j, v);
-    });
+    };
+    const int steps = (w.K + CK - 1) / CK;
+    load(0);
+    for (int c0 = 0; c0 < steps; c0 += kFlush) {
+      f32x16_t part[NJ][MI];
+      zero_acc(part);
+      for (int c = c0; c < min(c0 + kFlush, steps); ++c) {
+        __syncthreads();  // the step before is read
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          split_store<PKS>(0, t + 256 * h, pr[h]);
+          split_store<QKS>(1, t + 256 * h, qr[h]);
+        }
+        __syncthreads();
+        if (c + 1 < steps) load((c + 1) * CK);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          bf16x8_t p[3][MI], q[3][NJ];
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+              p[k][i] = Half::template frag<PKS>(plane(0, k), wi * 32 * MI + 32 * i, g, lane);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+              q[k][j] = Half::template frag<QKS>(plane(1, k), wj * 32 * NJ + 32 * j, g, lane);
+          }
+          // (p, q): lo hi, mid mid, hi lo, mid hi, hi mid, hi hi
+          constexpr int PK[6] = {2, 1, 0, 1, 0, 0}, QK[6] = {0, 1, 2, 0, 1, 0};
+#pragma unroll
+          for (int m = 0; m < 6; ++m)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+              for (int i = 0; i < MI; ++i)
+                part[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(q[QK[m]][j], p[PK[m]][i],
+                                                                     part[j][i], 0, 0, 0);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int i = 0; i < MI; ++i) acc[j][i] += part[j][i];
+    }
+    bool odd = false;  // x - x is 0 unless x is not finite
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) odd |= !(acc[j][i][v] - acc[j][i][v] == 0.0f);
+    if (__syncthreads_or(odd)) {
+      // only the results that are not finite are replaced: a row's result does
+      // not depend on what the rows beside it hold
+      f32x16_t again[NJ][MI];
+      Exact::run_in(w, again, lds());
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+          for (int v = 0; v < 16; ++v)
+            if (!(acc[j][i][v] - acc[j][i][v] == 0.0f)) acc[j][i][v] = again[j][i][v];
+    }
+  }
+
+  template <typename TO, typename TA>
+  static __device__ __forceinline__ void write(f32x16_t (&acc)[NJ][MI], TO* C, int64_t ldc,
+                                               const TA* add, int64_t lda, int rows, int cols) {
+    write_quads<SplitCore>(acc, C, ldc, add, lda, rows, cols);
   }
 };
 
@@ -787,5 +927,9 @@ template <typename T, typename R>
 bool pick_any_large(R&& rows, int64_t cols, int64_t k) {
   return pick_shape(sizeof(T) == 2 ? kShapeAnyBf16 : kShapeAnyFp32, rows, cols, k) == 0;
 }
+
+// The core of operands that the DMA core does not take.
+template <typename T, bool PKS, bool QKS, int B>
+using OtherCore = std::conditional_t<sizeof(T) == 4, SplitCore<PKS, QKS, B>, AnyCore<T, PKS, QKS, B>>;
 
 }  // namespace muon

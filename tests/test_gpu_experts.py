@@ -185,3 +185,44 @@ def test_gradients_are_the_adjoints_of_the_product(gpu):
     y2 = M.expert_matmul(x, w2, o)
     diff = float(((y2.double() - y.double()) * dy.double()).sum())
     assert abs(diff - float(dw[2, 5, 6])) <= tol
+
+
+@pytest.mark.parametrize("k", [40, 264])
+def test_fp32_values_at_the_ends_of_the_range(gpu, k):
+    # not finite; the largest fp32 (whose nearest bf16 is infinite); results
+    # that overflow; operands near the smallest normal
+    x = torch.ones(200, k, device=gpu)
+    w = torch.ones(2, k, 70, device=gpu)
+    big = float(torch.finfo(torch.float32).max)
+    x[3] = float("nan")
+    x[5, 1] = float("inf")
+    x[7] = 0.0
+    x[7, 2] = big
+    x[9] = big
+    x[150] = 2.0 ** -120
+    w[1, :, 69] = 2.0 ** -60
+    o = torch.tensor([0, 100, 200], dtype=torch.int32, device=gpu)
+    y = M.expert_matmul(x, w, o)
+    assert bool(y[3].isnan().all()) and bool((y[5] == float("inf")).all())
+    assert bool((y[7] == big).all()) and bool((y[9] == float("inf")).all())
+    rest = [r for r in range(100) if r not in (3, 5, 7, 9)]
+    assert bool((y[rest] == k).all())
+    assert bool((y[150, :69] == k * 2.0 ** -120).all())
+    assert bool((y[151:, 69] == k * 2.0 ** -60).all())
+
+
+def test_fp32_products_keep_fp32_accuracy(gpu):
+    # operands whose bits reach from the first to the last place: a product
+    # of two loses at most 2^-24, the sum of k as the bound at the top says,
+    # and without cancellation (all positive) that is relative to the result
+    g = torch.Generator(device=gpu)
+    g.manual_seed(8)
+    k = 300
+    x = 1.0 + torch.rand(130, k, generator=g, device=gpu)
+    w = 1.0 + torch.rand(1, k, 90, generator=g, device=gpu)
+    o = torch.tensor([0, 130], dtype=torch.int32, device=gpu)
+    want = x.double() @ w[0].double()
+    y = M.expert_matmul(x, w, o)
+    # sums of 256 restart; a random walk of their roundings stays far below
+    # the worst case, 2^-24 sqrt(256) with a factor 4 for the largest of 11700
+    assert float(((y.double() - want) / want).abs().max()) <= 4 * 16 * 2.0 ** -24
