@@ -906,7 +906,7 @@ constexpr ShapeCost kShapeTN[] = {{256, 256, 1, 1.45, 1.65, 9.0}, {128, 256, 2, 
                                   {128, 128, 2, 0.55, 1.10, 3.2}};
 // the core for any operands: 128 x 128, 64 x 64
 constexpr ShapeCost kShapeAnyBf16[] = {{128, 128, 2, 1.20, 1.85, 3.0}, {64, 64, 4, 0.70, 1.60, 2.0}};
-constexpr ShapeCost kShapeAnyFp32[] = {{128, 128, 2, 5.60, 9.40, 3.0}, {64, 64, 4, 2.40, 5.40, 2.0}};
+constexpr ShapeCost kShapeAnyFp32[] = {{128, 128, 2, 3.80, 5.80, 6.0}, {64, 64, 4, 1.80, 4.10, 2.5}};
 // rows(bm): row tiles of bm rows
 template <int N, typename R>
 Shape pick_shape(const ShapeCost (&c)[N], R&& rows, int64_t cols, int64_t k) {
