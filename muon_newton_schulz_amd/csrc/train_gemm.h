@@ -547,10 +547,11 @@ struct DmaCore {
   static constexpr int NP = PB / 4096, NQ = QB / 4096;      // DMA per wave and stage
   static constexpr int kSlotBytes = PB + QB;
   static constexpr bool kGrid = true;  // rows on the 16-byte grid
+  static constexpr bool kWhole = NS == 2;  // run(): a stage's fragments in registers
   static constexpr int kLdsBytes = kSlotBytes;  // of lds()
   // waves per SIMD: what the LDS allows of workgroups per CU
   static constexpr int kWaves = 160 * 1024 / (NS * kSlotBytes) < 3 ? 160 * 1024 / (NS * kSlotBytes) : 3;
-  static_assert(BK == 32 || BK == 64, "");
+  static_assert(BK == 64 || (BK == 32 && !kWhole), "a stage of two slots is four k steps");
   static_assert(PB % 4096 == 0 && QB % 4096 == 0, "whole DMA instructions for four waves");
 
   template <int S>
@@ -695,68 +696,146 @@ struct DmaCore {
     else wait_counts<0>();
     pipe_barrier();
 
-    Frags f[2];
     auto read = [&](Frags& fr, auto slot_c, int g, auto r_c) {
       constexpr int r = decltype(r_c)::value;
       const char* tile = slot<decltype(slot_c)::value>();
       if constexpr (r < MI) fr.p[r] = frag<PKS, BM>(tile, ri, r, g, lane);
       else fr.q[r - MI] = frag<QKS, BN>(tile + PB, rj, r - MI, g, lane);
     };
-    static_for<0, MI + NJ>([&](auto r) { read(f[0], Int<0>{}, 0, r); });
+    auto mfma = [&](Frags& fr, auto m_c) {
+      constexpr int m = decltype(m_c)::value;
+      acc[m / MI][m % MI] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+          fr.q[m / MI], fr.p[m % MI], acc[m / MI][m % MI], 0, 0, 0);
+    };
+    constexpr int M = MI * NJ, R = MI + NJ;  // MFMAs and fragments of a k step
 
-    // One stage: the matrix instructions of a k step run while the next
-    // step's fragments are read.  Before the last step every wave has its
-    // fragments of this stage and waits for the next stage's data; behind
-    // the barrier the next stage is whole and this stage's slot is free, and
-    // stage kt + NS goes into it.  STEADY: there is such a stage.
-    auto stage = [&](int kt, auto slot_c, auto steady_c) {
-      constexpr int S = decltype(slot_c)::value;
-      constexpr bool STEADY = decltype(steady_c)::value;
-      static_for<0, SK>([&](auto g_c) {
-        constexpr int g = decltype(g_c)::value;
-        constexpr bool last = g == SK - 1;
-        Frags& cur = f[g & 1];
-        Frags& nxt = f[(g + 1) & 1];
-        if constexpr (last) {
-          if constexpr (STEADY) wait_counts<(NS - 2) * DPS>();
-          else landed(nk - 2 - kt);
-          pipe_barrier();
-          if constexpr (!STEADY) {
-            if (kt + NS < nk) issue(kt + NS, slot_c);
-          }
-          __builtin_amdgcn_sched_barrier(0);
-        }
-        static_for<0, MI * NJ>([&](auto m_c) {
-          constexpr int m = decltype(m_c)::value;
-          acc[m / MI][m % MI] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-              cur.q[m / MI], cur.p[m % MI], acc[m / MI][m % MI], 0, 0, 0);
-          // (behind the last stage the reads find old data, which is not used)
-          constexpr int RM = MI * NJ < MI + NJ ? MI * NJ : MI + NJ;
-          if constexpr (m < RM)
-            static_for<m * (MI + NJ) / RM, (m + 1) * (MI + NJ) / RM>([&](auto r_c) {
-              if constexpr (!last) read(nxt, slot_c, g + 1, r_c);
-              else read(nxt, Int<(S + 1) % NS>{}, 0, r_c);
-            });
-          // the refill's DMA spread over the step's second part
-          if constexpr (last && STEADY) {
-            constexpr int M0 = MI + NJ < MI * NJ ? MI + NJ : 0, MS = MI * NJ - M0;
-            if constexpr (m >= M0)
-              static_for<(m - M0) * DPS / MS, (m - M0 + 1) * DPS / MS>(
-                  [&](auto d_c) { issue1(kt + NS, slot_c, d_c); });
-          }
+    if constexpr (kWhole) {
+      // Two slots of four k steps, the fragments of a whole stage in
+      // registers.  A slot is read in two steps' time (the last step of the
+      // stage before and the first of its own) and then free: the DMA of stage
+      // kt + 2 goes out in step 1 of stage kt and is needed in step 3 of stage
+      // kt + 1, six k steps later.  With fragments of two steps only, a slot
+      // is free behind step 2 and the DMA has four.  The two measured, us:
+      // loss 4096 x 163840 x 7168 (256 x 256) 7185 against 7340, experts'
+      // products 65536 rows of 128 (256 x 256 NT) 2155 against 2214, 700 rows
+      // of 20 (128 x 128 NN) 13.4 against 16.4, loss 33 x 32000 x 2048 30.5
+      // against 32.7, 1024 x 50048 x 1024 113 against 115.
+      Frags f[4];
+      constexpr int RM = M * 3 / 4;  // reads are spread over the first RM MFMAs
+      static_for<0, R>([&](auto r) { read(f[0], Int<0>{}, 0, r); });
+      static_for<0, R>([&](auto r) { read(f[1], Int<0>{}, 1, r); });
+      auto reads = [&](auto slot_c, auto g_c, auto m_c) {
+        constexpr int m = decltype(m_c)::value, g = decltype(g_c)::value;
+        if constexpr (m < RM)
+          static_for<m * 2 * R / RM, (m + 1) * 2 * R / RM>([&](auto i_c) {
+            constexpr int i = decltype(i_c)::value;
+            read(f[g + i / R], slot_c, g + i / R, Int<i % R>{});
+          });
+      };
+      auto stage = [&](int kt, auto slot_c, auto steady_c) {
+        constexpr int S = decltype(slot_c)::value;
+        constexpr bool STEADY = decltype(steady_c)::value;
+        static_for<0, M>([&](auto m_c) {
+          mfma(f[0], m_c);
+          reads(slot_c, Int<2>{}, m_c);
           __builtin_amdgcn_sched_barrier(0);
         });
-      });
-    };
-    static_assert(SK % 2 == 0, "fragment buffers alternate evenly over a stage");
-    int kt = 0;
-    for (; kt + 2 * NS <= nk; kt += NS)
-      static_for<0, NS>([&](auto s) { stage(kt + decltype(s)::value, s, std::true_type{}); });
-    for (; kt < nk; kt += NS)
-      static_for<0, NS>([&](auto s) {
-        if (kt + decltype(s)::value < nk)
-          stage(kt + decltype(s)::value, s, std::false_type{});
-      });
+        wait_counts<63>();  // this wave has read the slot
+        pipe_barrier();     // so has everybody
+        if constexpr (!STEADY) {
+          if (kt + 2 < nk) issue(kt + 2, slot_c);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        static_for<0, M>([&](auto m_c) {
+          constexpr int m = decltype(m_c)::value;
+          mfma(f[1], m_c);
+          if constexpr (STEADY)
+            static_for<m * DPS / M, (m + 1) * DPS / M>(
+                [&](auto d_c) { issue1(kt + 2, slot_c, d_c); });
+          __builtin_amdgcn_sched_barrier(0);
+        });
+        static_for<0, M>([&](auto m_c) {
+          mfma(f[2], m_c);
+          __builtin_amdgcn_sched_barrier(0);
+        });
+        if (STEADY || kt + 2 < nk) wait_counts<DPS>();
+        else wait_counts<0>();
+        pipe_barrier();  // the next stage is whole
+        __builtin_amdgcn_sched_barrier(0);
+        static_for<0, M>([&](auto m_c) {
+          mfma(f[3], m_c);
+          // (behind the last stage the reads find old data, which is not used)
+          reads(Int<S ^ 1>{}, Int<0>{}, m_c);
+          __builtin_amdgcn_sched_barrier(0);
+        });
+      };
+      int kt = 0;
+      for (; kt + 4 <= nk; kt += 2) {
+        stage(kt, Int<0>{}, std::true_type{});
+        stage(kt + 1, Int<1>{}, std::true_type{});
+      }
+      for (; kt < nk; kt += 2) {
+        stage(kt, Int<0>{}, std::false_type{});
+        if (kt + 1 < nk) stage(kt + 1, Int<1>{}, std::false_type{});
+      }
+    } else {
+      Frags f[2];
+      static_for<0, MI + NJ>([&](auto r) { read(f[0], Int<0>{}, 0, r); });
+
+      // One stage: the matrix instructions of a k step run while the next
+      // step's fragments are read.  Before the last step every wave has its
+      // fragments of this stage and waits for the next stage's data; behind
+      // the barrier the next stage is whole and this stage's slot is free, and
+      // stage kt + NS goes into it.  STEADY: there is such a stage.
+      auto stage = [&](int kt, auto slot_c, auto steady_c) {
+        constexpr int S = decltype(slot_c)::value;
+        constexpr bool STEADY = decltype(steady_c)::value;
+        static_for<0, SK>([&](auto g_c) {
+          constexpr int g = decltype(g_c)::value;
+          constexpr bool last = g == SK - 1;
+          Frags& cur = f[g & 1];
+          Frags& nxt = f[(g + 1) & 1];
+          if constexpr (last) {
+            if constexpr (STEADY) wait_counts<(NS - 2) * DPS>();
+            else landed(nk - 2 - kt);
+            pipe_barrier();
+            if constexpr (!STEADY) {
+              if (kt + NS < nk) issue(kt + NS, slot_c);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          static_for<0, MI * NJ>([&](auto m_c) {
+            constexpr int m = decltype(m_c)::value;
+            acc[m / MI][m % MI] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                cur.q[m / MI], cur.p[m % MI], acc[m / MI][m % MI], 0, 0, 0);
+            // (behind the last stage the reads find old data, which is not used)
+            constexpr int RM = MI * NJ < MI + NJ ? MI * NJ : MI + NJ;
+            if constexpr (m < RM)
+              static_for<m * (MI + NJ) / RM, (m + 1) * (MI + NJ) / RM>([&](auto r_c) {
+                if constexpr (!last) read(nxt, slot_c, g + 1, r_c);
+                else read(nxt, Int<(S + 1) % NS>{}, 0, r_c);
+              });
+            // the refill's DMA spread over the step's second part
+            if constexpr (last && STEADY) {
+              constexpr int M0 = MI + NJ < MI * NJ ? MI + NJ : 0, MS = MI * NJ - M0;
+              if constexpr (m >= M0)
+                static_for<(m - M0) * DPS / MS, (m - M0 + 1) * DPS / MS>(
+                    [&](auto d_c) { issue1(kt + NS, slot_c, d_c); });
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          });
+        });
+      };
+      static_assert(SK % 2 == 0, "fragment buffers alternate evenly over a stage");
+      int kt = 0;
+      for (; kt + 2 * NS <= nk; kt += NS)
+        static_for<0, NS>([&](auto s) { stage(kt + decltype(s)::value, s, std::true_type{}); });
+      for (; kt < nk; kt += NS)
+        static_for<0, NS>([&](auto s) {
+          if (kt + decltype(s)::value < nk)
+            stage(kt + decltype(s)::value, s, std::false_type{});
+        });
+    }
   }
 
   // C[i][j] = acc (+ add[i][j]) for i < rows, j < cols.  add may be C.  The
@@ -852,13 +931,13 @@ struct DmaCore {
   }
 };
 
-// The tile shapes of the DMA core.  Large: the least operand traffic for a flop (512 rows and
-// columns of operands for 256 x 256 results), one workgroup to a CU, so
-// nothing hides its prologue and epilogue.  Half and Medium: two workgroups
+// The tile shapes of the DMA core.  Large: the least operand traffic for a
+// flop (512 rows and columns of operands for 256 x 256 results), one
+// workgroup to a CU, so nothing hides its prologue and epilogue.  Half and Medium: two workgroups
 // to a CU.  Thin: a deep ring for streaming Q past a few rows of P.
 // K-contiguous operands take 64 k a stage, whole 128-byte lines; K-strided
 // ones always read whole lines and take 32, which doubles the stages in
-// flight.  Large NN (one of each) measured 2323 us with 32 k and 2473 with
+// flight.  Large NN (one of each) measured 2147 us with 32 k and 2200 with
 // 64 (65536 rows, 128 experts of 7168 x 2048).
 template <bool PKS, bool QKS>
 using LargeCore = DmaCore<PKS, QKS, 256, 256, 2, (PKS || QKS) ? 32 : 64, (PKS || QKS) ? 4 : 2>;
@@ -876,11 +955,11 @@ using ThinCore = DmaCore<PKS, QKS, 32, 128, 1, 64, 6>;
 // whole ones while they are few.  The constants are fits to measured
 // products of 8 to 65536 rows, 1 to 128 experts, sides 1000 to 7168 and 32000
 // to 163840 vocabulary rows; some of what they rest on (us, shape by shape):
-//   8 rows x 64 experts 2048x1408 (NN): Thin 11.8, Medium 21.5, Half 24, Large 43
-//   700 rows x 20 experts 1280x1024 (NN): Medium 16.5, Half 18.2, Thin 20.5, Large 30
-//   8192 rows x 16 experts 1024x2048 (TN): Half 41.0, Medium 47.9, Large 48.2
-//   loss 1024 x 50048 x 1024 (NT): Medium 164, Large 198, Half 255
-//   loss 4096 x 163840 x 7168 (NT): Large 7900, Medium 9530, Half 10240
+//   8 rows x 64 experts 2048x1408 (NN): Thin 12.1, Medium 17.2, Half 24.9, Large 38.8
+//   700 rows x 20 experts 1280x1024 (NN): Medium 13.5, Thin 14.5, Half 18.9, Large 27.9
+//   8192 rows x 16 experts 1024x2048 (TN): Half 43.0, Large 46.0, Medium 47.9
+//   loss 1024 x 50048 x 1024 (NT): Medium 115, Half 118, Large 133, Thin 356
+//   loss 4096 x 163840 x 7168 (NT): Large 7240, Medium 8700, Half 9720
 struct ShapeCost {
   int bm, bn, per_cu;
   double alone, full, fixed;
