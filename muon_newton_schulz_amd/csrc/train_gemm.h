@@ -952,7 +952,9 @@ using ThinCore = DmaCore<PKS, QKS, 32, 128, 1, 64, 6>;
 // stage x K / 64 + fixed microseconds, where the time of 64 k grows from
 // `alone` to `full` with the number of workgroups that share the GPU (matrix
 // cores of their CU, memory); tiles beyond one a place take further rounds,
-// whole ones while they are few.  The constants are fits to measured
+// the last with the time of the tiles that are left for it (counting it as a
+// whole one kept loss 1024 x 50048 x 1024 and 1500 x 50304 x 768 from the
+// better tiles: backward 349 and 385 us against 364 and 403).  The constants are fits to measured
 // products of 8 to 65536 rows, 1 to 128 experts, sides 1000 to 7168 and 32000
 // to 163840 vocabulary rows; some of what they rest on (us, shape by shape):
 //   8 rows x 64 experts 2048x1408 (NN): Thin 12.1, Medium 17.2, Half 24.9, Large 38.8
@@ -967,14 +969,13 @@ struct ShapeCost {
 inline double shape_time(const ShapeCost& c, double row_tiles, int64_t cols, int64_t k) {
   const double tiles = row_tiles * static_cast<double>((cols + c.bn - 1) / c.bn);
   const double places = 256.0 * c.per_cu;
-  const double load = std::fmin(1.0, std::fmax(0.0, (tiles - 128.0) / (places - 128.0)));
-  double rounds = 1.0;
-  if (tiles > places) {
-    const double r = tiles / places;
-    rounds = r < 8.0 ? std::ceil(r) : r + 0.5;
-  }
-  const double stage = c.alone + (c.full - c.alone) * load;
-  return rounds * (static_cast<double>(k) / 64.0 * stage + c.fixed);
+  auto round = [&](double n) {  // n workgroups
+    const double load = std::fmin(1.0, std::fmax(0.0, (n - 128.0) / (places - 128.0)));
+    return static_cast<double>(k) / 64.0 * (c.alone + (c.full - c.alone) * load) + c.fixed;
+  };
+  if (tiles >= 8.0 * places) return (tiles / places + 0.5) * round(places);
+  const double whole = std::floor(tiles / places), rest = tiles - whole * places;
+  return whole * round(places) + (rest > 0.0 ? round(rest) : 0.0);
 }
 enum Shape { kLarge, kHalf, kMedium, kThin };
 constexpr ShapeCost kShapeNT[] = {{256, 256, 1, 1.40, 1.72, 12.0}, {128, 256, 2, 1.40, 2.45, 4.0},
