@@ -512,7 +512,7 @@ int embed_backward(const void* dout, int32_t dout_dtype, int64_t ld_dout, const 
  * A row whose target lies outside [0, vocab) (an ignore index such as -100)
  * has loss 0 and no gradient.  Types: hidden and weight share dtype; logits,
  * statistics and sums are fp32; backward's g (below), over the largest
- * |dloss|, is rounded to dtype before its products.  vocab <= 2^21.
+ * |dloss|, is rounded to dtype before its products.  n <= 2^24, vocab <= 2^21.
  * A NaN in a row's logits makes its loss and lse NaN. */
 
 /* Device workspace of the two calls below: with backward != 0 enough for

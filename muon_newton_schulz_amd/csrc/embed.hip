@@ -641,11 +641,16 @@ int check_sizes(int64_t n, int64_t vocab, int64_t dim, float scale) {
 template <typename TT, typename TO, typename ID>
 void run_fwd(const void* table, const void* ids, int64_t n, int64_t vocab, int64_t dim,
              float scale, void* out, int64_t ld, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>((n + kRows - 1) / kRows),
-                  static_cast<unsigned>((dim + kCols - 1) / kCols));
-  hipLaunchKernelGGL((k_embed_fwd<TT, TO, ID>), grid, dim3(kThreads), 0, s,
-                     static_cast<const TT*>(table), static_cast<const ID*>(ids), n, vocab, dim,
-                     scale, static_cast<TO*>(out), ld);
+  // a launch holds fewer than 2^32 threads along x
+  constexpr int64_t kMost = int64_t{1} << 25;
+  const unsigned ny = static_cast<unsigned>((dim + kCols - 1) / kCols);
+  for (int64_t t0 = 0; t0 < n; t0 += kMost) {
+    const int64_t m = std::min(n - t0, kMost);
+    hipLaunchKernelGGL((k_embed_fwd<TT, TO, ID>),
+                       dim3(static_cast<unsigned>((m + kRows - 1) / kRows), ny), dim3(kThreads), 0,
+                       s, static_cast<const TT*>(table), static_cast<const ID*>(ids) + t0, m,
+                       vocab, dim, scale, static_cast<TO*>(out) + t0 * ld, ld);
+  }
 }
 
 // Workgroups that zero `bytes`: enough to reach the write rate, few enough

@@ -403,7 +403,10 @@ constexpr int64_t kStatsRows = 16384;
 // fp32 sums of dh; g should stay near what the last-level cache holds.
 constexpr int64_t kPieceBytes = static_cast<int64_t>(256) << 20;
 constexpr int64_t kMinPiece = 2048, kPieceStep = 256;  // whole tiles
-constexpr int64_t kMaxVocabLoss = static_cast<int64_t>(1) << 21;  // kStatsRows x this in 64 x 64 tiles fits a launch
+// A launch holds fewer than 2^24 workgroups of 256: kStatsRows x kMaxVocabLoss
+// and kMaxTokensLoss x kMinPiece in 64 x 64 tiles are at most 2^23.
+constexpr int64_t kMaxVocabLoss = static_cast<int64_t>(1) << 21;
+constexpr int64_t kMaxTokensLoss = static_cast<int64_t>(1) << 24;
 // Shares of dh's sum at most: the tiles of the core for any operands take
 // longer, and gain from more (515 x 33001 x 500, g and dh: fp32 540 us with
 // 16, 411 with 25; bf16 151 and 121; DMA core, 33 x 32000 x 2048: 54 and 59).
@@ -616,6 +619,7 @@ int check_loss(int64_t n, int64_t vocab, int64_t dim, int64_t ldh, int32_t dtype
   if (rc != MUON_OK) return rc;
   if (vocab > kMaxVocabLoss)
     return set_error(MUON_ERR_UNSUPPORTED, "vocab must be at most 2^21");
+  if (n > kMaxTokensLoss) return set_error(MUON_ERR_UNSUPPORTED, "n must be at most 2^24");
   if (!train_dtype_ok(dtype))
     return set_error(MUON_ERR_BAD_DTYPE, "hidden and weight must be fp32 or bf16");
   if (ldh < dim) return set_error(MUON_ERR_BAD_SHAPE, "ld_hidden < dim");

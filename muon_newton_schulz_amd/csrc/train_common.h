@@ -61,8 +61,7 @@ __device__ __forceinline__ void store8(float* p, const float* v) { __builtin_mem
 
 inline bool train_dtype_ok(int32_t d) { return d == MUON_DTYPE_FP32 || d == MUON_DTYPE_BF16; }
 inline size_t train_dtype_size(int32_t d) { return d == MUON_DTYPE_FP32 ? 4 : 2; }
-// Positions are 32-bit in the kernels, and a launch's threads (64 for each
-// position at most) stay below 2^32.
+// Positions are 32-bit in the kernels.
 constexpr int64_t kMaxTokens = (static_cast<int64_t>(1) << 26) - 1;
 constexpr int64_t kMaxVocab = (static_cast<int64_t>(1) << 31) - 2;
 constexpr int64_t kMaxDim = static_cast<int64_t>(1) << 22;

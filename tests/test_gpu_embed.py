@@ -86,6 +86,16 @@ def test_lookup_of_non_finite_rows_and_offsets_past_32_bits(gpu):
     assert float(table[1:vocab - 2].float().abs().max()) == 0.0
 
 
+def test_lookup_of_the_most_positions(gpu):
+    # 2^26 - 1 positions: more than one launch holds
+    n, vocab = (1 << 26) - 1, 97
+    table = torch.arange(vocab, device=gpu, dtype=torch.bfloat16).view(vocab, 1)
+    ids = torch.arange(n, device=gpu, dtype=torch.int32).remainder_(vocab + 1)  # vocab: no row
+    out = M.embed_forward(table, ids)
+    want = torch.where(ids < vocab, ids, torch.zeros_like(ids)).to(torch.bfloat16)
+    assert torch.equal(out.view(n), want)
+
+
 @pytest.mark.parametrize("n,vocab,dim,dd,gd,idt,kind,acc,off,pad", [
     (0, 40, 9, "bf16", "bf16", torch.int64, "uniform", False, 1, 0),
     (0, 40, 9, "bf16", "bf16", torch.int64, "uniform", True, 1, 0),

@@ -183,6 +183,17 @@ def test_loss_entry_points_refuse():
     assert bwd(n=0, dw=None) == M.MUON_OK and bwd(n=0, acc=1) == M.MUON_OK
 
 
+def test_loss_refuses_more_rows_than_a_launch_holds():
+    p = ctypes.c_void_p(256)
+    n = (1 << 24) + 1
+    assert M.lm_loss_workspace_size(n, 10, 8, "bf16") == 0
+    assert M.lm_loss_workspace_size(n - 1, 10, 8, "bf16") > 0
+    assert _rc("lm_loss_forward", p, 8, p, 1, p, 1, n, 10, 8, p, p, p, 1 << 40, None) == \
+        M.MUON_ERR_UNSUPPORTED
+    assert _rc("lm_loss_backward", p, 8, p, 1, p, 1, n, 10, 8, p, p, p, 1, 8, p, 1, 0, p, 1 << 40,
+               None) == M.MUON_ERR_UNSUPPORTED
+
+
 def test_expert_binding_checks():
     x, w, o = Fake((40, 16)), Fake((5, 16, 24)), Fake((6,), torch.int32)
     f = M.expert_matmul
