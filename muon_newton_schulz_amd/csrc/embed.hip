@@ -530,8 +530,10 @@ __global__ __launch_bounds__(kSumThreads) void k_embed_direct(
     for (int i = t; i < zero_len / 32; i += kSumThreads) bits[i] = 0u;
     __syncthreads();
     for (int i = t; i < n; i += kSumThreads) {
-      const int64_t v = static_cast<int64_t>(ids[i]) - r0;
-      if (v >= 0 && v < zero_len) atomicOr(&bits[v >> 5], 1u << (v & 31));
+      const int64_t id = static_cast<int64_t>(ids[i]);
+      if (id < r0 || id >= r0 + zero_len) continue;
+      const int v = static_cast<int>(id - r0);
+      atomicOr(&bits[v >> 5], 1u << (v & 31));
     }
     __syncthreads();
     for (int i = 0; i < zero_len / 32 && r0 + 32 * i < vocab; ++i)
