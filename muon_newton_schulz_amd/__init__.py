@@ -732,6 +732,26 @@ def _one_device(**tensors):
     return dev
 
 
+def _apart(name: str, out, rows: int, cols: int, ld: int, **inputs):
+    """Refuses an output of ``rows`` x ``cols``, row stride ``ld``, that shares
+    memory with an input, given as (tensor, rows, cols, row stride): the
+    kernels read inputs after they have written outputs.  Columns of one
+    buffer beside each other are apart."""
+    e = out.element_size()
+    a, row, step = out.data_ptr(), cols * e, ld * e
+    end = a + (rows - 1) * step + row
+    for other, (t, r, c, l) in inputs.items():
+        if r == 0 or rows == 0:
+            continue
+        b, e = t.data_ptr(), t.element_size()
+        if b >= end or a >= b + ((r - 1) * l + c) * e:
+            continue
+        gap = (b - a) % step
+        if l * e == step and rows > 1 and r > 1 and gap >= row and gap + c * e <= step:
+            continue
+        raise MuonError(MUON_ERR_INVALID_ARG, f"{name} shares memory with {other}")
+
+
 def _current_handle(dev) -> int:
     """hipStream_t of the current stream of ``dev`` (the raw query where torch
     has it: the Stream object costs more than the rest of a small call)."""
@@ -807,6 +827,8 @@ def embed_forward(table, ids, scale: float = 1.0, out=None, out_dtype=None, stre
         if out_dtype is not None and dtype_code(out_dtype) != dtype_code(out.dtype):
             raise MuonError(MUON_ERR_BAD_DTYPE, f"out has dtype {out.dtype}, not {out_dtype}")
     dev = _one_device(table=table, ids=ids, out=out)
+    if out is not None:
+        _apart("out", out, n, dim, ld, table=(table, vocab, dim, dim))
     with _Launch(dev, stream) as on:
         if out is None:
             td = {MUON_DTYPE_FP32: torch.float32, MUON_DTYPE_BF16: torch.bfloat16}
@@ -838,6 +860,7 @@ def embed_backward(dout, ids, dtable, scale: float = 1.0, accumulate: bool = Fal
     n = ids.numel()
     ld = _rows(dout, "dout", n, dim)
     dev = _one_device(dtable=dtable, ids=ids, dout=dout, workspace=workspace)
+    _apart("dtable", dtable, vocab, dim, dim, dout=(dout, n, dim, ld))
     with _Launch(dev, stream) as on:
         ws = _workspace(workspace, embed_backward_workspace_size(n, vocab, dim), dev)
         _check(lib().embed_backward(_ptr(dout), dtype_code(dout.dtype), ld, _ptr(ids), i64, n,
@@ -877,6 +900,8 @@ def lm_loss_forward(hidden, weight, targets, loss=None, lse=None, workspace=None
             _block(t, name, (n,), F32)
     dev = _one_device(weight=weight, hidden=hidden, targets=targets, loss=loss, lse=lse,
                       workspace=workspace)
+    if loss is not None and lse is not None:
+        _apart("loss", loss, 1, n, n, lse=(lse, 1, n, n))
     with _Launch(dev, stream) as on:
         if loss is None:
             loss = torch.empty(n, dtype=torch.float32, device=dev)
@@ -911,6 +936,13 @@ def lm_loss_backward(hidden, weight, targets, lse, dloss, dhidden=None, dweight=
     dev = _one_device(weight=weight, hidden=hidden, targets=targets, lse=lse, dloss=dloss,
                       dhidden=None if dhidden is False else dhidden,
                       dweight=None if dweight is False else dweight, workspace=workspace)
+    ins = {"hidden": (hidden, n, dim, ld), "weight": (weight, vocab, dim, dim)}
+    if dhidden is not None and dhidden is not False:
+        _apart("dhidden", dhidden, n, dim, ld_dh, **ins)
+    if dweight is not None and dweight is not False:
+        _apart("dweight", dweight, vocab, dim, dim, **ins)
+        if dhidden is not None and dhidden is not False:
+            _apart("dweight", dweight, vocab, dim, dim, dhidden=(dhidden, n, dim, ld_dh))
     with _Launch(dev, stream) as on:
         if dhidden is None:
             dhidden = torch.empty((n, dim), dtype=hidden.dtype, device=dev)
@@ -968,6 +1000,8 @@ def expert_matmul(x, w, offsets, trans: bool = False, out=None, out_dtype=None, 
         if out_dtype is not None and dtype_code(out_dtype) != dtype_code(out.dtype):
             raise MuonError(MUON_ERR_BAD_DTYPE, f"out has dtype {out.dtype}, not {out_dtype}")
     dev = _one_device(w=w, x=x, offsets=offsets, out=out)
+    if out is not None:
+        _apart("out", out, rows, n, ldy, x=(x, rows, k, ldx), w=(w, experts * k, n, n))
     with _Launch(dev, stream) as on:
         if out is None:
             td = {MUON_DTYPE_FP32: torch.float32, MUON_DTYPE_BF16: torch.bfloat16}
@@ -996,6 +1030,7 @@ def expert_wgrad(a, b, offsets, dw, accumulate: bool = False, stream=None):
     ldb = _rows(b, "b", rows, n, (dtype_code(a.dtype),))
     _offsets(offsets, experts)
     dev = _one_device(dw=dw, a=a, b=b, offsets=offsets)
+    _apart("dw", dw, experts * m, n, n, a=(a, rows, m, lda), b=(b, rows, n, ldb))
     with _Launch(dev, stream) as on:
         _check(lib().expert_wgrad(_ptr(a), lda, _ptr(b), ldb, dtype_code(a.dtype), _ptr(offsets),
                                   experts, rows, m, n, _ptr(dw), dtype_code(dw.dtype),

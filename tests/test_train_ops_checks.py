@@ -245,3 +245,69 @@ def test_expert_entry_points_refuse():
     for k in ("a", "b", "off", "dw"):
         assert wg(**{k: None}) == INVALID
     assert wg(rows=0, a=None, b=None, acc=1) == M.MUON_OK
+
+
+class Placed(Fake):
+    """A stand-in at an address of its own."""
+
+    def __init__(self, at, shape, dtype=torch.bfloat16, stride=None):
+        super().__init__(shape, dtype, stride)
+        self._at = at
+
+    def data_ptr(self):
+        return self._at
+
+
+def test_outputs_that_share_memory_with_inputs_are_refused():
+    f32, ids = torch.float32, Fake((6,), I64)
+    at = 1 << 20
+    table = Placed(at, (100, 16))  # 3200 bytes
+    _err(INVALID, M.embed_forward, table, ids, out=Placed(at, (6, 16)))
+    _err(INVALID, M.embed_forward, table, ids, out=Placed(at + 3198, (6, 16)))
+    _err(INVALID, M.embed_forward, table, ids, out=Placed(at - 190, (6, 16)))
+    _err(INVALID, M.embed_forward, table, ids, out=Placed(at - 190, (6, 16), stride=(17, 1)))
+    _err(INVALID, M.embed_backward, Placed(at + 64, (6, 16)), ids, table)
+    h, t = Placed(at, (6, 16), stride=(48, 1)), ids
+    w = Placed(at + 4096, (100, 16))
+    lse, dl = Fake((6,), f32), Fake((6,), f32)
+    loss = Placed(at, (6,), f32)
+    _err(INVALID, M.lm_loss_forward, h, w, t, loss=loss, lse=loss)
+    b = M.lm_loss_backward
+    _err(INVALID, b, h, w, t, lse, dl, dhidden=h)
+    # columns [8, 24) of the buffer whose columns [0, 16) are hidden
+    _err(INVALID, b, h, w, t, lse, dl, dhidden=Placed(at + 16, (6, 16), stride=(48, 1)))
+    # columns [40, 56): the last ones are the next row's first
+    _err(INVALID, b, h, w, t, lse, dl, dhidden=Placed(at + 80, (6, 16), stride=(48, 1)))
+    _err(INVALID, b, h, w, t, lse, dl, dhidden=Placed(at + 32, (6, 16), stride=(47, 1)))
+    _err(INVALID, b, h, w, t, lse, dl, dweight=w)
+    _err(INVALID, b, h, w, t, lse, dl, dhidden=False, dweight=Placed(at + 100, (100, 16)))
+    far = 1 << 30
+    _err(INVALID, b, h, w, t, lse, dl, dhidden=Placed(far, (6, 16)),
+         dweight=Placed(far - 3198, (100, 16)))
+    x, o = Placed(at, (40, 24)), Fake((6,), torch.int32)
+    w3 = Placed(far, (5, 24, 24))
+    _err(INVALID, M.expert_matmul, x, w3, o, out=x)
+    _err(INVALID, M.expert_matmul, x, w3, o, trans=True, out=Placed(far + 5758, (40, 24)))
+    _err(INVALID, M.expert_wgrad, x, Placed(far, (40, 24)), o, Placed(at - 2, (5, 24, 24), f32))
+    _err(INVALID, M.expert_wgrad, x, Placed(far, (40, 24)), o, Placed(far + 1918, (5, 24, 24), f32))
+
+
+def test_memory_beside_an_input_is_no_overlap():
+    at = 1 << 20
+    a = Placed(at, (6, 16), stride=(48, 1))
+
+    def apart(p, stride=48, cols=16, rows=6):
+        M._apart("out", Placed(p, (rows, cols)), rows, cols, stride, a=(a, 6, 16, 48))
+
+    apart(at + 32)
+    apart(at + 64)
+    apart(at - 32)
+    apart(at - 6 * 96 + 96 - 32)      # before the buffer's first row
+    apart(at + 6 * 96 - 64, 16)       # from the byte after the last row
+    apart(at, rows=0)
+    with pytest.raises(M.MuonError):
+        apart(at + 30)
+    with pytest.raises(M.MuonError):
+        apart(at + 66)
+    with pytest.raises(M.MuonError):
+        apart(at + 6 * 96 - 66, 16)
