@@ -59,6 +59,11 @@ __device__ __forceinline__ int scan_row_tiles(const int32_t* off, int experts, i
   return base;
 }
 
+// Row tiles that any group sizes can need.
+__host__ __device__ __forceinline__ int most_row_tiles(int rows, int experts, int bm) {
+  return rows / bm + (experts < rows ? experts : rows);
+}
+
 struct MatmulArgs {
   const void* x;
   const void* w;
@@ -79,7 +84,10 @@ struct MatmulTile : TileArgs<T> {
 template <typename Core, typename T, bool QKS, typename TO>
 __global__ __launch_bounds__(kThreads, Core::kWaves) void k_expert_matmul(MatmulArgs a, int ny) {
   using W = MatmulTile<T>;
-  const int nx = scan_row_tiles<false>(a.off, a.experts, a.rows, Core::BM, 0, nullptr);
+  // (offsets out of order can give any number of tiles: no more than the
+  // launch's are taken)
+  const int nx = min(scan_row_tiles<false>(a.off, a.experts, a.rows, Core::BM, 0, nullptr),
+                     most_row_tiles(a.rows, a.experts, Core::BM));
   int x, y;
   if (!my_tile(nx, ny, x, y)) return;
   W w;
@@ -147,7 +155,7 @@ constexpr int kMaxExperts = 4096;
 
 template <typename Core, typename T, bool QKS, typename TO>
 void launch_matmul(const MatmulArgs& a, hipStream_t s) {
-  const int nx = a.rows / Core::BM + std::min(a.experts, a.rows);
+  const int nx = most_row_tiles(a.rows, a.experts, Core::BM);
   const int ny = (a.N + Core::BN - 1) / Core::BN;
   hipLaunchKernelGGL((k_expert_matmul<Core, T, QKS, TO>),
                      dim3(tile_blocks(nx, ny)), dim3(kThreads), 0, s, a, ny);
