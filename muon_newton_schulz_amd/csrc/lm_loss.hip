@@ -358,11 +358,11 @@ struct DwArgs {
   const void* h;
   const float* c;
   void* dw;  // the piece's first row
-  int64_t ldg, ldh;
+  int64_t ldg, ldh, vocab;
   int n, dim, len, accumulate;
 };
 
-template <typename Core, typename T, typename TO>
+template <typename Core, bool STREAM, typename T, typename TO>
 __global__ __launch_bounds__(kThreads, Core::kWaves) void k_loss_dw(DwArgs a, int nx, int ny) {
   using W = LossTile<T>;
   int x, y;
@@ -381,8 +381,8 @@ __global__ __launch_bounds__(kThreads, Core::kWaves) void k_loss_dw(DwArgs a, in
   Core::run(w, acc);
   scale_acc(acc, *a.c);
   TO* C = static_cast<TO*>(a.dw) + static_cast<int64_t>(w.i0) * a.dim + w.j0;
-  Core::write(acc, C, a.dim, a.accumulate ? C : static_cast<const TO*>(nullptr), a.dim, w.pn,
-              w.qn);
+  Core::template write<STREAM>(acc, C, a.dim, a.accumulate ? C : static_cast<const TO*>(nullptr),
+                               a.dim, w.pn, w.qn);
 }
 
 template <typename T>
@@ -553,8 +553,12 @@ template <typename Core, typename T, typename TO>
 void launch_dw(const DwArgs& a, hipStream_t s) {
   const int nx = static_cast<int>(ceil_div(a.len, Core::BM));
   const int ny = static_cast<int>(ceil_div(a.dim, Core::BN));
-  hipLaunchKernelGGL((k_loss_dw<Core, T, TO>), dim3(tile_blocks(nx, ny)),
-                     dim3(kThreads), 0, s, a, nx, ny);
+  auto* kernel = k_loss_dw<Core, false, T, TO>;
+  if constexpr (Core::kGrid) {
+    if (stream_gradient(static_cast<const TO*>(a.dw), a.vocab, a.dim))
+      kernel = k_loss_dw<Core, true, T, TO>;
+  }
+  hipLaunchKernelGGL(kernel, dim3(tile_blocks(nx, ny)), dim3(kThreads), 0, s, a, nx, ny);
 }
 template <typename T, typename TO>
 void run_dw(const DwArgs& a, bool grid, hipStream_t s) {
@@ -603,7 +607,7 @@ void run_backward(const BackwardArgs& b, const LossWs& w, hipStream_t s) {
                     grid && on_grid(b.dh, b.ld_dh, b.dim), s);
     }
     if (b.dw != nullptr)
-      run_dw<T, TW>(DwArgs{g, b.h, c, static_cast<TW*>(b.dw) + v0 * b.dim, w.ldg, b.ldh,
+      run_dw<T, TW>(DwArgs{g, b.h, c, static_cast<TW*>(b.dw) + v0 * b.dim, w.ldg, b.ldh, b.vocab,
                            static_cast<int>(b.n), static_cast<int>(b.dim), len, b.accumulate},
                     grid && on_grid(b.dw, b.dim, b.dim), s);
   }

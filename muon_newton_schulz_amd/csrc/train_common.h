@@ -50,12 +50,23 @@ __device__ __forceinline__ void load8(const uint16_t* p, float* o) {
 __device__ __forceinline__ void load8(const float* p, float* o) {
   __builtin_memcpy(o, p, 32);
 }
-__device__ __forceinline__ void store8(uint16_t* p, const float* v) {
-  const u32x4_t w = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
-                     pack_bf16(v[6], v[7])};
-  __builtin_memcpy(p, &w, 16);
+// Stores a 16-byte vector; STREAM: not to be kept in the caches (p aligned).
+template <bool STREAM, typename V>
+__device__ __forceinline__ void put16(void* p, V v) {
+  static_assert(sizeof(V) == 16, "");
+  if constexpr (STREAM) __builtin_nontemporal_store(v, static_cast<V*>(p));
+  else __builtin_memcpy(p, &v, 16);
 }
-__device__ __forceinline__ void store8(float* p, const float* v) { __builtin_memcpy(p, v, 32); }
+template <bool STREAM = false>
+__device__ __forceinline__ void store8(uint16_t* p, const float* v) {
+  put16<STREAM>(p, u32x4_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                           pack_bf16(v[6], v[7])});
+}
+template <bool STREAM = false>
+__device__ __forceinline__ void store8(float* p, const float* v) {
+  put16<STREAM>(p, f32x4_t{v[0], v[1], v[2], v[3]});
+  put16<STREAM>(p + 4, f32x4_t{v[4], v[5], v[6], v[7]});
+}
 
 // ---- host side ----
 

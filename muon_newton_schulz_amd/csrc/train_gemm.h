@@ -82,7 +82,9 @@ __device__ __forceinline__ void store_quad(TO* p, int left, f32x4_t v) {
 }
 
 // C[i][j] = acc (+ add[i][j]) for i < rows, j < cols, no alignment needed.
-// add may be C.
+// add may be C.  (Its stores are parts of lines, which the caches have to put
+// together: with nontemporal ones the weight gradient of 700 x 1281 x 1021,
+// 20 experts, took 136 us instead of 27.)
 template <typename Core, typename TO, typename TA>
 __device__ __forceinline__ void write_quads(f32x16_t (&acc)[Core::NJ][Core::MI], TO* C, int64_t ldc,
                                             const TA* add, int64_t lda, int rows, int cols) {
@@ -318,7 +320,7 @@ struct AnyCore {
     }
   }
 
-  template <typename TO, typename TA>
+  template <bool STREAM = false, typename TO, typename TA>
   static __device__ __forceinline__ void write(f32x16_t (&acc)[NJ][MI], TO* C, int64_t ldc,
                                                const TA* add, int64_t lda, int rows, int cols) {
     write_quads<AnyCore>(acc, C, ldc, add, lda, rows, cols);
@@ -454,7 +456,7 @@ struct SplitCore {
     }
   }
 
-  template <typename TO, typename TA>
+  template <bool STREAM = false, typename TO, typename TA>
   static __device__ __forceinline__ void write(f32x16_t (&acc)[NJ][MI], TO* C, int64_t ldc,
                                                const TA* add, int64_t lda, int rows, int cols) {
     write_quads<SplitCore>(acc, C, ldc, add, lda, rows, cols);
@@ -843,11 +845,12 @@ struct DmaCore {
   // Each wave turns its accumulators into rows in LDS (16-byte chunk c of row
   // i at c ^ i, in the low bits) and stores 16 bytes a lane along the rows:
   // values already in the storage type, or fp32 where something is added.
-  template <typename TO, typename TA>
+  // STREAM: nontemporal stores (stream_gradient).
+  template <bool STREAM = false, typename TO, typename TA>
   static __device__ __forceinline__ void write(f32x16_t (&acc)[NJ][MI], TO* C, int64_t ldc,
                                                const TA* add, int64_t lda, int rows, int cols) {
-    if (sizeof(TO) == 2 && add == nullptr) rows_out<TO, TA, true>(acc, C, ldc, add, lda, rows, cols);
-    else rows_out<TO, TA, false>(acc, C, ldc, add, lda, rows, cols);
+    if (sizeof(TO) == 2 && add == nullptr) rows_out<STREAM, true>(acc, C, ldc, add, lda, rows, cols);
+    else rows_out<STREAM, false>(acc, C, ldc, add, lda, rows, cols);
   }
 
   // Bytes of a staged row: up to 256, as many as leave each wave a region in
@@ -859,7 +862,7 @@ struct DmaCore {
     return rb;
   }
   // HALF: staged as bf16, else as fp32
-  template <typename TO, typename TA, bool HALF>
+  template <bool STREAM, bool HALF, typename TO, typename TA>
   static __device__ __forceinline__ void rows_out(f32x16_t (&acc)[NJ][MI], TO* C, int64_t ldc,
                                                   const TA* add, int64_t lda, int rows, int cols) {
     constexpr int ES = HALF ? 2 : 4;
@@ -907,14 +910,14 @@ struct DmaCore {
           const int i = i0 + r;
           if (i >= rows) break;
           if constexpr (HALF) {
-            *reinterpret_cast<u32x4_t*>(C + i * ldc + j) = *reinterpret_cast<u32x4_t*>(chunk(r, c));
+            put16<STREAM>(C + i * ldc + j, *reinterpret_cast<u32x4_t*>(chunk(r, c)));
           } else if constexpr (sizeof(TO) == 4) {
             f32x4_t v = *reinterpret_cast<f32x4_t*>(chunk(r, c));
             if (add != nullptr) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) v[e] += to_f32(add[i * lda + j + e]);
             }
-            *reinterpret_cast<f32x4_t*>(C + i * ldc + j) = v;
+            put16<STREAM>(C + i * ldc + j, v);
           } else {
             float v[8], o[8];
             __builtin_memcpy(v, chunk(r, 2 * c), 16);
@@ -922,7 +925,7 @@ struct DmaCore {
             load8(add + i * lda + j, o);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] += o[e];
-            store8(C + i * ldc + j, v);
+            store8<STREAM>(C + i * ldc + j, v);
           }
         }
       }
@@ -1006,6 +1009,24 @@ Shape pick_shape(const ShapeCost (&c)[N], R&& rows, int64_t cols, int64_t k) {
 template <typename T, typename R>
 bool pick_any_large(R&& rows, int64_t cols, int64_t k) {
   return pick_shape(sizeof(T) == 2 ? kShapeAnyBf16 : kShapeAnyFp32, rows, cols, k) == 0;
+}
+
+// Whether the DMA core stores a weight gradient of rows x cols past the caches,
+// which leaves them to the operands; the optimizer step reads it after the
+// whole backward.  us with and without, bf16:
+//   rows of whole 128-byte lines: 4096 rows of 64 experts, 2048 x 1408, 79 and
+//   115; 65536 of 128, 7168 x 2048, 2310 and 2410; 700 of 20, 1280 x 1024, 14.2
+//   and 14.8; loss 1024 x 50048 x 1024, backward 340 and 353
+//   others pay for the parts of lines: 4096 of 16, 1024 x 1000 (33 MB), 24.6 and
+//   17.6; 8192 of 16, 2000 x 1032 (66 MB), 56.8 and 55.6; 20000 of 16, 2040 x
+//   2056 (134 MB), 198 and 218
+// Not activations, which the next call reads: a product and the one after it,
+// 10000 rows of 16 experts, 1024 x 2816, take 140 with it and 132 without.
+template <typename TO>
+bool stream_gradient(const TO* p, int64_t rows, int64_t cols) {
+  const int64_t line = cols * static_cast<int64_t>(sizeof(TO));
+  return (line % 128 == 0 && reinterpret_cast<uintptr_t>(p) % 128 == 0) ||
+         rows * line >= (int64_t{128} << 20);
 }
 
 // The core of operands that the DMA core does not take.

@@ -86,6 +86,25 @@ def test_lookup_of_non_finite_rows_and_offsets_past_32_bits(gpu):
     assert float(table[1:vocab - 2].float().abs().max()) == 0.0
 
 
+@pytest.mark.parametrize("pad", [0, 64, 8])
+@pytest.mark.parametrize("od", ["bf16", "fp32"])
+def test_lookup_of_a_large_output(gpu, od, pad):
+    # 360 MB and more, in whole lines (pad 8: not, for bf16)
+    g = torch.Generator(device=gpu)
+    g.manual_seed(pad)
+    n, vocab, dim = 24611 if od == "bf16" else 12307, 211, 7360
+    table, _ = guarded((vocab, dim), torch.bfloat16, gpu)
+    fill_normal(table, 1.0, g)
+    ids = _ids("uniform", n, vocab, g, gpu, torch.int64)
+    out, check = guarded((n, dim), DT[od], gpu, 0, dim + pad)
+    M.embed_forward(table, ids, 0.5, out=out)
+    torch.cuda.synchronize()
+    check()
+    row = torch.where((ids >= 0) & (ids < vocab), ids, torch.full_like(ids, vocab))
+    want = torch.cat([table * 0.5, torch.zeros_like(table[:1])])[row].to(DT[od])  # exact
+    assert torch.equal(out, want)
+
+
 def test_lookup_of_the_most_positions(gpu):
     # 2^26 - 1 positions: more than one launch holds
     n, vocab = (1 << 26) - 1, 97

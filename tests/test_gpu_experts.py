@@ -133,6 +133,12 @@ def test_wgrad(gpu, rows, experts, k, n, kind, dt, od, off, pad, acc):
     assert same_bits(again, dw)
 
 
+@pytest.mark.parametrize("acc", [False, True])
+def test_wgrad_of_large_gradients(gpu, acc):
+    # 134 MB, rows that are no whole lines
+    test_wgrad(gpu, 400, 16, 2040, 2056, "gaps", "bf16", "bf16", 0, 0, acc)
+
+
 def test_offsets_out_of_order_stay_in_bounds(gpu):
     # clamped to [0, rows]; a range that is not positive holds no rows
     x = torch.ones(40, 64, dtype=torch.bfloat16, device=gpu)
