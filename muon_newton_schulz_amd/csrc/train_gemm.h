@@ -962,7 +962,8 @@ using ThinCore = DmaCore<PKS, QKS, 32, 128, 1, 64, 6>;
 // to 163840 vocabulary rows; some of what they rest on (us, shape by shape):
 //   8 rows x 64 experts 2048x1408 (NN): Thin 12.1, Medium 17.2, Half 24.9, Large 38.8
 //   700 rows x 20 experts 1280x1024 (NN): Medium 13.5, Thin 14.5, Half 18.9, Large 27.9
-//   8192 rows x 16 experts 1024x2048 (TN): Half 43.0, Large 46.0, Medium 47.9
+//   8192 rows x 16 experts 1000x1416 (TN): Half 32, Medium 37.5, Large 39
+//   2000 rows x 1 expert 1024x4096 (TN): Medium 20.4, Half 24.9
 //   loss 1024 x 50048 x 1024 (NT): Medium 115, Half 118, Large 133, Thin 356
 //   loss 4096 x 163840 x 7168 (NT): Large 7240, Medium 8700, Half 9720
 struct ShapeCost {
@@ -986,7 +987,7 @@ constexpr ShapeCost kShapeNT[] = {{256, 256, 1, 1.40, 1.72, 12.0}, {128, 256, 2,
 constexpr ShapeCost kShapeNN[] = {{256, 256, 1, 1.50, 1.79, 12.0}, {128, 256, 2, 1.10, 2.15, 3.0},
                                   {128, 128, 2, 0.50, 1.13, 3.0}, {32, 128, 1, 0.30, 0.80, 2.0}};
 constexpr ShapeCost kShapeTN[] = {{256, 256, 1, 1.45, 1.65, 9.0}, {128, 256, 2, 1.05, 2.10, 4.2},
-                                  {128, 128, 2, 0.55, 1.10, 3.2}};
+                                  {128, 128, 2, 0.55, 1.20, 3.4}};
 // the core for any operands: 128 x 128, 64 x 64
 constexpr ShapeCost kShapeAnyBf16[] = {{128, 128, 2, 1.20, 1.85, 3.0}, {64, 64, 4, 0.70, 1.60, 2.0}};
 constexpr ShapeCost kShapeAnyFp32[] = {{128, 128, 2, 3.80, 5.80, 6.0}, {64, 64, 4, 1.80, 4.10, 2.5}};
