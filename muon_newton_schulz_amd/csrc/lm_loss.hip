@@ -162,8 +162,8 @@ __global__ __launch_bounds__(kThreads, Core::kWaves) void k_loss_stats(StatsArgs
 }
 
 // Joins a row's tiles in a fixed order: thread (r, p) of a workgroup takes
-// tiles p, p + P, ... of row r, R rows x P parts, then the parts are joined in
-// order.  Rows run along the lanes, so loads of many rows are whole lines; few
+// tiles p, p + P, ... of row r, R rows x P parts, then the parts are joined
+// pairwise.  Rows run along the lanes, so loads of many rows are whole lines; few
 // rows take more parts.
 template <int R>
 __global__ __launch_bounds__(kThreads) void k_loss_join(const float* __restrict__ tile_m,
@@ -173,7 +173,7 @@ __global__ __launch_bounds__(kThreads) void k_loss_join(const float* __restrict_
                                                         int64_t vocab, float* __restrict__ loss,
                                                         float* __restrict__ lse) {
   constexpr int P = kThreads / R;
-  __shared__ float red[P][R][2];
+  __shared__ float red[kThreads / 64][R][2];
   const int r = threadIdx.x % R, part = threadIdx.x / R;
   const int t = blockIdx.x * R + r;
   float m = -INFINITY, s = 0.0f;
@@ -191,11 +191,21 @@ __global__ __launch_bounds__(kThreads) void k_loss_join(const float* __restrict_
       for (int u = 0; u < U; ++u) join_stats(m, s, tm[u], ts[u]);
     }
   }
-  red[part][r][0] = m;
-  red[part][r][1] = s;
+  // the parts of a wave, then the four waves
+#pragma unroll
+  for (int o = R; o < 64; o <<= 1) {
+    const float m2 = __shfl_xor(m, o, 64), s2 = __shfl_xor(s, o, 64);
+    join_stats(m, s, m2, s2);
+  }
+  const int wave = threadIdx.x >> 6;
+  if ((threadIdx.x & 63) < R) {
+    red[wave][r][0] = m;
+    red[wave][r][1] = s;
+  }
   __syncthreads();
   if (part != 0 || t >= n) return;
-  for (int p = 1; p < P; ++p) join_stats(m, s, red[p][r][0], red[p][r][1]);
+#pragma unroll
+  for (int p = 1; p < kThreads / 64; ++p) join_stats(m, s, red[p][r][0], red[p][r][1]);
   const float l = m + logf(s);
   lse[t] = l;
   loss[t] = target_of(targets, t64, t, vocab) >= 0 ? l - at[t] : 0.0f;
@@ -677,10 +687,13 @@ int lm_loss_forward(const void* hidden, int64_t ld_hidden, const void* weight, i
     const bool grid = on_grid(a.h, ld_hidden, dim) && on_grid(weight, dim, dim);
     const int v_tiles = static_cast<int>(dtype == MUON_DTYPE_BF16 ? run_stats<uint16_t>(a, grid, stream)
                                                                  : run_stats<float>(a, grid, stream));
-    // 16 rows a workgroup: 16 parts, and enough workgroups from 4096 rows on
-    hipLaunchKernelGGL(k_loss_join<16>, dim3(static_cast<unsigned>(ceil_div(rows, 16))),
-                       dim3(kThreads), 0, stream, tm, ts, at, v_tiles, rows, tg, targets_64 != 0,
-                       vocab, loss + r0, lse + r0);
+    // 16 rows a workgroup and 16 parts of a row; few rows take 4 and 64 (the
+    // call: 33 x 32000 x 2048 27.1 us against 29.7, 512 x 163840 x 64 40.1
+    // against 40.5, but 2048 x 32000 x 64 34.6 against 30.8)
+    const int per = rows <= 512 ? 4 : 16;
+    hipLaunchKernelGGL(per == 4 ? k_loss_join<4> : k_loss_join<16>,
+                       dim3(static_cast<unsigned>(ceil_div(rows, per))), dim3(kThreads), 0, stream,
+                       tm, ts, at, v_tiles, rows, tg, targets_64 != 0, vocab, loss + r0, lse + r0);
   }
   return check_launch("vocabulary loss launch");
 }
