@@ -827,16 +827,19 @@ def embed_forward(table, ids, scale: float = 1.0, out=None, out_dtype=None, stre
         if out_dtype is not None and dtype_code(out_dtype) != dtype_code(out.dtype):
             raise MuonError(MUON_ERR_BAD_DTYPE, f"out has dtype {out.dtype}, not {out_dtype}")
     dev = _one_device(table=table, ids=ids, out=out)
+    src = table.data_ptr()
     if out is not None:
-        _apart("out", out, n, dim, ld, table=(table, vocab, dim, dim))
+        dst = out.data_ptr()  # 4: the largest element (a small call's time is the binding's)
+        if dst < src + 4 * vocab * dim and src < dst + 4 * n * ld:
+            _apart("out", out, n, dim, ld, table=(table, vocab, dim, dim))
     with _Launch(dev, stream) as on:
         if out is None:
             td = {MUON_DTYPE_FP32: torch.float32, MUON_DTYPE_BF16: torch.bfloat16}
             dt = table.dtype if out_dtype is None else td[dtype_code(out_dtype)]
             out = torch.empty((*ids.shape, dim), dtype=dt, device=dev)
-        _check(lib().embed_forward(_ptr(table), dtype_code(table.dtype), vocab, dim, _ptr(ids), i64,
-                                   n, float(scale), _ptr(out), dtype_code(out.dtype), ld,
-                                   on.handle))
+            dst = out.data_ptr()
+        _check(lib().embed_forward(src, dtype_code(table.dtype), vocab, dim, _ptr(ids), i64, n,
+                                   float(scale), dst, dtype_code(out.dtype), ld, on.handle))
     return out
 
 
