@@ -513,14 +513,15 @@ int embed_backward(const void* dout, int32_t dout_dtype, int64_t ld_dout, const 
  *   loss[t] = lse[t] - hidden[t] . weight[targets[t]]
  * A row whose target lies outside [0, vocab) (an ignore index such as -100)
  * has loss 0 and no gradient.  Types: hidden and weight share dtype; logits,
- * statistics and sums are fp32; backward's g (below), over the largest
- * |dloss|, is rounded to dtype before its products.  n <= 2^24, vocab <= 2^21.
+ * statistics and sums are fp32; backward's g (below) enters its products as
+ * fp32, or with bf16 operands as the sum of two bf16 values, which is off by
+ * 2^-16 of it at most.  n <= 2^24, vocab <= 2^21.
  * A NaN in a row's logits makes its loss and lse NaN. */
 
 /* Device workspace of the two calls below: with backward != 0 enough for
  * both, else for the forward (0 for n == 0 or sizes they refuse).  The
- * backward needs about 256 MiB at least once n * vocab reaches that, for the
- * gradients of one piece of the logits, and fp32 sums of dhidden.
+ * backward needs 256 MiB (bf16: 512) and more once the gradients of all logits
+ * take that, for those of one piece of them, and fp32 sums of dhidden.
  * Host-only. */
 size_t lm_loss_workspace_size(int64_t n, int64_t vocab, int64_t dim, int32_t dtype,
                               int32_t backward);

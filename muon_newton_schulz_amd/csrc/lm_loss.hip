@@ -13,13 +13,19 @@
 // Backward, one piece of the vocabulary after another: the piece's logits
 // are computed again and turned into g / c in the epilogue, with c the
 // largest |dloss|; then dW of the piece = c (g/c)^T h and dh += c (g/c) W,
-// summed over the pieces in fp32.  g / c is stored in the operands' type, as
-// the matrix cores take it: for bf16 a rounding of half a step of each
-// value.  Without the division a common dloss such as 1 / n would lose the
-// same half step in every row, and the whole gradient with it (2^-8 at
-// worst); with it that factor is exact.  Few rows give few tiles of dh with
-// a long sum: it is split over workgroups, which add into fp32 sums of their
-// own, and a last kernel joins those in order.
+// summed over the pieces in fp32.  The matrix cores take bf16, so bf16 calls
+// store g / c as two bf16 planes, the nearest value (high) and what is left
+// of it (low), off by 2^-16 of it at most; both products run over the low
+// plane and then the high one.  One plane alone is off by up to 2^-8, and not
+// at random: a row's target value, -(1 - p) dloss, is most of its gradient.
+// Norm of the error of fp32 dhidden, 1024 x 32000 x 256: 1.5e-3 with random
+// dloss and 3.8e-3 with two values of it, against 2.2e-6 and 4.5e-6 with two
+// planes (fp32 products of the same g: 1.7e-6).  It costs the two products
+// twice their work: backward of 8192 x 32000 x 2048 2.93 -> 4.84 ms, of 4096 x
+// 163840 x 7168 24.7 -> 41.1 ms.  The division keeps both planes within bf16's
+// range, however small dloss is.  Few rows give few tiles of dh with a long
+// sum: it is split over workgroups, which add into fp32 sums of their own, and
+// a last kernel joins those in order.
 #include <algorithm>
 #include <cmath>
 
@@ -238,12 +244,29 @@ struct GradArgs {
   const float* lse;
   const float* dloss;
   const float* c;
-  void* g;             // [n][ldg], g / c
+  void* g;             // [n][ldg], g / c; bf16: low plane, high plane
   int64_t ldh, ldg, vocab, v0;
   int n, dim, len, t64;  // len: vocabulary rows of the piece
 };
 
-// g / c of the piece, in the operands' type.
+// What rounding to bf16 leaves of each value (0 where that is not finite).
+template <int NJ, int MI>
+__device__ __forceinline__ void low_part(f32x16_t (&acc)[NJ][MI]) {
+#pragma unroll
+  for (int a = 0; a < NJ; ++a)
+#pragma unroll
+    for (int b = 0; b < MI; ++b)
+#pragma unroll
+      for (int v = 0; v < 16; v += 2) {
+        const uint32_t h = pack_bf16(acc[a][b][v], acc[a][b][v + 1]);
+        const float x = acc[a][b][v] - __uint_as_float(h << 16);
+        const float y = acc[a][b][v + 1] - __uint_as_float(h & 0xffff0000u);
+        acc[a][b][v] = fabsf(x) < INFINITY ? x : 0.0f;
+        acc[a][b][v + 1] = fabsf(y) < INFINITY ? y : 0.0f;
+      }
+}
+
+// g / c of the piece, in the operands' type (bf16: two planes).
 template <typename Core, typename T>
 __device__ __forceinline__ void g_out(const GradArgs& a, const LossTile<T>& w,
                                       f32x16_t (&acc)[Core::NJ][Core::MI]) {
@@ -284,8 +307,27 @@ __device__ __forceinline__ void g_out(const GradArgs& a, const LossTile<T>& w,
       }
     __builtin_amdgcn_sched_barrier(0);
   }
-  Core::write(acc, static_cast<T*>(a.g) + i0 * a.ldg + j0, a.ldg, static_cast<const T*>(nullptr),
-              0, a.n - i0, Core::kGrid ? static_cast<int>(a.ldg) - j0 : a.len - j0);
+  T* low = static_cast<T*>(a.g) + i0 * a.ldg + j0;
+  const int cols = Core::kGrid ? static_cast<int>(a.ldg) - j0 : a.len - j0;
+  const T* none = nullptr;
+  if constexpr (sizeof(T) == 2) {
+    Core::write(acc, low + a.n * a.ldg, a.ldg, none, 0, a.n - i0, cols);
+    low_part(acc);
+  }
+  Core::write(acc, low, a.ldg, none, 0, a.n - i0, cols);
+}
+
+// A product with g: the sum over its planes, `plane` elements apart.
+template <typename Core, typename T>
+__device__ __forceinline__ void run_planes(LossTile<T>& w, int64_t plane,
+                                           f32x16_t (&acc)[Core::NJ][Core::MI]) {
+  if constexpr (sizeof(T) == 2) {
+    zero_acc(acc);
+#pragma unroll 1
+    for (int p = 0; p < 2; ++p, w.P += plane) Core::template run<true>(w, acc);
+  } else {
+    Core::run(w, acc);
+  }
 }
 
 template <typename Core, typename T>
@@ -338,7 +380,7 @@ __global__ __launch_bounds__(kThreads, Core::kWaves) void k_loss_dh(DhArgs a, in
   w.qn = a.dim - w.j0;
   w.K = min(share, a.len - k0);
   f32x16_t acc[Core::NJ][Core::MI];
-  Core::run(w, acc);
+  run_planes<Core, T>(w, a.n * a.ldg, acc);
   scale_acc(acc, *a.c);
   float* D = a.part + (static_cast<int64_t>(w.s) * a.n + w.i0) * a.dim + w.j0;
   const float* old = a.first ? nullptr : D;
@@ -388,7 +430,7 @@ __global__ __launch_bounds__(kThreads, Core::kWaves) void k_loss_dw(DwArgs a, in
   w.qn = a.dim - w.j0;
   w.K = a.n;
   f32x16_t acc[Core::NJ][Core::MI];
-  Core::run(w, acc);
+  run_planes<Core, T>(w, a.n * a.ldg, acc);
   scale_acc(acc, *a.c);
   TO* C = static_cast<TO*>(a.dw) + static_cast<int64_t>(w.i0) * a.dim + w.j0;
   Core::template write<STREAM>(acc, C, a.dim, a.accumulate ? C : static_cast<const TO*>(nullptr),
@@ -409,8 +451,10 @@ constexpr int kTile = 64;  // the narrowest tile: bounds the tile statistics
 // Forward: rows per pass, which bounds the tile statistics (vocab / 16 bytes
 // a row) without leaving the GPU short of tiles.
 constexpr int64_t kStatsRows = 16384;
-// Backward: bytes of g at a time.  Fewer pieces mean fewer passes over the
-// fp32 sums of dh; g should stay near what the last-level cache holds.
+// Backward: bytes of a plane of g at a time.  Fewer pieces mean fewer passes
+// over the fp32 sums of dh; g should stay near what the last-level cache holds
+// (bf16, two planes, 8192 x 32000 x 2048: 4.84 ms, with half of it 5.00; 4096 x
+// 163840 x 7168: 41.1 and 42.2).
 constexpr int64_t kPieceBytes = static_cast<int64_t>(256) << 20;
 constexpr int64_t kMinPiece = 2048, kPieceStep = 256;  // whole tiles
 // A launch holds fewer than 2^24 workgroups of 256: kStatsRows x kMaxVocabLoss
@@ -454,6 +498,7 @@ LossWs loss_ws(int64_t n, int64_t vocab, int64_t dim, int32_t dtype, bool backwa
   // backward (the forward's part of the workspace is free again)
   o = 0;
   const int64_t sz = static_cast<int64_t>(train_dtype_size(dtype));
+  const int64_t planes = dtype == MUON_DTYPE_BF16 ? 2 : 1;
   w.piece = std::max(kMinPiece, kPieceBytes / (sz * n) / kPieceStep * kPieceStep);
   if (w.piece >= vocab) {
     w.piece = vocab;
@@ -469,7 +514,7 @@ LossWs loss_ws(int64_t n, int64_t vocab, int64_t dim, int32_t dtype, bool backwa
   w.c = o;
   o += 256;
   w.g = o;
-  o += align256(static_cast<size_t>(n * w.ldg * sz));
+  o += align256(static_cast<size_t>(planes * n * w.ldg * sz));
   // dh tiles against the GPU's 256 workgroups of one tile each
   const int64_t tiles = ceil_div(n, 128) * ceil_div(dim, 128);
   w.splits = static_cast<int>(

@@ -6,7 +6,8 @@
 // on the matrix cores with fp32 accumulation.  An operand is K-contiguous
 // (element (r, k) at p[r * ld + k]) or K-strided (at p[k * ld + r]); pn and
 // qn are the rows of P and Q that exist from the tile's first row on (the
-// others count as zero and are not read), K the length of the sum.
+// others count as zero and are not read), K the length of the sum.  run<true>
+// adds to what acc holds; a second run may follow a first at once.
 //
 // Accumulators (A operand = Q, B operand = P): acc[bj][bi][4 q + e] of a
 // lane is element
@@ -240,9 +241,11 @@ struct AnyCore {
     }
   }
 
+  template <bool ADD = false>
   static __device__ __forceinline__ void run(const TileArgs<T>& w, f32x16_t (&acc)[NJ][MI]) {
-    run_in(w, acc, lds());
+    run_in<ADD>(w, acc, lds());
   }
+  template <bool ADD = false>
   static __device__ __forceinline__ void run_in(const TileArgs<T>& w, f32x16_t (&acc)[NJ][MI],
                                                 char* smem) {
     const T *P = w.P, *Q = w.Q;
@@ -268,11 +271,11 @@ struct AnyCore {
         *reinterpret_cast<u32x4_t*>(lds_piece<QKS>(buf(b, 1), t + 256 * h)) = qr[h];
       }
     };
-    zero_acc(acc);
+    if constexpr (!ADD) zero_acc(acc);
     if (K <= 0) return;
     const int steps = (K + CK - 1) / CK;
     load(0);
-    store(0);
+    store(0);  // (no wave reads the buffers of a run before this one any more)
     __syncthreads();
     auto span = [&](f32x16_t (&d)[NJ][MI], int c0, int c1) {
       for (int c = c0; c < c1; ++c) {
@@ -642,12 +645,13 @@ struct DmaCore {
 
   static constexpr int DPS = NP + NQ;  // a wave's DMA instructions per stage
 
+  template <bool ADD = false>
   static __device__ __forceinline__ void run(const TileArgs<uint16_t>& w,
                                              f32x16_t (&acc)[NJ][MI]) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int ri = (wave % WM) * 32 * MI, rj = (wave / WM) * 32 * NJ;
-    zero_acc(acc);
+    if constexpr (!ADD) zero_acc(acc);
     if (w.K <= 0) return;
     Operand<PKS, BM> po;
     Operand<QKS, BN> qo;
