@@ -512,7 +512,7 @@ int embed_backward(const void* dout, int32_t dout_dtype, int64_t ld_dout, const 
  *   lse[t]  = log sum_v exp(hidden[t] . weight[v])
  *   loss[t] = lse[t] - hidden[t] . weight[targets[t]]
  * A row whose target lies outside [0, vocab) (an ignore index such as -100)
- * has loss 0 and no gradient.  Types: hidden and weight share dtype; logits,
+ * has loss 0 and no gradient, whatever its hidden and dloss hold.  Types: hidden and weight share dtype; logits,
  * statistics and sums are fp32; backward's g (below) enters its products as
  * fp32, or with bf16 operands as the sum of two bf16 values, which is off by
  * 2^-16 of it at most.  n <= 2^24, vocab <= 2^21.
@@ -521,7 +521,8 @@ int embed_backward(const void* dout, int32_t dout_dtype, int64_t ld_dout, const 
 /* Device workspace of the two calls below: with backward != 0 enough for
  * both, else for the forward (0 for n == 0 or sizes they refuse).  The
  * backward needs 256 MiB (bf16: 512) and more once the gradients of all logits
- * take that, for those of one piece of them, and fp32 sums of dhidden.
+ * take that, for those of one piece of them, fp32 sums of dhidden and a copy
+ * of hidden.
  * Host-only. */
 size_t lm_loss_workspace_size(int64_t n, int64_t vocab, int64_t dim, int32_t dtype,
                               int32_t backward);

@@ -349,14 +349,44 @@ __global__ __launch_bounds__(kThreads, Core::kWaves) void k_loss_g(GradArgs a, i
   g_out<Core, T>(a, w, acc);
 }
 
+// hidden with zeros in the rows without a target, [n][dim]: dW's sum runs over
+// all rows, and 0 times what such a row holds is 0 only where that is finite.
+// One read and one write of hidden (backward of 8192 x 32000 x 2048: 4.60 ms
+// against 4.56 without, of 33 x 32000 x 2048: 114 us against 112).
+template <typename T>
+__global__ __launch_bounds__(kThreads) void k_loss_rows(const T* __restrict__ h, int64_t ldh,
+                                                        const void* targets, int t64, int n,
+                                                        int dim, int64_t vocab,
+                                                        T* __restrict__ out) {
+  constexpr int E = 16 / sizeof(T);
+  const int per = (dim + E - 1) / E;
+  const int64_t total = static_cast<int64_t>(n) * per;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * kThreads) {
+    const int64_t t = i / per;
+    const int c = static_cast<int>(i - t * per) * E;
+    const bool row = target_of(targets, t64, t, vocab) >= 0;
+    const T* p = h + t * ldh + c;
+    T* o = out + t * dim + c;
+    if (c + E <= dim) {
+      u32x4_t v = {0, 0, 0, 0};
+      if (row) __builtin_memcpy(&v, p, 16);
+      __builtin_memcpy(o, &v, 16);
+    } else {
+      for (int e = 0; c + e < dim; ++e) o[e] = row ? p[e] : T{};
+    }
+  }
+}
+
 struct DhArgs {
   const void* g;
   const void* w;  // the piece's first row
+  const void* targets;
   const float* c;
   float* part;    // fp32 sums, [splits][n][dim]
   void* out;      // dhidden, or null: leave the sums in part
-  int64_t ldg, ld_out;
-  int n, dim, len, splits, first;
+  int64_t ldg, ld_out, vocab;
+  int n, dim, len, splits, first, t64;
 };
 
 // dh (+)= g W of the piece; split s takes its share of the piece's rows.
@@ -381,7 +411,18 @@ __global__ __launch_bounds__(kThreads, Core::kWaves) void k_loss_dh(DhArgs a, in
   w.K = min(share, a.len - k0);
   f32x16_t acc[Core::NJ][Core::MI];
   run_planes<Core, T>(w, a.n * a.ldg, acc);
-  scale_acc(acc, *a.c);
+  // no gradient for a row without a target, where a weight is not finite too
+  const float c = *a.c;
+  const int t0 = w.i0 + (threadIdx.x >> 6) % Core::WM * 32 * Core::MI + (opaque_lane() & 31);
+#pragma unroll
+  for (int bi = 0; bi < Core::MI; ++bi) {
+    const int t = t0 + 32 * bi;
+    const bool row = t < a.n && target_of(a.targets, a.t64, t, a.vocab) >= 0;
+#pragma unroll
+    for (int bj = 0; bj < Core::NJ; ++bj)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[bj][bi][v] = row ? acc[bj][bi][v] * c : 0.0f;
+  }
   float* D = a.part + (static_cast<int64_t>(w.s) * a.n + w.i0) * a.dim + w.j0;
   const float* old = a.first ? nullptr : D;
   if (a.out == nullptr)
@@ -407,7 +448,7 @@ __global__ __launch_bounds__(kThreads) void k_loss_dh_join(const float* __restri
 
 struct DwArgs {
   const void* g;
-  const void* h;
+  const void* h;  // k_loss_rows' copy
   const float* c;
   void* dw;  // the piece's first row
   int64_t ldg, ldh, vocab;
@@ -479,7 +520,7 @@ struct LossWs {
   int64_t stats_rows, v_tiles;          // forward
   int64_t piece, ldg;                   // backward
   int splits;
-  size_t tile_m, tile_s, at, c, g, part, total;
+  size_t tile_m, tile_s, at, c, g, rows, part, total;
 };
 LossWs loss_ws(int64_t n, int64_t vocab, int64_t dim, int32_t dtype, bool backward) {
   LossWs w{};
@@ -515,6 +556,8 @@ LossWs loss_ws(int64_t n, int64_t vocab, int64_t dim, int32_t dtype, bool backwa
   o += 256;
   w.g = o;
   o += align256(static_cast<size_t>(planes * n * w.ldg * sz));
+  w.rows = o;
+  o += align256(static_cast<size_t>(n * dim * sz));
   // dh tiles against the GPU's 256 workgroups of one tile each
   const int64_t tiles = ceil_div(n, 128) * ceil_div(dim, 128);
   w.splits = static_cast<int>(
@@ -647,6 +690,14 @@ void run_backward(const BackwardArgs& b, const LossWs& w, hipStream_t s) {
   float* c = reinterpret_cast<float*>(b.ws + w.c);
   hipLaunchKernelGGL(k_loss_scale, dim3(1), dim3(kScaleThreads), 0, s, b.dloss,
                      static_cast<int>(b.n), b.targets, b.t64, b.vocab, c);
+  T* rows = reinterpret_cast<T*>(b.ws + w.rows);
+  if (b.dw != nullptr) {
+    const int64_t pieces = b.n * ceil_div(b.dim, 16 / static_cast<int64_t>(sizeof(T)));
+    hipLaunchKernelGGL(k_loss_rows<T>,
+                       dim3(static_cast<unsigned>(std::min<int64_t>(8192, ceil_div(pieces, kThreads)))),
+                       dim3(kThreads), 0, s, static_cast<const T*>(b.h), b.ldh, b.targets, b.t64,
+                       static_cast<int>(b.n), static_cast<int>(b.dim), b.vocab, rows);
+  }
   const bool grid = on_grid(b.h, b.ldh, b.dim) && on_grid(b.w, b.dim, b.dim);
   for (int64_t v0 = 0; v0 < b.vocab; v0 += w.piece) {
     const int len = static_cast<int>(std::min(w.piece, b.vocab - v0));
@@ -656,13 +707,13 @@ void run_backward(const BackwardArgs& b, const LossWs& w, hipStream_t s) {
              grid, s);
     if (b.dh != nullptr) {
       const bool last = v0 + len == b.vocab;
-      run_dh<T, TH>(DhArgs{g, wp, c, part, last && w.splits == 1 ? b.dh : nullptr, w.ldg, b.ld_dh,
-                           static_cast<int>(b.n), static_cast<int>(b.dim), len, w.splits,
-                           v0 == 0 ? 1 : 0},
+      run_dh<T, TH>(DhArgs{g, wp, b.targets, c, part, last && w.splits == 1 ? b.dh : nullptr,
+                           w.ldg, b.ld_dh, b.vocab, static_cast<int>(b.n),
+                           static_cast<int>(b.dim), len, w.splits, v0 == 0 ? 1 : 0, b.t64},
                     grid && on_grid(b.dh, b.ld_dh, b.dim), s);
     }
     if (b.dw != nullptr)
-      run_dw<T, TW>(DwArgs{g, b.h, c, static_cast<TW*>(b.dw) + v0 * b.dim, w.ldg, b.ldh, b.vocab,
+      run_dw<T, TW>(DwArgs{g, rows, c, static_cast<TW*>(b.dw) + v0 * b.dim, w.ldg, b.dim, b.vocab,
                            static_cast<int>(b.n), static_cast<int>(b.dim), len, b.accumulate},
                     grid && on_grid(b.dw, b.dim, b.dim), s);
   }

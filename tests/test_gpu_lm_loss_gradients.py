@@ -1,4 +1,5 @@
-"""The vocabulary loss's gradients: what bf16 calls keep of g.
+"""The vocabulary loss's gradients: what bf16 calls keep of g, and rows
+without a target.
 
 Bounds as in test_gpu_lm_loss.py, but for g's own rounding in bf16 calls: g
 is the sum of two bf16 values, of which the first is off by half a step, 2^-8
@@ -9,7 +10,7 @@ import torch
 
 import muon_newton_schulz_amd as M
 from test_gpu_lm_loss import Ref, _inputs
-from train_ops_util import DT, HALF, assert_within
+from train_ops_util import DT, HALF, assert_within, same_bits
 
 pytestmark = pytest.mark.gpu
 
@@ -55,3 +56,30 @@ def test_bf16_gradients_keep_more_of_g_than_bf16(gpu, kind, od, dim):
                                 dweight=torch.empty(vocab, dim, dtype=DT[od], device=gpu))
     assert_within(dh, ref.dh, 1.01 * (ref.dh_err + ref.dh.abs() * HALF[DT[od]]))
     assert_within(dw, ref.dw, 1.01 * (ref.dw_err + ref.dw.abs() * HALF[DT[od]]))
+
+
+@pytest.mark.parametrize("dt,n,vocab,dim", [("bf16", 70, 400, 64), ("bf16", 70, 400, 61),
+                                            ("fp32", 70, 400, 61), ("bf16", 600, 2000, 1024),
+                                            ("fp32", 600, 2000, 1024)])
+def test_what_ignored_rows_hold_reaches_no_gradient(gpu, dt, n, vocab, dim):
+    h, w, tgt, dl = _inputs(gpu, n, vocab, dim, dt, 0, 3, 1)
+    gone = ~((tgt >= 0) & (tgt < vocab))
+    assert 3 < int(gone.sum()) < n
+    _, lse = M.lm_loss_forward(h, w, tgt)
+    dh, dw = M.lm_loss_backward(h, w, tgt, lse, dl)
+    assert bool(dw.isfinite().all()) and not bool(dh[gone].any())
+    bad = torch.tensor([float("nan"), float("inf"), -float("inf")], device=gpu)
+    at = gone.nonzero()[:, 0]
+    held = h[at]
+    h[at] = bad[torch.arange(at.numel(), device=gpu) % 3].to(h.dtype)[:, None].expand(-1, dim)
+    loss2, lse2 = M.lm_loss_forward(h, w, tgt)
+    assert same_bits(lse2[~gone], lse[~gone]) and not bool(loss2[gone].any())
+    dh2, dw2 = M.lm_loss_backward(h, w, tgt, lse2, dl)
+    assert same_bits(dw2, dw) and same_bits(dh2, dh)
+    h[at] = held
+    # a weight that is not finite: no gradient for those rows still
+    w[vocab // 2, dim // 2] = float("inf")
+    w[vocab - 1] = float("nan")
+    _, lse3 = M.lm_loss_forward(h, w, tgt)
+    dh3, _ = M.lm_loss_backward(h, w, tgt, lse3, dl, dweight=False)
+    assert not bool(dh3[gone].any())
