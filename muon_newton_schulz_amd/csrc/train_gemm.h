@@ -334,15 +334,21 @@ struct AnyCore {
 //
 // fp32 products on the bf16 matrix cores: an operand x is the sum of three
 // bf16 values, hi = bf16(x), mid = bf16(x - hi), lo = bf16(x - hi - mid),
-// exactly up to 2^-27 x, and of the nine products the six above 2^-26 of
-// the largest are added, smallest first, in fp32 (products of bf16 are
-// exact in fp32).  The result is as accurate as a sum of fp32 products
-// (Henry, Tang, Heinecke, "Leveraging the bfloat16 artificial intelligence
-// datatype for higher-precision computations", 2019).  Six bf16
+// exactly while lo is in fp32's normal range or 0, and of the nine products the six
+// above 2^-26 of the largest are added, smallest first, in fp32 (products of
+// bf16 are exact in fp32).  The result is as accurate as a sum of fp32
+// products (Henry, Tang, Heinecke, "Leveraging the bfloat16 artificial
+// intelligence datatype for higher-precision computations", 2019).  Six bf16
 // instructions take 192 cycles for 16 k, the fp32 ones 512.
 // An operand that is not finite, or rounds to an infinite hi, makes its
-// results NaN here: a tile that holds a value that is not finite is computed
-// again on the fp32 instructions, and those values are taken from there.
+// results NaN here, and one below 2^-109 loses bits of its lo and mid under
+// bf16's smallest value, 2^-133 (a third of the mantissa at 2^-120); its lo is
+// below fp32's normal range (which starts for some values at 2^-103).  A tile
+// with either is computed again on the fp32 instructions; results that are not
+// finite, and those of rows and columns with such a small operand, are taken
+// from there.  Looking for small ones is one instruction a value: 16384 rows of
+// 8 experts, 2048 x 2048, 807 us with it and 778 without (by the bits of x, for
+// 0 < |x| < 2^-107: 833), loss 515 x 33001 x 500 backward 452 and 439.
 // 32 k a step; the operands are split on their way into LDS (single buffer;
 // two to four workgroups share a CU).  Sums restart every 256 k.
 template <bool PKS, bool QKS, int B>
@@ -364,8 +370,13 @@ struct SplitCore {
   static __device__ __forceinline__ uint16_t* plane(int op, int k) {
     return reinterpret_cast<uint16_t*>(lds() + (3 * op + k) * kPlane);
   }
+  // 0 < |x| < 2^-126
+  static __device__ __forceinline__ bool subnormal(float x) {
+    return __builtin_amdgcn_classf(x, 0x90);
+  }
+  // low: set if a lo is of a value below fp32's normal range
   template <bool KS>
-  static __device__ __forceinline__ void split_store(int op, int pc, u32x4_t w) {
+  static __device__ __forceinline__ void split_store(int op, int pc, u32x4_t w, bool& low) {
     constexpr int PR = (KS ? B : CK) / 4;
     const int o = pc / PR * (KS ? Half::SS : Half::SC) + pc % PR * 4;
     const f32x4_t x = __builtin_bit_cast(f32x4_t, w);
@@ -374,16 +385,41 @@ struct SplitCore {
     for (int k = 0; k < 3; ++k) {
       const u32x2_t h = {pack_bf16(a[0], a[1]), pack_bf16(b[0], b[1])};
       *reinterpret_cast<u32x2_t*>(plane(op, k) + o) = h;
+      if (k == 2) break;
       a[0] -= __uint_as_float(h[0] << 16);
       a[1] -= __uint_as_float(h[0] & 0xffff0000u);
       b[0] -= __uint_as_float(h[1] << 16);
       b[1] -= __uint_as_float(h[1] & 0xffff0000u);
     }
+    low |= subnormal(a[0]) | subnormal(a[1]) | subnormal(b[0]) | subnormal(b[1]);
+  }
+
+  // Marks the rows of an operand that hold a small value, a bit each.
+  template <bool KS>
+  static __device__ __forceinline__ void mark_small(const float* p, int64_t ld, int n, int K,
+                                                    uint32_t* marks) {
+    constexpr int PR = (KS ? B : CK) / 4;
+    for (int k0 = 0; k0 < K; k0 += CK)
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        const int pc = threadIdx.x + 256 * h;
+        const u32x4_t w = load_piece<float, KS, B, CK>(p, ld, n, K, k0, pc);
+        const f32x4_t x = __builtin_bit_cast(f32x4_t, w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float a = x[e];
+          a -= __uint_as_float(pack_bf16(a, a) << 16);
+          a -= __uint_as_float(pack_bf16(a, a) << 16);
+          const int r = KS ? pc % PR * 4 + e : pc / PR;
+          if (subnormal(a)) atomicOr(&marks[r >> 5], 1u << (r & 31));
+        }
+      }
   }
 
   static __device__ __forceinline__ void run(const TileArgs<float>& w, f32x16_t (&acc)[NJ][MI]) {
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     const int wi = wave % WM, wj = wave / WM;
+    bool low = false;
     zero_acc(acc);
     if (w.K <= 0) return;
     u32x4_t pr[H], qr[H];
@@ -403,8 +439,8 @@ struct SplitCore {
         __syncthreads();  // the step before is read
 #pragma unroll
         for (int h = 0; h < H; ++h) {
-          split_store<PKS>(0, t + 256 * h, pr[h]);
-          split_store<QKS>(1, t + 256 * h, qr[h]);
+          split_store<PKS>(0, t + 256 * h, pr[h], low);
+          split_store<QKS>(1, t + 256 * h, qr[h], low);
         }
         __syncthreads();
         if (c + 1 < steps) load((c + 1) * CK);
@@ -437,7 +473,7 @@ struct SplitCore {
 #pragma unroll
         for (int i = 0; i < MI; ++i) acc[j][i] += part[j][i];
     }
-    bool odd = false;  // x - x is 0 unless x is not finite
+    bool odd = low;  // x - x is 0 unless x is not finite
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
@@ -445,17 +481,28 @@ struct SplitCore {
 #pragma unroll
         for (int v = 0; v < 16; ++v) odd |= !(acc[j][i][v] - acc[j][i][v] == 0.0f);
     if (__syncthreads_or(odd)) {
-      // only the results that are not finite are replaced: a row's result does
-      // not depend on what the rows beside it hold
+      // only those results are replaced: a row's result does not depend on
+      // what the rows beside it hold
+      __shared__ uint32_t marks[2][B / 32];
+      if (t < 2 * (B / 32)) marks[0][t] = 0u;
+      __syncthreads();
+      mark_small<PKS>(w.P, w.ldp, w.pn, w.K, marks[0]);
+      mark_small<QKS>(w.Q, w.ldq, w.qn, w.K, marks[1]);
       f32x16_t again[NJ][MI];
-      Exact::run_in(w, again, lds());
+      Exact::run_in(w, again, lds());  // (its barriers stand between marks and their readers)
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
 #pragma unroll
-        for (int i = 0; i < MI; ++i)
+        for (int i = 0; i < MI; ++i) {
+          // bit 8 q + e: column 8 q + 4 (lane / 32) + e of the block
+          const uint32_t cols = marks[1][wj * NJ + j] >> 4 * (lane >> 5);
+          const bool row = (marks[0][wi * MI + i] >> (lane & 31)) & 1u;
 #pragma unroll
           for (int v = 0; v < 16; ++v)
-            if (!(acc[j][i][v] - acc[j][i][v] == 0.0f)) acc[j][i][v] = again[j][i][v];
+            if (row || ((cols >> (8 * (v >> 2) + (v & 3))) & 1u) ||
+                !(acc[j][i][v] - acc[j][i][v] == 0.0f))
+              acc[j][i][v] = again[j][i][v];
+        }
     }
   }
 
