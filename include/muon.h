@@ -478,8 +478,8 @@ int muon_clip(const muon_clip_plan_t* plan, void* params, int32_t mode, float ta
  *     contiguous.  No alignment is required beyond the element size;
  *     workspaces are 256-byte aligned, scratch only (contents on entry are
  *     ignored), and calls that overlap in time need one each.
- *   - Outputs share no memory with inputs or with each other (columns of one
- *     buffer beside each other do not share any).
+ *   - Outputs and workspaces share no memory with inputs or with each other
+ *     (columns of one buffer beside each other do not share any).
  *   - Results do not depend on timing: repeated calls give the same bits.
  *   - 0 <= n < 2^26 positions, 1 <= vocab <= 2^31 - 2, 1 <= dim <= 2^22.  */
 

@@ -736,7 +736,8 @@ def _apart(name: str, out, rows: int, cols: int, ld: int, **inputs):
     """Refuses an output of ``rows`` x ``cols``, row stride ``ld``, that shares
     memory with an input, given as (tensor, rows, cols, row stride): the
     kernels read inputs after they have written outputs.  Columns of one
-    buffer beside each other are apart."""
+    buffer beside each other are apart, and so is a vector (one row) that
+    lies between two rows' columns."""
     e = out.element_size()
     a, row, step = out.data_ptr(), cols * e, ld * e
     end = a + (rows - 1) * step + row
@@ -746,10 +747,29 @@ def _apart(name: str, out, rows: int, cols: int, ld: int, **inputs):
         b, e = t.data_ptr(), t.element_size()
         if b >= end or a >= b + ((r - 1) * l + c) * e:
             continue
-        gap = (b - a) % step
-        if l * e == step and rows > 1 and r > 1 and gap >= row and gap + c * e <= step:
-            continue
+        if rows > 1 and (r == 1 or l * e == step):
+            gap = (b - a) % step
+            if gap >= row and gap + c * e <= step:
+                continue
+        elif rows == 1 and r > 1:
+            gap = (a - b) % (l * e)
+            if gap >= c * e and gap + row <= l * e:
+                continue
         raise MuonError(MUON_ERR_INVALID_ARG, f"{name} shares memory with {other}")
+
+
+def _vector(t):
+    """A contiguous tensor as _apart takes it."""
+    n = t.numel()
+    return t, 1, n, n
+
+
+def _apart_workspace(workspace, **tensors):
+    """Refuses a caller's workspace that shares memory with a tensor of the
+    call."""
+    if workspace is not None:
+        _buf(workspace, "workspace")
+        _apart("workspace", *_vector(workspace), **tensors)
 
 
 def _current_handle(dev) -> int:
@@ -832,6 +852,9 @@ def embed_forward(table, ids, scale: float = 1.0, out=None, out_dtype=None, stre
         dst = out.data_ptr()  # 4: the largest element (a small call's time is the binding's)
         if dst < src + 4 * vocab * dim and src < dst + 4 * n * ld:
             _apart("out", out, n, dim, ld, table=(table, vocab, dim, dim))
+        at = ids.data_ptr()
+        if dst < at + 8 * n and at < dst + 4 * n * ld:
+            _apart("out", out, n, dim, ld, ids=_vector(ids))
     with _Launch(dev, stream) as on:
         if out is None:
             td = {MUON_DTYPE_FP32: torch.float32, MUON_DTYPE_BF16: torch.bfloat16}
@@ -863,7 +886,9 @@ def embed_backward(dout, ids, dtable, scale: float = 1.0, accumulate: bool = Fal
     n = ids.numel()
     ld = _rows(dout, "dout", n, dim)
     dev = _one_device(dtable=dtable, ids=ids, dout=dout, workspace=workspace)
-    _apart("dtable", dtable, vocab, dim, dim, dout=(dout, n, dim, ld))
+    ins = {"dout": (dout, n, dim, ld), "ids": _vector(ids)}
+    _apart("dtable", dtable, vocab, dim, dim, **ins)
+    _apart_workspace(workspace, dtable=(dtable, vocab, dim, dim), **ins)
     with _Launch(dev, stream) as on:
         ws = _workspace(workspace, embed_backward_workspace_size(n, vocab, dim), dev)
         _check(lib().embed_backward(_ptr(dout), dtype_code(dout.dtype), ld, _ptr(ids), i64, n,
@@ -903,8 +928,14 @@ def lm_loss_forward(hidden, weight, targets, loss=None, lse=None, workspace=None
             _block(t, name, (n,), F32)
     dev = _one_device(weight=weight, hidden=hidden, targets=targets, loss=loss, lse=lse,
                       workspace=workspace)
-    if loss is not None and lse is not None:
-        _apart("loss", loss, 1, n, n, lse=(lse, 1, n, n))
+    outs = {k: _vector(t) for k, t in (("loss", loss), ("lse", lse)) if t is not None}
+    if len(outs) == 2:
+        _apart("loss", *outs["loss"], lse=outs["lse"])
+    ins = {"hidden": (hidden, n, dim, ld), "weight": (weight, vocab, dim, dim),
+           "targets": _vector(targets)}
+    for name, out in outs.items():
+        _apart(name, *out, **ins)
+    _apart_workspace(workspace, **outs, **ins)
     with _Launch(dev, stream) as on:
         if loss is None:
             loss = torch.empty(n, dtype=torch.float32, device=dev)
@@ -939,13 +970,18 @@ def lm_loss_backward(hidden, weight, targets, lse, dloss, dhidden=None, dweight=
     dev = _one_device(weight=weight, hidden=hidden, targets=targets, lse=lse, dloss=dloss,
                       dhidden=None if dhidden is False else dhidden,
                       dweight=None if dweight is False else dweight, workspace=workspace)
-    ins = {"hidden": (hidden, n, dim, ld), "weight": (weight, vocab, dim, dim)}
+    outs = {}
     if dhidden is not None and dhidden is not False:
-        _apart("dhidden", dhidden, n, dim, ld_dh, **ins)
+        outs["dhidden"] = (dhidden, n, dim, ld_dh)
     if dweight is not None and dweight is not False:
-        _apart("dweight", dweight, vocab, dim, dim, **ins)
-        if dhidden is not None and dhidden is not False:
-            _apart("dweight", dweight, vocab, dim, dim, dhidden=(dhidden, n, dim, ld_dh))
+        outs["dweight"] = (dweight, vocab, dim, dim)
+    if len(outs) == 2:
+        _apart("dweight", *outs["dweight"], dhidden=outs["dhidden"])
+    ins = {"hidden": (hidden, n, dim, ld), "weight": (weight, vocab, dim, dim),
+           "targets": _vector(targets), "lse": _vector(lse), "dloss": _vector(dloss)}
+    for name, out in outs.items():
+        _apart(name, *out, **ins)
+    _apart_workspace(workspace, **outs, **ins)
     with _Launch(dev, stream) as on:
         if dhidden is None:
             dhidden = torch.empty((n, dim), dtype=hidden.dtype, device=dev)
@@ -1004,7 +1040,8 @@ def expert_matmul(x, w, offsets, trans: bool = False, out=None, out_dtype=None, 
             raise MuonError(MUON_ERR_BAD_DTYPE, f"out has dtype {out.dtype}, not {out_dtype}")
     dev = _one_device(w=w, x=x, offsets=offsets, out=out)
     if out is not None:
-        _apart("out", out, rows, n, ldy, x=(x, rows, k, ldx), w=(w, experts * k, n, n))
+        _apart("out", out, rows, n, ldy, x=(x, rows, k, ldx), w=(w, experts * k, n, n),
+               offsets=_vector(offsets))
     with _Launch(dev, stream) as on:
         if out is None:
             td = {MUON_DTYPE_FP32: torch.float32, MUON_DTYPE_BF16: torch.bfloat16}
@@ -1033,7 +1070,8 @@ def expert_wgrad(a, b, offsets, dw, accumulate: bool = False, stream=None):
     ldb = _rows(b, "b", rows, n, (dtype_code(a.dtype),))
     _offsets(offsets, experts)
     dev = _one_device(dw=dw, a=a, b=b, offsets=offsets)
-    _apart("dw", dw, experts * m, n, n, a=(a, rows, m, lda), b=(b, rows, n, ldb))
+    _apart("dw", dw, experts * m, n, n, a=(a, rows, m, lda), b=(b, rows, n, ldb),
+           offsets=_vector(offsets))
     with _Launch(dev, stream) as on:
         _check(lib().expert_wgrad(_ptr(a), lda, _ptr(b), ldb, dtype_code(a.dtype), _ptr(offsets),
                                   experts, rows, m, n, _ptr(dw), dtype_code(dw.dtype),
