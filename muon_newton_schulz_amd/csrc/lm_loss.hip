@@ -629,19 +629,22 @@ void launch_dh(const DhArgs& a, hipStream_t s) {
                      dim3(tile_blocks(nx, static_cast<int64_t>(ny) * a.splits)),
                      dim3(kThreads), 0, s, a, nx, ny);
 }
+// bf16: a sum runs over both planes of g
+template <typename T>
+constexpr int64_t kPlanes = sizeof(T) == 2 ? 2 : 1;
 template <typename T, typename TO>
 void run_dh(const DhArgs& a, bool grid, hipStream_t s) {
+  const int64_t k = kPlanes<T> * ceil_div(a.len, a.splits);
   if constexpr (sizeof(T) == 2) {
     if (grid) {
-      const Shape shape =
-          pick_shape(kShapeNN, dh_tiles(a.n, a.splits), a.dim, ceil_div(a.len, a.splits));
+      const Shape shape = pick_shape(kShapeNN, dh_tiles(a.n, a.splits), a.dim, k);
       if (shape == kLarge) return launch_dh<LargeCore<false, true>, T, TO>(a, s);
       if (shape == kHalf) return launch_dh<HalfCore<false, true>, T, TO>(a, s);
       if (shape == kMedium) return launch_dh<MediumCore<false, true>, T, TO>(a, s);
       return launch_dh<ThinCore<false, true>, T, TO>(a, s);
     }
   }
-  if (pick_any_large<T>(dh_tiles(a.n, a.splits), a.dim, ceil_div(a.len, a.splits)))
+  if (pick_any_large<T>(dh_tiles(a.n, a.splits), a.dim, k))
     launch_dh<OtherCore<T, false, true, 128>, T, TO>(a, s);
   else
     launch_dh<OtherCore<T, false, true, 64>, T, TO>(a, s);
@@ -662,13 +665,13 @@ template <typename T, typename TO>
 void run_dw(const DwArgs& a, bool grid, hipStream_t s) {
   if constexpr (sizeof(T) == 2) {
     if (grid) {
-      const Shape shape = pick_shape(kShapeTN, row_tiles(a.len), a.dim, a.n);
+      const Shape shape = pick_shape(kShapeTN, row_tiles(a.len), a.dim, kPlanes<T> * a.n);
       if (shape == kLarge) return launch_dw<LargeCore<true, true>, T, TO>(a, s);
       if (shape == kHalf) return launch_dw<HalfCore<true, true>, T, TO>(a, s);
       return launch_dw<MediumCore<true, true>, T, TO>(a, s);
     }
   }
-  if (pick_any_large<T>(row_tiles(a.len), a.dim, a.n))
+  if (pick_any_large<T>(row_tiles(a.len), a.dim, kPlanes<T> * a.n))
     launch_dw<OtherCore<T, true, true, 128>, T, TO>(a, s);
   else
     launch_dw<OtherCore<T, true, true, 64>, T, TO>(a, s);
