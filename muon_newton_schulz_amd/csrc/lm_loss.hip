@@ -44,8 +44,11 @@ __device__ __forceinline__ int64_t target_of(const void* targets, int t64, int64
   return v >= 0 && v < vocab ? v : -1;
 }
 
-// exp: the fp32 path takes the accurate one, the bf16 path the hardware's
-// (relative error 2^-21 at |x| = 8, against bf16's 2^-8)
+// exp: the fp32 path takes the accurate one, the bf16 path the hardware's, whose
+// relative error, 2^-21 at |x| = 8, is below the 2^-16 that g keeps.  The loss
+// gains nothing from the accurate one, whose terms' errors average out (rms
+// error, 1024 x 32000 x 256: 5.6e-7 with it, 5.5e-7 without), and the forward of
+// 8192 x 32000 x 2048 takes 940 us with it and 878 without.
 template <typename T>
 __device__ __forceinline__ float exp_of(float x) {
   if constexpr (sizeof(T) == 4) return expf(x);
@@ -212,9 +215,11 @@ __global__ __launch_bounds__(kThreads) void k_loss_join(const float* __restrict_
   if (part != 0 || t >= n) return;
 #pragma unroll
   for (int p = 1; p < kThreads / 64; ++p) join_stats(m, s, red[p][r][0], red[p][r][1]);
-  const float l = m + logf(s);
-  lse[t] = l;
-  loss[t] = target_of(targets, t64, t, vocab) >= 0 ? l - at[t] : 0.0f;
+  // (m - at) + log s, not lse - at: the rounding of lse, half a step of m, is
+  // all there is of a likely target's loss
+  const float ls = logf(s);
+  lse[t] = m + ls;
+  loss[t] = target_of(targets, t64, t, vocab) >= 0 ? (m - at[t]) + ls : 0.0f;
 }
 
 // c: the largest finite |dloss| of the rows with a target, 1 if that is 0.
