@@ -553,7 +553,8 @@ int lm_loss_backward(const void* hidden, int64_t ld_hidden, const void* weight, 
  * memory, read by the kernels; values outside [0, rows] are clamped, an
  * expert whose range is not positive has no rows).  Rows outside every range
  * are neither read nor written.  1 <= experts <= 4096, 0 <= rows < 2^26,
- * sides of a weight in [1, 2^22].
+ * sides of a weight in [1, 2^22]; calls whose result has more tiles than a
+ * launch holds (thousands of experts with a side of millions) are refused.
  *
  * y[r] = x[r] w[e] with w [experts][k][n] (trans_w == 0), or x[r] w[e]^T with
  * w [experts][n][k] (trans_w != 0).  The gradient by x is the same call on dy

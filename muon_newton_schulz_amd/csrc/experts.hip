@@ -172,16 +172,24 @@ __global__ __launch_bounds__(kThreads, Core::kWaves) void k_expert_wgrad(WgradAr
 
 constexpr int kMaxExperts = 4096;
 
+// Narrow matrices of many experts with a side of millions can need more tiles
+// than a launch holds.
+int refuse_tiles() {
+  return set_error(MUON_ERR_UNSUPPORTED, "more result tiles than a launch holds (2^24)");
+}
 template <typename Core, typename T, bool QKS, typename TO>
-void launch_matmul(const MatmulArgs& a, hipStream_t s) {
+int launch_matmul(const MatmulArgs& a, hipStream_t s) {
   const int nx = most_row_tiles(a.rows, a.experts, Core::BM);
   const int ny = (a.N + Core::BN - 1) / Core::BN;
+  if (!tiles_fit(nx, ny)) return refuse_tiles();
   hipLaunchKernelGGL((k_expert_matmul<Core, T, QKS, TO>),
                      dim3(tile_blocks(nx, ny)), dim3(kThreads), 0, s, a, ny);
+  return check_launch("expert product launch");
 }
 template <typename Core, typename T, typename TO>
-void launch_wgrad(const WgradArgs& g, hipStream_t s) {
+int launch_wgrad(const WgradArgs& g, hipStream_t s) {
   const int nx = (g.M + Core::BM - 1) / Core::BM, ny = (g.N + Core::BN - 1) / Core::BN;
+  if (!tiles_fit(static_cast<int64_t>(nx) * g.experts, ny)) return refuse_tiles();
   auto* kernel = k_expert_wgrad<Core, false, T, TO>;
   if constexpr (Core::kGrid) {
     if (stream_gradient(static_cast<const TO*>(g.dw), static_cast<int64_t>(g.experts) * g.M, g.N))
@@ -189,6 +197,7 @@ void launch_wgrad(const WgradArgs& g, hipStream_t s) {
   }
   hipLaunchKernelGGL(kernel, dim3(tile_blocks(static_cast<int64_t>(nx) * g.experts, ny)),
                      dim3(kThreads), 0, s, g, nx, ny);
+  return check_launch("expert weight gradient launch");
 }
 
 // Row tiles of the groups, whose sizes the host does not know: rows spread
@@ -199,52 +208,49 @@ double group_tiles(int rows, int experts, int bm) {
 }
 
 template <bool QKS, typename TO>
-void run_matmul_grid(const MatmulArgs& a, hipStream_t s) {
+int run_matmul_grid(const MatmulArgs& a, hipStream_t s) {
   const Shape shape = pick_shape(QKS ? kShapeNN : kShapeNT, [&](int bm) {
     return group_tiles(a.rows, a.experts, bm);
   }, a.N, a.K);
   using T = uint16_t;
-  if (shape == kLarge) launch_matmul<LargeCore<false, QKS>, T, QKS, TO>(a, s);
-  else if (shape == kHalf) launch_matmul<HalfCore<false, QKS>, T, QKS, TO>(a, s);
-  else if (shape == kMedium) launch_matmul<MediumCore<false, QKS>, T, QKS, TO>(a, s);
-  else launch_matmul<ThinCore<false, QKS>, T, QKS, TO>(a, s);
+  if (shape == kLarge) return launch_matmul<LargeCore<false, QKS>, T, QKS, TO>(a, s);
+  if (shape == kHalf) return launch_matmul<HalfCore<false, QKS>, T, QKS, TO>(a, s);
+  if (shape == kMedium) return launch_matmul<MediumCore<false, QKS>, T, QKS, TO>(a, s);
+  return launch_matmul<ThinCore<false, QKS>, T, QKS, TO>(a, s);
 }
 
 template <typename T, typename TO>
-void run_matmul(const MatmulArgs& a, bool trans, hipStream_t s) {
+int run_matmul(const MatmulArgs& a, bool trans, hipStream_t s) {
   if constexpr (sizeof(T) == 2) {
     if (on_grid(a.x, a.ldx, a.K) && on_grid(a.w, a.N, a.K) && on_grid(a.y, a.ldy, a.N)) {
-      if (trans) run_matmul_grid<false, TO>(a, s);
-      else run_matmul_grid<true, TO>(a, s);
-      return;
+      return trans ? run_matmul_grid<false, TO>(a, s) : run_matmul_grid<true, TO>(a, s);
     }
   }
   const bool large = pick_any_large<T>(
       [&](int bm) { return group_tiles(a.rows, a.experts, bm); }, a.N, a.K);
   if (trans) {
-    if (large) launch_matmul<OtherCore<T, false, false, 128>, T, false, TO>(a, s);
-    else launch_matmul<OtherCore<T, false, false, 64>, T, false, TO>(a, s);
-  } else {
-    if (large) launch_matmul<OtherCore<T, false, true, 128>, T, true, TO>(a, s);
-    else launch_matmul<OtherCore<T, false, true, 64>, T, true, TO>(a, s);
+    if (large) return launch_matmul<OtherCore<T, false, false, 128>, T, false, TO>(a, s);
+    return launch_matmul<OtherCore<T, false, false, 64>, T, false, TO>(a, s);
   }
+  if (large) return launch_matmul<OtherCore<T, false, true, 128>, T, true, TO>(a, s);
+  return launch_matmul<OtherCore<T, false, true, 64>, T, true, TO>(a, s);
 }
 
 template <typename T, typename TO>
-void run_wgrad(const WgradArgs& g, hipStream_t s) {
+int run_wgrad(const WgradArgs& g, hipStream_t s) {
   auto tiles = [&](int bm) { return static_cast<double>(g.experts) * ((g.M + bm - 1) / bm); };
   const int64_t k = g.rows / g.experts;
   if constexpr (sizeof(T) == 2) {
     if (on_grid(g.a, g.lda, g.M) && on_grid(g.b, g.ldb, g.N) && on_grid(g.dw, g.N, g.M)) {
       const Shape shape = pick_shape(kShapeTN, tiles, g.N, k);
-      if (shape == kLarge) launch_wgrad<LargeCore<true, true>, T, TO>(g, s);
-      else if (shape == kHalf) launch_wgrad<HalfCore<true, true>, T, TO>(g, s);
-      else launch_wgrad<MediumCore<true, true>, T, TO>(g, s);
-      return;
+      if (shape == kLarge) return launch_wgrad<LargeCore<true, true>, T, TO>(g, s);
+      if (shape == kHalf) return launch_wgrad<HalfCore<true, true>, T, TO>(g, s);
+      return launch_wgrad<MediumCore<true, true>, T, TO>(g, s);
     }
   }
-  if (pick_any_large<T>(tiles, g.N, k)) launch_wgrad<OtherCore<T, true, true, 128>, T, TO>(g, s);
-  else launch_wgrad<OtherCore<T, true, true, 64>, T, TO>(g, s);
+  if (pick_any_large<T>(tiles, g.N, k))
+    return launch_wgrad<OtherCore<T, true, true, 128>, T, TO>(g, s);
+  return launch_wgrad<OtherCore<T, true, true, 64>, T, TO>(g, s);
 }
 
 int check_group(int64_t rows, int32_t experts, int64_t k, int64_t n) {
@@ -252,7 +258,6 @@ int check_group(int64_t rows, int32_t experts, int64_t k, int64_t n) {
     return set_error(MUON_ERR_BAD_SHAPE, "rows must be in [0, 2^26)");
   if (experts < 1 || experts > kMaxExperts)
     return set_error(MUON_ERR_BAD_SHAPE, "experts must be in [1, 4096]");
-  // 65535 tiles of 128 is the least any launch dimension holds
   if (k < 1 || k > (1 << 22) || n < 1 || n > (1 << 22))
     return set_error(MUON_ERR_BAD_SHAPE, "a weight's sides must be in [1, 2^22]");
   return MUON_OK;
@@ -279,14 +284,10 @@ int expert_matmul(const void* x, int64_t ldx, const void* w, int32_t dtype,
   const MatmulArgs a{x, w, y, offsets, ldx, ldy, experts, static_cast<int>(rows),
                      static_cast<int>(k), static_cast<int>(n)};
   const bool tr = trans_w != 0, yb = y_dtype == MUON_DTYPE_BF16;
-  if (dtype == MUON_DTYPE_BF16) {
-    if (yb) run_matmul<uint16_t, uint16_t>(a, tr, stream);
-    else run_matmul<uint16_t, float>(a, tr, stream);
-  } else {
-    if (yb) run_matmul<float, uint16_t>(a, tr, stream);
-    else run_matmul<float, float>(a, tr, stream);
-  }
-  return check_launch("expert product launch");
+  if (dtype == MUON_DTYPE_BF16)
+    return yb ? run_matmul<uint16_t, uint16_t>(a, tr, stream)
+              : run_matmul<uint16_t, float>(a, tr, stream);
+  return yb ? run_matmul<float, uint16_t>(a, tr, stream) : run_matmul<float, float>(a, tr, stream);
 }
 
 int expert_wgrad(const void* a, int64_t lda, const void* b, int64_t ldb, int32_t dtype,
@@ -305,14 +306,9 @@ int expert_wgrad(const void* a, int64_t lda, const void* b, int64_t ldb, int32_t
   const WgradArgs g{a, b, dw, offsets, lda, ldb, experts, static_cast<int>(rows),
                     static_cast<int>(m), static_cast<int>(n), accumulate != 0};
   const bool wb = dw_dtype == MUON_DTYPE_BF16;
-  if (dtype == MUON_DTYPE_BF16) {
-    if (wb) run_wgrad<uint16_t, uint16_t>(g, stream);
-    else run_wgrad<uint16_t, float>(g, stream);
-  } else {
-    if (wb) run_wgrad<float, uint16_t>(g, stream);
-    else run_wgrad<float, float>(g, stream);
-  }
-  return check_launch("expert weight gradient launch");
+  if (dtype == MUON_DTYPE_BF16)
+    return wb ? run_wgrad<uint16_t, uint16_t>(g, stream) : run_wgrad<uint16_t, float>(g, stream);
+  return wb ? run_wgrad<float, uint16_t>(g, stream) : run_wgrad<float, float>(g, stream);
 }
 
 }  // extern "C"

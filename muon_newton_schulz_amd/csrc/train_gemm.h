@@ -142,6 +142,8 @@ __device__ __forceinline__ bool my_tile(int64_t nx, int64_t ny, int& x, int& y) 
 inline unsigned tile_blocks(int64_t nx, int64_t ny) {
   return static_cast<unsigned>((nx * ny + kXcds - 1) / kXcds * kXcds);
 }
+// Whether a launch holds that many: fewer than 2^32 threads.
+inline bool tiles_fit(int64_t nx, int64_t ny) { return nx * ny <= (int64_t{1} << 24) - kXcds; }
 
 // 8 k (bf16) or 4 k (fp32) of a 16-wide (8-wide) k step from LDS:
 // transposed read of a K-strided tile.  Within each group of 16 lanes, lane

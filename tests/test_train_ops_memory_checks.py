@@ -1,6 +1,9 @@
 """Outputs and workspaces of the operators that write gradients share no
 memory with index vectors, statistics, matrices or each other: the binding
-refuses such calls before any library call (CPU, stand-in tensors)."""
+refuses such calls before any library call (CPU, stand-in tensors).  Nor may a
+result have more tiles than a launch holds."""
+
+import ctypes
 
 import pytest
 import torch
@@ -110,3 +113,16 @@ def test_apart_calls_reach_the_library(monkeypatch):
     with pytest.raises(Reached):
         M.lm_loss_backward(out, table, ids, lse, dl, dhidden=_at(5, (60, 16)),
                            dweight=_at(6, (100, 16)), workspace=ws)
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("trans", [0, 1])
+def test_more_tiles_than_a_launch_holds_are_refused(dtype, trans):
+    # 4096 experts with a side of 2^22: 4096 x 16384 tiles even of 256 columns
+    p, side = ctypes.c_void_p(256), 1 << 22  # never dereferenced
+    L = M.lib()
+    assert L.expert_matmul(p, 8, p, dtype, p, 4096, 4096, 8, side, trans, p, dtype, side,
+                           None) == M.MUON_ERR_UNSUPPORTED
+    for m, n in ((8, side), (side, 8)):
+        assert L.expert_wgrad(p, m, p, n, dtype, p, 4096, 40, m, n, p, dtype, 0,
+                              None) == M.MUON_ERR_UNSUPPORTED
