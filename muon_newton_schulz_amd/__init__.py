@@ -675,6 +675,10 @@ def muon_clip(plan: MuonClipPlan, params, mode, tau: float, max_logits=None, wor
 # run on that GPU's current stream unless ``stream`` names another of its
 # streams.  What a call allocates (outputs and workspaces left out) belongs
 # to the stream the call runs on.
+#
+# Like the steps, they are no autograd functions: nothing is recorded, tensors
+# that require gradients are read as they are, and an output has no graph.  A
+# program calls each gradient itself (or from its own autograd.Function).
 
 TRAIN = (MUON_DTYPE_FP32, MUON_DTYPE_BF16)
 
