@@ -516,7 +516,7 @@ int embed_backward(const void* dout, int32_t dout_dtype, int64_t ld_dout, const 
  * statistics and sums are fp32; backward's g (below) enters its products as
  * fp32, or with bf16 operands as the sum of two bf16 values, which is off by
  * 2^-16 of it at most.  n <= 2^24, vocab <= 2^21.
- * A NaN in a row's logits makes its loss and lse NaN. */
+ * A NaN or +infinity in a row's logits makes its loss and lse NaN. */
 
 /* Device workspace of the two calls below: with backward != 0 enough for
  * both, else for the forward (0 for n == 0 or sizes they refuse).  The

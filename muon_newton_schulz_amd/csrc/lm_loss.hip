@@ -23,7 +23,7 @@
 // planes (fp32 products of the same g: 1.7e-6).  It costs the two products
 // twice their work: backward of 8192 x 32000 x 2048 2.93 -> 4.84 ms, of 4096 x
 // 163840 x 7168 24.7 -> 41.1 ms.  The division keeps both planes within bf16's
-// range, however small dloss is.  Few rows give few tiles of dh with a long
+// range whatever the size of dloss.  Few rows give few tiles of dh with a long
 // sum: it is split over workgroups, which add into fp32 sums of their own, and
 // a last kernel joins those in order.
 #include <algorithm>
@@ -508,8 +508,9 @@ constexpr int64_t kMinPiece = 2048, kPieceStep = 256;  // whole tiles
 constexpr int64_t kMaxVocabLoss = static_cast<int64_t>(1) << 21;
 constexpr int64_t kMaxTokensLoss = static_cast<int64_t>(1) << 24;
 // Shares of dh's sum at most: the tiles of the core for any operands take
-// longer, and gain from more (515 x 33001 x 500, g and dh: fp32 540 us with
-// 16, 411 with 25; bf16 151 and 121; DMA core, 33 x 32000 x 2048: 54 and 59).
+// longer, and gain from more (backward of 515 x 33001 x 500: fp32 507 us with
+// 16, 455 with 25; bf16 342 and 285; DMA core, 33 x 32000 x 2048: 112 and, with
+// 32, 119).
 constexpr int kMaxSplits = 16, kMaxSplitsAny = 32;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -554,7 +555,7 @@ LossWs loss_ws(int64_t n, int64_t vocab, int64_t dim, int32_t dtype, bool backwa
     w.piece = ceil_div(ceil_div(vocab, pieces), kPieceStep) * kPieceStep;
   }
   // off the multiples of 4 KiB, where the rows of a tile fall on the same
-  // memory channels (4096 x 163840 x 7168: dh 1.5% faster)
+  // memory channels (backward of 4096 x 163840 x 7168: 38.7 ms against 40.6)
   w.ldg = ceil_div(w.piece, 8) * 8;
   if (w.ldg % 1024 == 0) w.ldg += 128;
   w.c = o;

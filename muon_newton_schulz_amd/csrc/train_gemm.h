@@ -1009,8 +1009,9 @@ using ThinCore = DmaCore<PKS, QKS, 32, 128, 1, 64, 6>;
 // `alone` to `full` with the number of workgroups that share the GPU (matrix
 // cores of their CU, memory); tiles beyond one a place take further rounds,
 // the last with the time of the tiles that are left for it (counting it as a
-// whole one kept loss 1024 x 50048 x 1024 and 1500 x 50304 x 768 from the
-// better tiles: backward 349 and 385 us against 364 and 403).  The constants are fits to measured
+// whole one keeps 8192 rows of 16 experts, 1000 x 1416 (TN), 2048 of 8, 2048 x
+// 1408 (TN), and 8192 of 16, 1024 x 2048 (NT), from the better tiles: 34.4, 21.5
+// and 47.5 us against 39.7, 23.8 and 50.2).  The constants are fits to measured
 // products of 8 to 65536 rows, 1 to 128 experts, sides 1000 to 7168 and 32000
 // to 163840 vocabulary rows; some of what they rest on (us, shape by shape):
 //   8 rows x 64 experts 2048x1408 (NN): Thin 12.1, Medium 17.2, Half 24.9, Large 38.8
@@ -1068,9 +1069,9 @@ bool pick_any_large(R&& rows, int64_t cols, int64_t k) {
 // Whether the DMA core stores a weight gradient of rows x cols past the caches,
 // which leaves them to the operands; the optimizer step reads it after the
 // whole backward.  us with and without, bf16:
-//   rows of whole 128-byte lines: 4096 rows of 64 experts, 2048 x 1408, 79 and
-//   115; 65536 of 128, 7168 x 2048, 2310 and 2410; 700 of 20, 1280 x 1024, 14.2
-//   and 14.8; loss 1024 x 50048 x 1024, backward 340 and 353
+//   rows of whole 128-byte lines: 4096 rows of 64 experts, 2048 x 1408, 76 and
+//   103; 65536 of 128, 7168 x 2048, 2220 and 2308; 700 of 20, 1280 x 1024, 14.2
+//   and 14.8; loss 1024 x 50048 x 1024, backward 610 and 625
 //   others pay for the parts of lines: 4096 of 16, 1024 x 1000 (33 MB), 24.6 and
 //   17.6; 8192 of 16, 2000 x 1032 (66 MB), 56.8 and 55.6; 20000 of 16, 2040 x
 //   2056 (134 MB), 198 and 218
