@@ -336,10 +336,10 @@ struct AnyCore {
 //
 // fp32 products on the bf16 matrix cores: an operand x is the sum of three
 // bf16 values, hi = bf16(x), mid = bf16(x - hi), lo = bf16(x - hi - mid),
-// exactly while lo is in fp32's normal range or 0, and of the nine products the six
-// above 2^-26 of the largest are added, smallest first, in fp32 (products of
-// bf16 are exact in fp32).  The result is as accurate as a sum of fp32
-// products (Henry, Tang, Heinecke, "Leveraging the bfloat16 artificial
+// exactly while lo is in fp32's normal range or 0, and of the nine products
+// the six above 2^-26 of the largest are added, smallest first, in fp32
+// (products of bf16 are exact in fp32).  The result is as accurate as a sum of
+// fp32 products (Henry, Tang, Heinecke, "Leveraging the bfloat16 artificial
 // intelligence datatype for higher-precision computations", 2019).  Six bf16
 // instructions take 192 cycles for 16 k, the fp32 ones 512.
 // An operand that is not finite, or rounds to an infinite hi, makes its
@@ -350,7 +350,8 @@ struct AnyCore {
 // finite, and those of rows and columns with such a small operand, are taken
 // from there.  Looking for small ones is one instruction a value: 16384 rows of
 // 8 experts, 2048 x 2048, 807 us with it and 778 without (by the bits of x, for
-// 0 < |x| < 2^-107: 833), loss 515 x 33001 x 500 backward 452 and 439.
+// 0 < |x| < 2^-107: 833), loss 515 x 33001 x 500 backward 452 and 439.  With one
+// in every tile, small or not finite, a product takes 3.2 times as long.
 // 32 k a step; the operands are split on their way into LDS (single buffer;
 // two to four workgroups share a CU).  Sums restart every 256 k.
 template <bool PKS, bool QKS, int B>
