@@ -29,6 +29,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "lm_loss.h"
 #include "train_gemm.h"
 
 namespace muon {
@@ -55,36 +56,16 @@ __device__ __forceinline__ float exp_of(float x) {
   else return __expf(x);
 }
 
-// (m, s) <- (m, s) + (m2, s2): sums of exp(l - m) over disjoint sets.  A set
-// without a value above -inf has s = 0.
-__device__ __forceinline__ void join_stats(float& m, float& s, float m2, float s2) {
-  const float mm = fmaxf(m, m2);
-  const float a = m == mm ? s : s * expf(m - mm);
-  const float b = m2 == mm ? s2 : s2 * expf(m2 - mm);
-  m = mm;
-  s = a + b;
-}
-
-struct StatsArgs {
-  const void* h;
-  const void* w;
-  const void* targets;
-  float* tile_m;  // [vocabulary tiles][n]
-  float* tile_s;
-  float* at;      // [n], the target's logit
-  int64_t ldh, vocab;
-  int n, dim, t64;
-};
-
 // Row statistics of one tile: the maximum and the sum of a lane's 16 NJ
 // values of a row, joined with the lane that holds the row's other columns
-// (lane ^ 32), then with the waves beside it.
+// (lane ^ 32), then with the waves beside it.  POINTS: also the logits of the
+// row's listed columns.
 template <typename T>
 struct LossTile : TileArgs<T> {
   int i0, j0, s;
   int64_t v0;
 };
-template <typename Core, typename T>
+template <bool POINTS, typename Core, typename T>
 __device__ __forceinline__ void stats_out(const StatsArgs& a, const LossTile<T>& w,
                                           f32x16_t (&acc)[Core::NJ][Core::MI]) {
   const int i0 = w.i0, jn = w.qn;
@@ -94,6 +75,30 @@ __device__ __forceinline__ void stats_out(const StatsArgs& a, const LossTile<T>&
   const int jw = wj * 32 * Core::NJ + 4 * (lane >> 5);
   float* red = reinterpret_cast<float*>(Core::lds());  // [WN][BM][2]
   static_assert(Core::WN * Core::BM * 8 <= Core::kLdsBytes, "the waves' row statistics");
+  const float scale = a.scale;
+  // POINTS: the wave's columns as keys, and where each row's list reaches them
+  const int64_t c0 = v0 + wj * 32 * Core::NJ;
+  const uint32_t key0 = static_cast<uint32_t>(c0) << kPlaceBits;
+  const uint32_t key1 = static_cast<uint32_t>(c0 + 32 * Core::NJ) << kPlaceBits;
+  int first[Core::MI];
+  if constexpr (POINTS) {
+#pragma unroll
+    for (int bi = 0; bi < Core::MI; ++bi) {
+      const int64_t t = static_cast<int64_t>(i0) + wi * 32 * Core::MI + 32 * bi + (lane & 31);
+      int lo = 0, len = t < a.n ? a.top : 0;
+      if (len == 0) lo = a.top;
+      while (len > 0) {
+        const int half = len >> 1;
+        if (a.keys[t * a.top + lo + half] < key0) {
+          lo += half + 1;
+          len -= half + 1;
+        } else {
+          len = half;
+        }
+      }
+      first[bi] = lo;
+    }
+  }
   // EDGE: the vocabulary ends inside the tile (the test stays out of the
   // loops of the other tiles)
   auto rows = [&](auto edge_c) {
@@ -102,16 +107,44 @@ __device__ __forceinline__ void stats_out(const StatsArgs& a, const LossTile<T>&
     for (int bi = 0; bi < Core::MI; ++bi) {
       const int i = wi * 32 * Core::MI + 32 * bi + (lane & 31);
       const int64_t t = static_cast<int64_t>(i0) + i;
-      const int64_t tgt = t < a.n ? target_of(a.targets, a.t64, t, a.vocab) : -1;
-      // few lanes hold their row's target
-      const int64_t at64 = tgt - v0 - jw;
-      const int at = tgt >= 0 && at64 >= 0 && at64 < 32 * Core::NJ ? static_cast<int>(at64) : -1;
-      if (__ballot(at >= 0) != 0) {
+      if constexpr (POINTS) {
+        // one entry of each lane's row at a time; the lane of the pair that
+        // holds the column picks its value by the bits of the column
+        for (int p = first[bi];; ++p) {
+          const uint32_t key = p < a.top ? a.keys[t * a.top + p] : ~0u;
+          const bool more = key < key1;
+          if (__ballot(more) == 0) break;
+          const int col = static_cast<int>((key - key0) >> kPlaceBits) & (32 * Core::NJ - 1);
+          float x[16];
 #pragma unroll
-        for (int bj = 0; bj < Core::NJ; ++bj)
+          for (int v = 0; v < 16; ++v) {
+            x[v] = acc[0][bi][v];
 #pragma unroll
-          for (int v = 0; v < 16; ++v)
-            if (at == 32 * bj + 8 * (v >> 2) + (v & 3)) a.at[t] = acc[bj][bi][v];
+            for (int bj = 1; bj < Core::NJ; ++bj) x[v] = col >> 5 == bj ? acc[bj][bi][v] : x[v];
+          }
+          // column bits 0, 1, 3, 4 are the index's
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const bool odd = (col >> (b < 2 ? b : b + 1)) & 1;
+#pragma unroll
+            for (int v = 0; v < 8 >> b; ++v) x[v] = odd ? x[2 * v + 1] : x[2 * v];
+          }
+          if (more && ((col >> 2) & 1) == lane >> 5)
+            a.points[t * a.top + (key & ((1u << kPlaceBits) - 1))] = x[0];
+          if (!more) p = a.top;
+        }
+      } else {
+        const int64_t tgt = t < a.n ? target_of(a.targets, a.t64, t, a.vocab) : -1;
+        // few lanes hold their row's target
+        const int64_t at64 = tgt - v0 - jw;
+        const int at = tgt >= 0 && at64 >= 0 && at64 < 32 * Core::NJ ? static_cast<int>(at64) : -1;
+        if (__ballot(at >= 0) != 0) {
+#pragma unroll
+          for (int bj = 0; bj < Core::NJ; ++bj)
+#pragma unroll
+            for (int v = 0; v < 16; ++v)
+              if (at == 32 * bj + 8 * (v >> 2) + (v & 3)) a.at[t] = acc[bj][bi][v];
+        }
       }
       float m = -INFINITY;
 #pragma unroll
@@ -119,6 +152,7 @@ __device__ __forceinline__ void stats_out(const StatsArgs& a, const LossTile<T>&
 #pragma unroll
         for (int v = 0; v < 16; ++v)
           if (!EDGE || jw + 32 * bj + 8 * (v >> 2) + (v & 3) < jn) m = fmaxf(m, acc[bj][bi][v]);
+      m *= scale;
       // nothing above -inf: every term is exp(-inf) = 0
       const float ms = m == -INFINITY ? 0.0f : m;
       float s = 0.0f;
@@ -127,7 +161,7 @@ __device__ __forceinline__ void stats_out(const StatsArgs& a, const LossTile<T>&
 #pragma unroll
         for (int v = 0; v < 16; ++v)
           if (!EDGE || jw + 32 * bj + 8 * (v >> 2) + (v & 3) < jn)
-            s += exp_of<T>(acc[bj][bi][v] - ms);
+            s += exp_of<T>(__builtin_fmaf(acc[bj][bi][v], scale, -ms));
       const float m2 = __shfl_xor(m, 32, 64), s2 = __shfl_xor(s, 32, 64);
       if (lane < 32) {
         join_stats(m, s, m2, s2);
@@ -150,7 +184,7 @@ __device__ __forceinline__ void stats_out(const StatsArgs& a, const LossTile<T>&
     a.tile_s[o] = s;
   }
 }
-template <typename Core, typename T>
+template <bool POINTS, typename Core, typename T>
 __global__ __launch_bounds__(kThreads, Core::kWaves) void k_loss_stats(StatsArgs a, int nx, int ny) {
   using W = LossTile<T>;
   int x, y;
@@ -167,13 +201,9 @@ __global__ __launch_bounds__(kThreads, Core::kWaves) void k_loss_stats(StatsArgs
   w.qn = static_cast<int>(a.vocab - w.v0 < Core::BN ? a.vocab - w.v0 : Core::BN);
   f32x16_t acc[Core::NJ][Core::MI];
   Core::run(w, acc);
-  stats_out<Core, T>(a, w, acc);
+  stats_out<POINTS, Core, T>(a, w, acc);
 }
 
-// Joins a row's tiles in a fixed order: thread (r, p) of a workgroup takes
-// tiles p, p + P, ... of row r, R rows x P parts, then the parts are joined
-// pairwise.  Rows run along the lanes, so loads of many rows are whole lines; few
-// rows take more parts.
 template <int R>
 __global__ __launch_bounds__(kThreads) void k_loss_join(const float* __restrict__ tile_m,
                                                         const float* __restrict__ tile_s,
@@ -181,40 +211,10 @@ __global__ __launch_bounds__(kThreads) void k_loss_join(const float* __restrict_
                                                         int n, const void* targets, int t64,
                                                         int64_t vocab, float* __restrict__ loss,
                                                         float* __restrict__ lse) {
-  constexpr int P = kThreads / R;
-  __shared__ float red[kThreads / 64][R][2];
-  const int r = threadIdx.x % R, part = threadIdx.x / R;
-  const int t = blockIdx.x * R + r;
-  float m = -INFINITY, s = 0.0f;
-  if (t < n) {
-    constexpr int U = 8;
-    for (int k0 = part; k0 < tiles; k0 += U * P) {
-      float tm[U], ts[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int k = k0 + u * P;
-        tm[u] = k < tiles ? tile_m[static_cast<int64_t>(k) * n + t] : -INFINITY;
-        ts[u] = k < tiles ? tile_s[static_cast<int64_t>(k) * n + t] : 0.0f;
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) join_stats(m, s, tm[u], ts[u]);
-    }
-  }
-  // the parts of a wave, then the four waves
-#pragma unroll
-  for (int o = R; o < 64; o <<= 1) {
-    const float m2 = __shfl_xor(m, o, 64), s2 = __shfl_xor(s, o, 64);
-    join_stats(m, s, m2, s2);
-  }
-  const int wave = threadIdx.x >> 6;
-  if ((threadIdx.x & 63) < R) {
-    red[wave][r][0] = m;
-    red[wave][r][1] = s;
-  }
-  __syncthreads();
-  if (part != 0 || t >= n) return;
-#pragma unroll
-  for (int p = 1; p < kThreads / 64; ++p) join_stats(m, s, red[p][r][0], red[p][r][1]);
+  const int t = blockIdx.x * R + threadIdx.x % R;
+  float m, s;
+  join_tiles<R>(tile_m, tile_s, tiles, n, t, m, s);
+  if (threadIdx.x >= R || t >= n) return;
   // (m - at) + log s, not lse - at: the rounding of lse, half a step of m, is
   // all there is of a likely target's loss
   const float ls = logf(s);
@@ -252,6 +252,7 @@ struct GradArgs {
   void* g;             // [n][ldg], g / c; bf16: low plane, high plane
   int64_t ldh, ldg, vocab, v0;
   int n, dim, len, t64;  // len: vocabulary rows of the piece
+  float scale;           // of the logits
 };
 
 // What rounding to bf16 leaves of each value (0 where that is not finite).
@@ -307,7 +308,7 @@ __device__ __forceinline__ void g_out(const GradArgs& a, const LossTile<T>& w,
 #pragma unroll
       for (int v = 0; v < 16; ++v) {
         const int j = 32 * bj + 8 * (v >> 2) + (v & 3);
-        const float p = exp_of<T>(acc[bj][bi][v] - lse[bi]);
+        const float p = exp_of<T>(__builtin_fmaf(acc[bj][bi][v], a.scale, -lse[bi]));
         acc[bj][bi][v] = j < left ? (at == j ? p - 1.0f : p) * dl[bi] : 0.0f;
       }
     __builtin_amdgcn_sched_barrier(0);
@@ -392,6 +393,7 @@ struct DhArgs {
   void* out;      // dhidden, or null: leave the sums in part
   int64_t ldg, ld_out, vocab;
   int n, dim, len, splits, first, t64;
+  float scale;
 };
 
 // dh (+)= g W of the piece; split s takes its share of the piece's rows.
@@ -417,7 +419,7 @@ __global__ __launch_bounds__(kThreads, Core::kWaves) void k_loss_dh(DhArgs a, in
   f32x16_t acc[Core::NJ][Core::MI];
   run_planes<Core, T>(w, a.n * a.ldg, acc);
   // no gradient for a row without a target, where a weight is not finite too
-  const float c = *a.c;
+  const float c = *a.c * a.scale;
   const int t0 = w.i0 + (threadIdx.x >> 6) % Core::WM * 32 * Core::MI + (opaque_lane() & 31);
 #pragma unroll
   for (int bi = 0; bi < Core::MI; ++bi) {
@@ -458,6 +460,7 @@ struct DwArgs {
   void* dw;  // the piece's first row
   int64_t ldg, ldh, vocab;
   int n, dim, len, accumulate;
+  float scale;
 };
 
 template <typename Core, bool STREAM, typename T, typename TO>
@@ -477,7 +480,7 @@ __global__ __launch_bounds__(kThreads, Core::kWaves) void k_loss_dw(DwArgs a, in
   w.K = a.n;
   f32x16_t acc[Core::NJ][Core::MI];
   run_planes<Core, T>(w, a.n * a.ldg, acc);
-  scale_acc(acc, *a.c);
+  scale_acc(acc, *a.c * a.scale);
   TO* C = static_cast<TO*>(a.dw) + static_cast<int64_t>(w.i0) * a.dim + w.j0;
   Core::template write<STREAM>(acc, C, a.dim, a.accumulate ? C : static_cast<const TO*>(nullptr),
                                a.dim, w.pn, w.qn);
@@ -522,12 +525,8 @@ auto dh_tiles(int64_t n, int splits) {
   return [n, splits](int bm) { return static_cast<double>(ceil_div(n, bm) * splits); };
 }
 
-struct LossWs {
-  int64_t stats_rows, v_tiles;          // forward
-  int64_t piece, ldg;                   // backward
-  int splits;
-  size_t tile_m, tile_s, at, c, g, rows, part, total;
-};
+}  // namespace
+
 LossWs loss_ws(int64_t n, int64_t vocab, int64_t dim, int32_t dtype, bool backward) {
   LossWs w{};
   size_t o = 0;
@@ -576,31 +575,33 @@ LossWs loss_ws(int64_t n, int64_t vocab, int64_t dim, int32_t dtype, bool backwa
   return w;
 }
 
+namespace {
+
 // bf16 operands on the 16-byte grid take the DMA core (grid), others the
 // core for any operands.
-template <typename Core, typename T>
+template <bool POINTS, typename Core, typename T>
 int launch_stats(const StatsArgs& a, hipStream_t s) {
   const int nx = static_cast<int>(ceil_div(a.n, Core::BM));
   const int ny = static_cast<int>(ceil_div(a.vocab, Core::BN));
-  hipLaunchKernelGGL((k_loss_stats<Core, T>), dim3(tile_blocks(nx, ny)),
+  hipLaunchKernelGGL((k_loss_stats<POINTS, Core, T>), dim3(tile_blocks(nx, ny)),
                      dim3(kThreads), 0, s, a, nx, ny);
   return ny;
 }
 // returns the number of tiles along the vocabulary
-template <typename T>
+template <bool POINTS, typename T>
 int run_stats(const StatsArgs& a, bool grid, hipStream_t s) {
   if constexpr (sizeof(T) == 2) {
     if (grid) {
       const Shape shape = pick_shape(kShapeNT, row_tiles(a.n), a.vocab, a.dim);
-      if (shape == kLarge) return launch_stats<LargeCore<false, false>, T>(a, s);
-      if (shape == kHalf) return launch_stats<HalfCore<false, false>, T>(a, s);
-      if (shape == kMedium) return launch_stats<MediumCore<false, false>, T>(a, s);
-      return launch_stats<ThinCore<false, false>, T>(a, s);
+      if (shape == kLarge) return launch_stats<POINTS, LargeCore<false, false>, T>(a, s);
+      if (shape == kHalf) return launch_stats<POINTS, HalfCore<false, false>, T>(a, s);
+      if (shape == kMedium) return launch_stats<POINTS, MediumCore<false, false>, T>(a, s);
+      return launch_stats<POINTS, ThinCore<false, false>, T>(a, s);
     }
   }
   if (pick_any_large<T>(row_tiles(a.n), a.vocab, a.dim))
-    return launch_stats<OtherCore<T, false, false, 128>, T>(a, s);
-  return launch_stats<OtherCore<T, false, false, 64>, T>(a, s);
+    return launch_stats<POINTS, OtherCore<T, false, false, 128>, T>(a, s);
+  return launch_stats<POINTS, OtherCore<T, false, false, 64>, T>(a, s);
 }
 
 template <typename Core, typename T>
@@ -683,15 +684,6 @@ void run_dw(const DwArgs& a, bool grid, hipStream_t s) {
     launch_dw<OtherCore<T, true, true, 64>, T, TO>(a, s);
 }
 
-struct BackwardArgs {
-  const void *h, *w, *targets;
-  const float *lse, *dloss;
-  void *dh, *dw;
-  int64_t n, vocab, dim, ldh, ld_dh;
-  int t64, accumulate;
-  char* ws;
-};
-
 template <typename T, typename TH, typename TW>
 void run_backward(const BackwardArgs& b, const LossWs& w, hipStream_t s) {
   T* g = reinterpret_cast<T*>(b.ws + w.g);
@@ -712,18 +704,21 @@ void run_backward(const BackwardArgs& b, const LossWs& w, hipStream_t s) {
     const int len = static_cast<int>(std::min(w.piece, b.vocab - v0));
     const T* wp = static_cast<const T*>(b.w) + v0 * b.dim;
     run_g<T>(GradArgs{b.h, wp, b.targets, b.lse, b.dloss, c, g, b.ldh, w.ldg, b.vocab, v0,
-                      static_cast<int>(b.n), static_cast<int>(b.dim), len, b.t64},
+                      static_cast<int>(b.n), static_cast<int>(b.dim), len, b.t64, b.scale},
              grid, s);
+    if (b.after_g != nullptr) b.after_g(b.context, g, w.ldg, c, v0, len, s);
     if (b.dh != nullptr) {
       const bool last = v0 + len == b.vocab;
       run_dh<T, TH>(DhArgs{g, wp, b.targets, c, part, last && w.splits == 1 ? b.dh : nullptr,
                            w.ldg, b.ld_dh, b.vocab, static_cast<int>(b.n),
-                           static_cast<int>(b.dim), len, w.splits, v0 == 0 ? 1 : 0, b.t64},
+                           static_cast<int>(b.dim), len, w.splits, v0 == 0 ? 1 : 0, b.t64,
+                           b.scale},
                     grid && on_grid(b.dh, b.ld_dh, b.dim), s);
     }
     if (b.dw != nullptr)
       run_dw<T, TW>(DwArgs{g, rows, c, static_cast<TW*>(b.dw) + v0 * b.dim, w.ldg, b.dim, b.vocab,
-                           static_cast<int>(b.n), static_cast<int>(b.dim), len, b.accumulate},
+                           static_cast<int>(b.n), static_cast<int>(b.dim), len, b.accumulate,
+                           b.scale},
                     grid && on_grid(b.dw, b.dim, b.dim), s);
   }
   if (b.dh != nullptr && w.splits > 1)
@@ -732,6 +727,8 @@ void run_backward(const BackwardArgs& b, const LossWs& w, hipStream_t s) {
                        dim3(kThreads), 0, s, part, w.splits, static_cast<int>(b.n),
                        static_cast<int>(b.dim), static_cast<TH*>(b.dh), b.ld_dh);
 }
+
+}  // namespace
 
 int check_loss(int64_t n, int64_t vocab, int64_t dim, int64_t ldh, int32_t dtype) {
   const int rc = check_token_sizes(n, vocab, dim);
@@ -753,7 +750,40 @@ int check_ws(const void* ws, size_t bytes, size_t need, const char* who) {
   return MUON_OK;
 }
 
-}  // namespace
+int loss_stats(const StatsArgs& a, int32_t dtype, hipStream_t s) {
+  const bool grid = on_grid(a.h, a.ldh, a.dim) && on_grid(a.w, a.dim, a.dim);
+  if (dtype == MUON_DTYPE_BF16)
+    return a.keys != nullptr ? run_stats<true, uint16_t>(a, grid, s)
+                             : run_stats<false, uint16_t>(a, grid, s);
+  return a.keys != nullptr ? run_stats<true, float>(a, grid, s) : run_stats<false, float>(a, grid, s);
+}
+
+void loss_backward(const BackwardArgs& b, const LossWs& w, int32_t dtype, int32_t dh_dtype,
+                   int32_t dw_dtype, hipStream_t s) {
+  const bool hb = dh_dtype == MUON_DTYPE_BF16, wb = dw_dtype == MUON_DTYPE_BF16;
+  auto run = [&](auto t) {
+    using T = decltype(t);
+    if (hb && wb) run_backward<T, uint16_t, uint16_t>(b, w, s);
+    else if (hb) run_backward<T, uint16_t, float>(b, w, s);
+    else if (wb) run_backward<T, float, uint16_t>(b, w, s);
+    else run_backward<T, float, float>(b, w, s);
+  };
+  if (dtype == MUON_DTYPE_BF16) run(uint16_t{});
+  else run(float{});
+}
+
+int loss_no_rows(void* dw, int32_t dw_dtype, int64_t vocab, int64_t dim, int accumulate,
+                 hipStream_t s) {
+  if (dw == nullptr || accumulate) return MUON_OK;
+  if (dw_dtype == MUON_DTYPE_BF16)
+    hipLaunchKernelGGL(k_zero_rows<uint16_t>, dim3(4096), dim3(kThreads), 0, s,
+                       static_cast<uint16_t*>(dw), vocab, dim, dim);
+  else
+    hipLaunchKernelGGL(k_zero_rows<float>, dim3(4096), dim3(kThreads), 0, s,
+                       static_cast<float*>(dw), vocab, dim, dim);
+  return check_launch("vocabulary loss gradient launch");
+}
+
 }  // namespace muon
 
 using namespace muon;
@@ -786,16 +816,21 @@ int lm_loss_forward(const void* hidden, int64_t ld_hidden, const void* weight, i
   for (int64_t r0 = 0; r0 < n; r0 += w.stats_rows) {
     const int rows = static_cast<int>(std::min(w.stats_rows, n - r0));
     const void* tg = static_cast<const char*>(targets) + static_cast<size_t>(r0) * tsz;
-    const StatsArgs a{static_cast<const char*>(hidden) + static_cast<size_t>(r0 * ld_hidden) * sz,
-                      weight, tg, tm, ts, at, ld_hidden, vocab, rows, static_cast<int>(dim),
-                      targets_64 != 0};
-    const bool grid = on_grid(a.h, ld_hidden, dim) && on_grid(weight, dim, dim);
-    const int v_tiles = static_cast<int>(dtype == MUON_DTYPE_BF16 ? run_stats<uint16_t>(a, grid, stream)
-                                                                 : run_stats<float>(a, grid, stream));
-    // 16 rows a workgroup and 16 parts of a row; few rows take 4 and 64 (the
-    // call: 33 x 32000 x 2048 27.1 us against 29.7, 512 x 163840 x 64 40.1
-    // against 40.5, but 2048 x 32000 x 64 34.6 against 30.8)
-    const int per = rows <= 512 ? 4 : 16;
+    StatsArgs a{};
+    a.h = static_cast<const char*>(hidden) + static_cast<size_t>(r0 * ld_hidden) * sz;
+    a.w = weight;
+    a.targets = tg;
+    a.tile_m = tm;
+    a.tile_s = ts;
+    a.at = at;
+    a.ldh = ld_hidden;
+    a.vocab = vocab;
+    a.n = rows;
+    a.dim = static_cast<int>(dim);
+    a.t64 = targets_64 != 0;
+    a.scale = 1.0f;
+    const int v_tiles = loss_stats(a, dtype, stream);
+    const int per = join_rows(rows);
     hipLaunchKernelGGL(per == 4 ? k_loss_join<4> : k_loss_join<16>,
                        dim3(static_cast<unsigned>(ceil_div(rows, per))), dim3(kThreads), 0, stream,
                        tm, ts, at, v_tiles, rows, tg, targets_64 != 0, vocab, loss + r0, lse + r0);
@@ -818,39 +853,32 @@ int lm_loss_backward(const void* hidden, int64_t ld_hidden, const void* weight, 
   }
   if (dweight != nullptr && !train_dtype_ok(dweight_dtype))
     return set_error(MUON_ERR_BAD_DTYPE, "dweight must be fp32 or bf16");
-  if (n == 0) {
-    // no rows: dweight is a sum of nothing
-    if (dweight != nullptr && !accumulate) {
-      if (dweight_dtype == MUON_DTYPE_BF16)
-        hipLaunchKernelGGL(k_zero_rows<uint16_t>, dim3(4096), dim3(kThreads), 0, stream,
-                           static_cast<uint16_t*>(dweight), vocab, dim, dim);
-      else
-        hipLaunchKernelGGL(k_zero_rows<float>, dim3(4096), dim3(kThreads), 0, stream,
-                           static_cast<float*>(dweight), vocab, dim, dim);
-      return check_launch("vocabulary loss gradient launch");
-    }
-    return MUON_OK;
-  }
+  // no rows: dweight is a sum of nothing
+  if (n == 0) return loss_no_rows(dweight, dweight_dtype, vocab, dim, accumulate, stream);
   if (dhidden == nullptr && dweight == nullptr) return MUON_OK;
   if (hidden == nullptr || weight == nullptr || targets == nullptr || lse == nullptr ||
       dloss == nullptr)
     return set_error(MUON_ERR_INVALID_ARG, "hidden, weight, targets, lse or dloss is null");
   const LossWs w = loss_ws(n, vocab, dim, dtype, true);
   if ((rc = check_ws(workspace, workspace_bytes, w.total, "lm_loss_backward")) != MUON_OK) return rc;
-  const BackwardArgs b{hidden, weight, targets, lse, dloss, dhidden, dweight, n, vocab, dim,
-                       ld_hidden, ld_dhidden, targets_64 != 0, accumulate != 0,
-                       static_cast<char*>(workspace)};
-  const bool hb = dhidden_dtype == MUON_DTYPE_BF16, wb = dweight_dtype == MUON_DTYPE_BF16;
-#define MUON_LOSS_BWD(T)                                           \
-  do {                                                             \
-    if (hb && wb) run_backward<T, uint16_t, uint16_t>(b, w, stream); \
-    else if (hb) run_backward<T, uint16_t, float>(b, w, stream);   \
-    else if (wb) run_backward<T, float, uint16_t>(b, w, stream);   \
-    else run_backward<T, float, float>(b, w, stream);              \
-  } while (0)
-  if (dtype == MUON_DTYPE_BF16) MUON_LOSS_BWD(uint16_t);
-  else MUON_LOSS_BWD(float);
-#undef MUON_LOSS_BWD
+  BackwardArgs b{};
+  b.h = hidden;
+  b.w = weight;
+  b.targets = targets;
+  b.lse = lse;
+  b.dloss = dloss;
+  b.dh = dhidden;
+  b.dw = dweight;
+  b.n = n;
+  b.vocab = vocab;
+  b.dim = dim;
+  b.ldh = ld_hidden;
+  b.ld_dh = ld_dhidden;
+  b.t64 = targets_64 != 0;
+  b.accumulate = accumulate != 0;
+  b.ws = static_cast<char*>(workspace);
+  b.scale = 1.0f;
+  loss_backward(b, w, dtype, dhidden_dtype, dweight_dtype, stream);
   return check_launch("vocabulary loss gradient launch");
 }
 
