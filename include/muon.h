@@ -545,6 +545,123 @@ int lm_loss_backward(const void* hidden, int64_t ld_hidden, const void* weight, 
                      int32_t dweight_dtype, int32_t accumulate, void* workspace,
                      size_t workspace_bytes, hipStream_t stream);
 
+/* ---- distillation from a teacher's top logits ------------------------ */
+
+/* The divergence of the student's softmax, hidden weight^T / temperature over
+ * the whole vocabulary, from a teacher's, known at `top` columns a row (1 <=
+ * top <= 1024): ids [n][top] and teacher [n][top], its logits or log
+ * probabilities there, in any order.  An entry counts if its id lies in
+ * [0, vocab) and its teacher value is above -infinity; q is the softmax of
+ * teacher / temperature over the row's entries that count.
+ *   lse[t]     = log sum_v exp(hidden[t] . weight[v] / temperature)
+ *   logp[t][k] = hidden[t] . weight[ids[t][k]] / temperature - lse[t]
+ *   loss[t]    = sum_k q[t][k] (log q[t][k] - logp[t][k])
+ * An entry that does not count has logp 0; a row without one that counts has
+ * loss 0 and no gradient, whatever its hidden and dloss hold.  An id that is
+ * listed more than once has the sum of its q.  No factor temperature^2 is
+ * applied (dloss can carry one).  Types and limits as for lm_loss_*; teacher
+ * has a type of its own; temperature in [1e-6, 1e6]; a NaN among a row's
+ * teacher values that count, or a NaN or +infinity in its logits, makes its
+ * loss NaN. */
+
+/* Device workspace of the two calls below, as lm_loss_workspace_size, with
+ * 4 bytes an entry more (for the forward, of at most 16384 rows). */
+size_t distill_loss_workspace_size(int64_t n, int64_t vocab, int64_t dim, int64_t top,
+                                   int32_t dtype, int32_t backward);
+
+/* loss, lse: fp32, n values; logp: fp32, [n][top] contiguous. */
+int distill_loss_forward(const void* hidden, int64_t ld_hidden, const void* weight, int32_t dtype,
+                         const void* ids, int32_t ids_64, int64_t ld_ids, const void* teacher,
+                         int32_t teacher_dtype, int64_t ld_teacher, int64_t n, int64_t vocab,
+                         int64_t dim, int64_t top, float temperature, float* loss, float* lse,
+                         float* logp, void* workspace, size_t workspace_bytes,
+                         hipStream_t stream);
+
+/* Gradients of sum_t dloss[t] loss[t], with lse and logp from the forward
+ * call on the same hidden, weight, lists and temperature:
+ *   g[t][v] = (exp(l[t][v] - lse[t]) - sum of q[t][k] with ids[t][k] == v)
+ *             * dloss[t] / temperature
+ *   dhidden = g weight,   dweight = g^T hidden   (added with accumulate != 0)
+ * dhidden and dweight as for lm_loss_backward. */
+int distill_loss_backward(const void* hidden, int64_t ld_hidden, const void* weight, int32_t dtype,
+                          const void* ids, int32_t ids_64, int64_t ld_ids, const void* teacher,
+                          int32_t teacher_dtype, int64_t ld_teacher, int64_t n, int64_t vocab,
+                          int64_t dim, int64_t top, float temperature, const float* lse,
+                          const float* logp, const float* dloss, void* dhidden,
+                          int32_t dhidden_dtype, int64_t ld_dhidden, void* dweight,
+                          int32_t dweight_dtype, int32_t accumulate, void* workspace,
+                          size_t workspace_bytes, hipStream_t stream);
+
+/* ---- losses over packed sequences ------------------------------------- */
+
+/* From the token losses that lm_loss_forward leaves, nll[t] = -log p of token
+ * t, of sequences packed behind each other: sequence s owns tokens
+ * [offsets[s], offsets[s + 1]) (offsets: sequences + 1 non-decreasing int32 in
+ * device memory, read by the kernels; values outside [0, n] are clamped).  A
+ * token counts if it is in a sequence and mask, one byte a token, is null or
+ * not 0 there; N_s is the number of a sequence's tokens that count.  What the
+ * other tokens hold is not used.  The backward calls write dnll of the tokens
+ * that are in a sequence (0 for one that does not count) and leave the others
+ * as they were; dnll is the dloss that lm_loss_backward takes.  Values are
+ * fp32, sums fp64.  0 <= n < 2^26, 0 <= sequences <= 2^24. */
+
+/* Device workspace of the two forward calls (0 for sequences == 0 or sizes they
+ * refuse).  Host-only. */
+size_t sequence_loss_workspace_size(int64_t n, int64_t sequences);
+
+/* Clipped policy loss with a KL term.  For a token, with r = exp(old_nll - nll)
+ * the ratio of its probability to the one it was drawn with, A its advantage
+ * and x = nll - ref_nll,
+ *   token = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A)
+ *           + kl_weight k,   k = exp(x) - 1 - x
+ *   loss[s] = sum of token over the tokens that count,  kl[s] = sum of k,
+ * each divided by N_s with mean != 0 (0 where N_s is).  count[s] = N_s;
+ * clipped[s]: how many of them the clip holds, whose r A has no gradient
+ * (r > 1 + clip_high with A > 0, r < 1 - clip_low with A < 0; a ratio on the
+ * border is not held).  advantages: one a sequence, or with per_token != 0 one
+ * a token.  ref_nll may be null if kl_weight is 0 (then kl is 0).  clip_low in
+ * [0, 1], clip_high >= 0. */
+int policy_loss_forward(const float* nll, const float* old_nll, const float* ref_nll,
+                        const uint8_t* mask, const float* advantages, int32_t per_token,
+                        const int32_t* offsets, int64_t sequences, int64_t n, double clip_low,
+                        double clip_high, float kl_weight, int32_t mean, float* loss, float* kl,
+                        int32_t* count, int32_t* clipped, void* workspace, size_t workspace_bytes,
+                        hipStream_t stream);
+
+/* dnll: the gradient of sum_s dloss[s] loss[s] by nll, with count from the
+ * forward call:  dloss[s] (/ N_s) ([not held] r A + kl_weight (exp(x) - 1)). */
+int policy_loss_backward(const float* nll, const float* old_nll, const float* ref_nll,
+                         const uint8_t* mask, const float* advantages, int32_t per_token,
+                         const int32_t* offsets, int64_t sequences, int64_t n, double clip_low,
+                         double clip_high, float kl_weight, int32_t mean, const int32_t* count,
+                         const float* dloss, float* dnll, hipStream_t stream);
+
+#define MUON_PREFERENCE_LOGISTIC 0 /* (1 - smoothing) log(1 + e^-x) + smoothing log(1 + e^x) */
+#define MUON_PREFERENCE_HINGE 1    /* max(0, 1 - x), slope 0 at x = 1 */
+#define MUON_PREFERENCE_SQUARED 2  /* (1 - x)^2 */
+
+/* Preference loss over pairs: sequence 2 i is preferred to sequence 2 i + 1
+ * (sequences is even).
+ *   reward[s]  = beta * sum of (ref_nll - nll) over the tokens that count
+ *                (/ N_s with mean != 0); ref_nll null: of -nll
+ *   margins[i] = x = reward[2 i] - reward[2 i + 1] - margin,  loss[i] = f(x)
+ * with f by kind (0 <= smoothing <= 1, 0 but for the logistic kind).  A
+ * sequence without a token that counts has reward 0; its pair has loss 0 and
+ * no gradient.  count[s] = N_s. */
+int preference_loss_forward(const float* nll, const float* ref_nll, const uint8_t* mask,
+                            const int32_t* offsets, int64_t sequences, int64_t n, int32_t kind,
+                            float beta, float margin, float smoothing, int32_t mean, float* loss,
+                            float* margins, float* reward, int32_t* count, void* workspace,
+                            size_t workspace_bytes, hipStream_t stream);
+
+/* dnll: the gradient of sum_i dloss[i] loss[i] by nll, with margins and count
+ * from the forward call:  -+ beta (/ N_s) dloss[i] f'(margins[i]), - in
+ * sequence 2 i. */
+int preference_loss_backward(const uint8_t* mask, const int32_t* offsets, int64_t sequences,
+                             int64_t n, int32_t kind, float beta, float smoothing, int32_t mean,
+                             const float* margins, const int32_t* count, const float* dloss,
+                             float* dnll, hipStream_t stream);
+
 /* ---- matrix products grouped by expert ------------------------------- */
 
 /* Products with the contiguous expert blocks that muon_step steps ([EP]).

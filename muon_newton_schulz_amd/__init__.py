@@ -44,11 +44,17 @@ EXPORTED = [
     "muon_clip_plan_upload", "muon_clip",
     "embed_forward", "embed_backward", "embed_backward_workspace_size",
     "lm_loss_workspace_size", "lm_loss_forward", "lm_loss_backward",
+    "distill_loss_workspace_size", "distill_loss_forward", "distill_loss_backward",
+    "sequence_loss_workspace_size", "policy_loss_forward", "policy_loss_backward",
+    "preference_loss_forward", "preference_loss_backward",
     "expert_matmul", "expert_wgrad",
 ]
 
 MUON_CLIP_FROBENIUS = 0
 MUON_CLIP_MAX_LOGIT = 1
+MUON_PREFERENCE_LOGISTIC = 0
+MUON_PREFERENCE_HINGE = 1
+MUON_PREFERENCE_SQUARED = 2
 # size of the library's static device workspace (muon_step_noalloc)
 MUON_NOALLOC_WORKSPACE_BYTES = 256 << 20
 
@@ -173,6 +179,20 @@ def lib() -> ctypes.CDLL:
     L.lm_loss_forward.argtypes = [P, I64, P, I32, P, I32, I64, I64, I64, P, P, P, SZ, P]
     L.lm_loss_backward.argtypes = [P, I64, P, I32, P, I32, I64, I64, I64, P, P, P, I32, I64, P,
                                    I32, I32, P, SZ, P]
+    L.distill_loss_workspace_size.argtypes = [I64, I64, I64, I64, I32, I32]
+    L.distill_loss_workspace_size.restype = SZ
+    lists = [P, I64, P, I32, P, I32, I64, P, I32, I64, I64, I64, I64, I64, F]
+    L.distill_loss_forward.argtypes = lists + [P, P, P, P, SZ, P]
+    L.distill_loss_backward.argtypes = lists + [P, P, P, P, I32, I64, P, I32, I32, P, SZ, P]
+    D = ctypes.c_double
+    L.sequence_loss_workspace_size.argtypes = [I64, I64]
+    L.sequence_loss_workspace_size.restype = SZ
+    policy = [P, P, P, P, P, I32, P, I64, I64, D, D, F, I32]
+    L.policy_loss_forward.argtypes = policy + [P, P, P, P, P, SZ, P]
+    L.policy_loss_backward.argtypes = policy + [P, P, P, P]
+    L.preference_loss_forward.argtypes = [P, P, P, P, I64, I64, I32, F, F, F, I32, P, P, P, P, P,
+                                          SZ, P]
+    L.preference_loss_backward.argtypes = [P, P, I64, I64, I32, F, F, I32, P, P, P, P, P]
     L.expert_matmul.argtypes = [P, I64, P, I32, P, I32, I64, I64, I64, I32, P, I32, I64, P]
     L.expert_wgrad.argtypes = [P, I64, P, I64, I32, P, I32, I64, I64, I64, P, I32, I32, P]
     L.muon_status_string.argtypes = [I32]
@@ -183,7 +203,8 @@ def lib() -> ctypes.CDLL:
         if name not in ("muon_plan_destroy", "muon_clip_plan_destroy", "muon_status_string",
                         "muon_last_error", "muon_plan_table_bytes", "muon_clip_plan_table_bytes",
                         "grad_norm_clip_workspace_size", "state_stats_workspace_size",
-                        "embed_backward_workspace_size", "lm_loss_workspace_size"):
+                        "embed_backward_workspace_size", "lm_loss_workspace_size",
+                        "distill_loss_workspace_size", "sequence_loss_workspace_size"):
             getattr(L, name).restype = ctypes.c_int
     _lib_handle = L
     return L
@@ -693,7 +714,7 @@ def _rows(t, name: str, rows: int, cols: int, dtypes=TRAIN):
     if tuple(t.shape) != (rows, cols):
         raise MuonError(MUON_ERR_BAD_SHAPE,
                         f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
-    if dtype_code(t.dtype) not in dtypes:
+    if dtypes is not None and dtype_code(t.dtype) not in dtypes:
         raise MuonError(MUON_ERR_BAD_DTYPE, f"{name} has dtype {t.dtype}")
     if cols > 1 and t.stride(1) != 1:
         raise MuonError(MUON_ERR_INVALID_ARG, f"{name}: a row's elements must be contiguous")
@@ -774,6 +795,23 @@ def _apart_workspace(workspace, **tensors):
     if workspace is not None:
         _buf(workspace, "workspace")
         _apart("workspace", *_vector(workspace), **tensors)
+
+
+def _outputs_apart(outs, ins, workspace):
+    """_apart for every output against the inputs and the other outputs, and
+    the caller's workspace against all of them.  Address ranges are compared
+    first: apart as a whole, nothing else is asked."""
+    if workspace is not None:
+        _buf(workspace, "workspace")
+        outs = {"workspace": _vector(workspace), **outs}
+    spans = [(name, b, b[0].data_ptr(), ((b[1] - 1) * b[3] + b[2]) * b[0].element_size())
+             for name, b in (*outs.items(), *ins.items()) if b[1] and b[2]]
+    for i, (name, b, at, size) in enumerate(spans):
+        if name not in outs:
+            break
+        for other, c, at2, size2 in spans[i + 1:]:
+            if at < at2 + size2 and at2 < at + size:
+                _apart(name, *b, **{other: c})
 
 
 def _current_handle(dev) -> int:
@@ -1001,6 +1039,367 @@ def lm_loss_backward(hidden, weight, targets, lse, dloss, dhidden=None, dweight=
             dtype_code(weight.dtype if dweight is None else dweight.dtype), int(bool(accumulate)),
             _ptr(ws), _nbytes(ws), on.handle))
     return dhidden, dweight
+
+
+# ------------------------------------------------------------ distillation
+
+def distill_loss_workspace_size(n: int, vocab: int, dim: int, top: int, dtype,
+                                backward: bool = True) -> int:
+    return int(lib().distill_loss_workspace_size(int(n), int(vocab), int(dim), int(top),
+                                                 dtype_code(dtype), int(bool(backward))))
+
+
+def _distill_args(hidden, weight, ids, teacher):
+    """Checks the inputs that forward and backward share.  Returns (n, vocab,
+    dim, top), the call's leading C arguments and the inputs as _apart takes
+    them."""
+    import torch
+    _buf(weight, "weight", dtypes=TRAIN)
+    if len(weight.shape) != 2:
+        raise MuonError(MUON_ERR_BAD_SHAPE,
+                        f"weight must be [vocab, dim], is {tuple(weight.shape)}")
+    vocab, dim = weight.shape
+    if ids is None or len(ids.shape) != 2:
+        raise MuonError(MUON_ERR_BAD_SHAPE, "ids must be [n, top]")
+    n, top = ids.shape
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise MuonError(MUON_ERR_BAD_DTYPE, f"ids must be int32 or int64, has {ids.dtype}")
+    ld_ids = _rows(ids, "ids", n, top, None)
+    ld_z = _rows(teacher, "teacher", n, top)
+    ld = _rows(hidden, "hidden", n, dim, (dtype_code(weight.dtype),))
+    ins = {"hidden": (hidden, n, dim, ld), "weight": (weight, vocab, dim, dim),
+           "ids": (ids, n, top, ld_ids), "teacher": (teacher, n, top, ld_z)}
+
+    def args(temperature):
+        return (_ptr(hidden), ld, _ptr(weight), dtype_code(weight.dtype), _ptr(ids),
+                int(ids.dtype == torch.int64), ld_ids, _ptr(teacher), dtype_code(teacher.dtype),
+                ld_z, n, vocab, dim, top, float(temperature))
+
+    return (n, vocab, dim, top), args, ins
+
+
+def distill_loss_forward(hidden, weight, ids, teacher, temperature: float = 1.0, loss=None,
+                         lse=None, logp=None, workspace=None, stream=None):
+    """Divergence of the softmax of ``hidden @ weight.T / temperature`` from a
+    teacher's per row, without storing the logits.  hidden, weight as for
+    lm_loss_forward; ids (int32 or int64) and teacher (bf16 or fp32, logits or
+    log-probabilities): [n, top], top <= 1024, rows may be strided.  An entry
+    counts if its id is in [0, vocab) and its value above -inf; the teacher's
+    distribution is the softmax of ``teacher / temperature`` over those; a row
+    without one has no loss.  Returns (loss, lse, logp): fp32 of n, n and
+    [n, top], logp being the student's log-probabilities at ids (0 for entries
+    that do not count)."""
+    import torch
+    (n, vocab, dim, top), args, ins = _distill_args(hidden, weight, ids, teacher)
+    for name, t in (("loss", loss), ("lse", lse)):
+        if t is not None:
+            _block(t, name, (n,), F32)
+    if logp is not None:
+        _block(logp, "logp", (n, top), F32)
+    dev = _one_device(weight=weight, hidden=hidden, ids=ids, teacher=teacher, loss=loss, lse=lse,
+                      logp=logp, workspace=workspace)
+    outs = {k: _vector(t) for k, t in (("loss", loss), ("lse", lse), ("logp", logp))
+            if t is not None}
+    _outputs_apart(outs, ins, workspace)
+    with _Launch(dev, stream) as on:
+        if loss is None:
+            loss = torch.empty(n, dtype=torch.float32, device=dev)
+        if lse is None:
+            lse = torch.empty(n, dtype=torch.float32, device=dev)
+        if logp is None:
+            logp = torch.empty((n, top), dtype=torch.float32, device=dev)
+        ws = workspace
+        if ws is None:
+            ws = _workspace(None, distill_loss_workspace_size(n, vocab, dim, top, weight.dtype,
+                                                              False), dev)
+        _check(lib().distill_loss_forward(*args(temperature), _ptr(loss), _ptr(lse), _ptr(logp),
+                                          _ptr(ws), _nbytes(ws), on.handle))
+    return loss, lse, logp
+
+
+def distill_loss_backward(hidden, weight, ids, teacher, lse, logp, dloss,
+                          temperature: float = 1.0, dhidden=None, dweight=None,
+                          accumulate: bool = False, workspace=None, stream=None):
+    """Gradients of ``sum(dloss * loss)`` by hidden and weight; lse and logp
+    from distill_loss_forward on the same inputs, dloss fp32 of n.  dhidden,
+    dweight and accumulate as for lm_loss_backward.  Returns (dhidden,
+    dweight), None for what was not computed."""
+    import torch
+    (n, vocab, dim, top), args, ins = _distill_args(hidden, weight, ids, teacher)
+    _block(lse, "lse", (n,), F32)
+    _block(logp, "logp", (n, top), F32)
+    _block(dloss, "dloss", (n,), F32)
+    ld_dh = dim
+    if dhidden is not None and dhidden is not False:
+        ld_dh = _rows(dhidden, "dhidden", n, dim)
+    if dweight is not None and dweight is not False:
+        _block(dweight, "dweight", (vocab, dim))
+    elif accumulate:
+        raise MuonError(MUON_ERR_INVALID_ARG, "accumulate needs a dweight to add to")
+    dev = _one_device(weight=weight, hidden=hidden, ids=ids, teacher=teacher, lse=lse, logp=logp,
+                      dloss=dloss, dhidden=None if dhidden is False else dhidden,
+                      dweight=None if dweight is False else dweight, workspace=workspace)
+    outs = {}
+    if dhidden is not None and dhidden is not False:
+        outs["dhidden"] = (dhidden, n, dim, ld_dh)
+    if dweight is not None and dweight is not False:
+        outs["dweight"] = (dweight, vocab, dim, dim)
+    ins.update(lse=_vector(lse), logp=_vector(logp), dloss=_vector(dloss))
+    _outputs_apart(outs, ins, workspace)
+    with _Launch(dev, stream) as on:
+        if dhidden is None:
+            dhidden = torch.empty((n, dim), dtype=hidden.dtype, device=dev)
+        if dweight is None:
+            dweight = torch.empty((vocab, dim), dtype=weight.dtype, device=dev)
+        dhidden = None if dhidden is False else dhidden
+        dweight = None if dweight is False else dweight
+        ws = workspace
+        if ws is None:
+            ws = _workspace(None, distill_loss_workspace_size(n, vocab, dim, top, weight.dtype), dev)
+        _check(lib().distill_loss_backward(
+            *args(temperature), _ptr(lse), _ptr(logp), _ptr(dloss), _ptr(dhidden),
+            dtype_code(weight.dtype if dhidden is None else dhidden.dtype), ld_dh, _ptr(dweight),
+            dtype_code(weight.dtype if dweight is None else dweight.dtype), int(bool(accumulate)),
+            _ptr(ws), _nbytes(ws), on.handle))
+    return dhidden, dweight
+
+
+# --------------------------------------------- losses over packed sequences
+
+_PREFERENCE_KINDS = {"logistic": MUON_PREFERENCE_LOGISTIC, "hinge": MUON_PREFERENCE_HINGE,
+                     "squared": MUON_PREFERENCE_SQUARED}
+
+
+def sequence_loss_workspace_size(n: int, sequences: int) -> int:
+    """Device workspace of policy_loss_forward and preference_loss_forward."""
+    return int(lib().sequence_loss_workspace_size(int(n), int(sequences)))
+
+
+def _values(t, name: str, n: int, dtype=None):
+    """A contiguous GPU tensor of ``n`` elements, fp32 unless ``dtype`` says
+    otherwise."""
+    import torch
+    _buf(t, name)
+    if t.dtype != (torch.float32 if dtype is None else dtype):
+        raise MuonError(MUON_ERR_BAD_DTYPE, f"{name} has dtype {t.dtype}")
+    if t.numel() != n:
+        raise MuonError(MUON_ERR_BAD_SHAPE, f"{name} has {t.numel()} elements, expected {n}")
+    return t
+
+
+def _mask(t, n: int):
+    import torch
+    if t is None:
+        return
+    _buf(t, "mask")
+    if t.dtype not in (torch.bool, torch.uint8):
+        raise MuonError(MUON_ERR_BAD_DTYPE, f"mask must be bool or uint8, has {t.dtype}")
+    if t.numel() != n:
+        raise MuonError(MUON_ERR_BAD_SHAPE, f"mask has {t.numel()} elements, expected {n}")
+
+
+def _sequences(offsets) -> int:
+    import torch
+    _buf(offsets, "offsets")
+    if offsets.dtype != torch.int32:
+        raise MuonError(MUON_ERR_BAD_DTYPE, f"offsets must be int32, has {offsets.dtype}")
+    if offsets.numel() < 1:
+        raise MuonError(MUON_ERR_BAD_SHAPE, "offsets must have sequences + 1 elements")
+    return offsets.numel() - 1
+
+
+def _policy_args(nll, old_nll, advantages, offsets, ref_nll, mask, clip_low, clip_high, kl_weight,
+                 mean, per_token):
+    """Checks the inputs that forward and backward share.  Returns n, the
+    number of sequences, the call's leading C arguments and the inputs."""
+    _buf(nll, "nll", dtypes=F32)
+    n, sequences = nll.numel(), _sequences(offsets)
+    _values(old_nll, "old_nll", n)
+    _values(advantages, "advantages", n if per_token else sequences)
+    if ref_nll is not None:
+        _values(ref_nll, "ref_nll", n)
+    elif kl_weight:
+        raise MuonError(MUON_ERR_INVALID_ARG, "kl_weight needs ref_nll")
+    _mask(mask, n)
+    ins = {"nll": nll, "old_nll": old_nll, "advantages": advantages, "offsets": offsets,
+           "ref_nll": ref_nll, "mask": mask}
+
+    def args():
+        return (_ptr(nll), _ptr(old_nll), _ptr(ref_nll), _ptr(mask), _ptr(advantages),
+                int(bool(per_token)), _ptr(offsets), sequences, n, float(clip_low),
+                float(clip_high), float(kl_weight), int(bool(mean)))
+
+    return n, sequences, args, ins
+
+
+def _vectors_apart(outs, ins, workspace):
+    """_outputs_apart for contiguous tensors, None among them."""
+    outs = {k: _vector(t) for k, t in outs.items() if t is not None}
+    if outs or workspace is not None:
+        _outputs_apart(outs, {k: _vector(t) for k, t in ins.items() if t is not None}, workspace)
+
+
+def policy_loss_forward(nll, old_nll, advantages, offsets, ref_nll=None, mask=None,
+                        clip_low: float = 0.2, clip_high: float = 0.2, kl_weight: float = 0.0,
+                        mean: bool = True, per_token: bool = False, loss=None, kl=None, count=None,
+                        clipped=None, workspace=None, stream=None):
+    """Clipped policy loss of packed sequences, sequence s being the tokens
+    [offsets[s], offsets[s + 1]) (int32 on the GPU).  nll: fp32 token losses
+    -log p, as lm_loss_forward returns them; old_nll: those the tokens were
+    drawn with; ref_nll: a reference's; advantages: fp32, one a sequence or
+    with ``per_token`` one a token; mask (bool or uint8): the tokens that
+    count, all by default.  A token's loss is
+    ``-min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl_weight k`` with
+    ``r = exp(old_nll - nll)`` and ``k = exp(x) - 1 - x``,
+    ``x = nll - ref_nll``; a sequence's the mean, or without ``mean`` the sum,
+    of its tokens that count.  Returns (loss, kl, count, clipped), one value a
+    sequence: fp32, the mean or sum of k (0 without ref_nll), int32 numbers
+    of tokens that count and of those that the clip holds."""
+    import torch
+    n, sequences, args, ins = _policy_args(nll, old_nll, advantages, offsets, ref_nll, mask,
+                                           clip_low, clip_high, kl_weight, mean, per_token)
+    outs = {"loss": loss, "kl": kl, "count": count, "clipped": clipped}
+    for name, t in outs.items():
+        if t is not None:
+            _values(t, name, sequences, torch.int32 if name[0] == "c" else None)
+    dev = _one_device(**ins, **outs, workspace=workspace)
+    _vectors_apart(outs, ins, workspace)
+    with _Launch(dev, stream) as on:
+        if loss is None:
+            loss = torch.empty(sequences, dtype=torch.float32, device=dev)
+        if kl is None:
+            kl = torch.empty(sequences, dtype=torch.float32, device=dev)
+        if count is None:
+            count = torch.empty(sequences, dtype=torch.int32, device=dev)
+        if clipped is None:
+            clipped = torch.empty(sequences, dtype=torch.int32, device=dev)
+        ws = workspace
+        if ws is None:
+            ws = _workspace(None, sequence_loss_workspace_size(n, sequences), dev)
+        _check(lib().policy_loss_forward(*args(), _ptr(loss), _ptr(kl), _ptr(count), _ptr(clipped),
+                                         _ptr(ws), _nbytes(ws), on.handle))
+    return loss, kl, count, clipped
+
+
+def policy_loss_backward(nll, old_nll, advantages, offsets, count, dloss, ref_nll=None, mask=None,
+                         clip_low: float = 0.2, clip_high: float = 0.2, kl_weight: float = 0.0,
+                         mean: bool = True, per_token: bool = False, dnll=None, stream=None):
+    """The gradient of ``sum(dloss * loss)`` by nll, which is the ``dloss`` of
+    lm_loss_backward; count from policy_loss_forward on the same inputs,
+    dloss fp32, one value a sequence.  dnll: fp32 of n; its tokens that belong
+    to no sequence are left as they were.  Without it a tensor is allocated,
+    with zeros there.  Returns dnll."""
+    import torch
+    n, sequences, args, ins = _policy_args(nll, old_nll, advantages, offsets, ref_nll, mask,
+                                           clip_low, clip_high, kl_weight, mean, per_token)
+    _values(count, "count", sequences, torch.int32)
+    _values(dloss, "dloss", sequences)
+    ins.update(count=count, dloss=dloss)
+    if dnll is not None:
+        _values(dnll, "dnll", n)
+    dev = _one_device(**ins, dnll=dnll)
+    _vectors_apart({"dnll": dnll}, ins, None)
+    with _Launch(dev, stream) as on:
+        if dnll is None:
+            dnll = torch.zeros(nll.shape, dtype=torch.float32, device=dev)
+        _check(lib().policy_loss_backward(*args(), _ptr(count), _ptr(dloss), _ptr(dnll), on.handle))
+    return dnll
+
+
+def _preference_kind(kind) -> int:
+    code = _PREFERENCE_KINDS.get(kind, kind)
+    if not isinstance(code, int):
+        raise MuonError(MUON_ERR_INVALID_ARG, f"unknown kind of preference loss {kind!r}")
+    return code
+
+
+def preference_loss_forward(nll, offsets, ref_nll=None, mask=None, beta: float = 0.1,
+                            kind="logistic", margin: float = 0.0, smoothing: float = 0.0,
+                            mean: bool = False, loss=None, margins=None, reward=None, count=None,
+                            workspace=None, stream=None):
+    """Preference loss of pairs of packed sequences: sequence 2 i is preferred
+    to sequence 2 i + 1.  nll, ref_nll, offsets and mask as for
+    policy_loss_forward.  A sequence's reward is beta times the sum (the mean
+    with ``mean``) of ``ref_nll - nll`` (``-nll`` without a reference) over its
+    tokens that count, and a pair's loss is f(x) of
+    ``x = reward[2 i] - reward[2 i + 1] - margin``: kind "logistic",
+    ``(1 - smoothing) log(1 + exp(-x)) + smoothing log(1 + exp(x))``; "hinge",
+    ``max(0, 1 - x)``; "squared", ``(1 - x)**2``.  A pair with a sequence in
+    which no token counts has loss 0 and no gradient.  Returns (loss, margins,
+    reward, count): fp32 of pairs (margins: the x), fp32 and int32 of
+    sequences."""
+    import torch
+    _buf(nll, "nll", dtypes=F32)
+    n, sequences = nll.numel(), _sequences(offsets)
+    if sequences % 2:
+        raise MuonError(MUON_ERR_BAD_SHAPE, f"{sequences} sequences: two to a pair")
+    code = _preference_kind(kind)
+    if ref_nll is not None:
+        _values(ref_nll, "ref_nll", n)
+    _mask(mask, n)
+    ins = {"nll": nll, "offsets": offsets, "ref_nll": ref_nll, "mask": mask}
+    outs = {"loss": loss, "margins": margins, "reward": reward, "count": count}
+    for name, t in outs.items():
+        if t is not None:
+            _values(t, name, sequences // (2 if name in ("loss", "margins") else 1),
+                    torch.int32 if name == "count" else None)
+    dev = _one_device(**ins, **outs, workspace=workspace)
+    _vectors_apart(outs, ins, workspace)
+    with _Launch(dev, stream) as on:
+        if loss is None:
+            loss = torch.empty(sequences // 2, dtype=torch.float32, device=dev)
+        if margins is None:
+            margins = torch.empty(sequences // 2, dtype=torch.float32, device=dev)
+        if reward is None:
+            reward = torch.empty(sequences, dtype=torch.float32, device=dev)
+        if count is None:
+            count = torch.empty(sequences, dtype=torch.int32, device=dev)
+        ws = workspace
+        if ws is None:
+            ws = _workspace(None, sequence_loss_workspace_size(n, sequences), dev)
+        _check(lib().preference_loss_forward(
+            _ptr(nll), _ptr(ref_nll), _ptr(mask), _ptr(offsets), sequences, n, code, float(beta),
+            float(margin), float(smoothing), int(bool(mean)), _ptr(loss), _ptr(margins),
+            _ptr(reward), _ptr(count), _ptr(ws), _nbytes(ws), on.handle))
+    return loss, margins, reward, count
+
+
+def preference_loss_backward(offsets, margins, count, dloss, n=None, mask=None, beta: float = 0.1,
+                             kind="logistic", smoothing: float = 0.0, mean: bool = False,
+                             dnll=None, stream=None):
+    """The gradient of ``sum(dloss * loss)`` by nll; margins and count from
+    preference_loss_forward, whose nll it does not need; dloss fp32, one value
+    a pair.  dnll as for policy_loss_backward; without it, ``n`` (the mask's
+    size by default) is the number of tokens.  Returns dnll."""
+    import torch
+    sequences = _sequences(offsets)
+    if sequences % 2:
+        raise MuonError(MUON_ERR_BAD_SHAPE, f"{sequences} sequences: two to a pair")
+    code = _preference_kind(kind)
+    for t in (dnll, mask):
+        if n is None and t is not None:
+            n = t.numel()
+    if n is None:
+        raise MuonError(MUON_ERR_INVALID_ARG, "n, mask or dnll must say how many tokens there are")
+    n = int(n)
+    _values(margins, "margins", sequences // 2)
+    _values(count, "count", sequences, torch.int32)
+    _values(dloss, "dloss", sequences // 2)
+    _mask(mask, n)
+    if dnll is not None:
+        _values(dnll, "dnll", n)
+    ins = {"offsets": offsets, "margins": margins, "count": count, "dloss": dloss, "mask": mask}
+    dev = _one_device(**ins, dnll=dnll)
+    _vectors_apart({"dnll": dnll}, ins, None)
+    with _Launch(dev, stream) as on:
+        if dnll is None:
+            if not 0 <= n < 1 << 26:
+                raise MuonError(MUON_ERR_BAD_SHAPE, "n must be in [0, 2^26)")
+            dnll = torch.zeros(n, dtype=torch.float32, device=dev)
+        _check(lib().preference_loss_backward(
+            _ptr(mask), _ptr(offsets), sequences, n, code, float(beta), float(smoothing),
+            int(bool(mean)), _ptr(margins), _ptr(count), _ptr(dloss), _ptr(dnll), on.handle))
+    return dnll
 
 
 # ---------------------------------------------------------- expert products
