@@ -229,7 +229,8 @@ def _run_own(s):
                                       s["dloss"], dnll=s["dnll"], **how)
         return loss, kl, count, clipped, dnll
     how = dict(mask=s["mask"], beta=BETA[case["mean"]], kind=case["kind"],
-               smoothing=case["smoothing"], mean=case["mean"])
+               smoothing=case["smoothing"] if case["kind"] == "logistic" else 0.0,
+               mean=case["mean"])
     loss, margin, reward, count = M.preference_loss_forward(
         s["nll"], s["offsets"], ref_nll=s["ref"], margin=MARGIN[case["mean"]], workspace=ws, **how)
     if not step:
