@@ -1175,68 +1175,81 @@ def sequence_loss_workspace_size(n: int, sequences: int) -> int:
     return int(lib().sequence_loss_workspace_size(int(n), int(sequences)))
 
 
-def _values(t, name: str, n: int, dtype=None):
-    """A contiguous GPU tensor of ``n`` elements, fp32 unless ``dtype`` says
-    otherwise."""
-    import torch
-    _buf(t, name)
-    if t.dtype != (torch.float32 if dtype is None else dtype):
-        raise MuonError(MUON_ERR_BAD_DTYPE, f"{name} has dtype {t.dtype}")
-    if t.numel() != n:
-        raise MuonError(MUON_ERR_BAD_SHAPE, f"{name} has {t.numel()} elements, expected {n}")
-    return t
+def _flat(device: int, specs, outputs: int = 0):
+    """The addresses (None for None) of contiguous tensors of GPU ``device``,
+    given as (name, tensor, elements, dtype), after all of them have been
+    checked; the first ``outputs`` of them share memory with no other.  (One
+    pass without a call per check: most of a small call's time is the
+    binding's.)"""
+    for name, t, n, dtype in specs:
+        if t is not None and (t.dtype is not dtype or t.numel() != n or t.get_device() != device
+                              or not t.is_contiguous()):
+            _buf(t, name)
+            if t.dtype is not dtype:
+                raise MuonError(MUON_ERR_BAD_DTYPE, f"{name} has dtype {t.dtype}, not {dtype}")
+            if t.numel() != n:
+                raise MuonError(MUON_ERR_BAD_SHAPE,
+                                f"{name} has {t.numel()} elements, expected {n}")
+            raise MuonError(MUON_ERR_INVALID_ARG, f"{name} is on {t.device}, others on {device}")
+    at = [None if s[1] is None else s[1].data_ptr() for s in specs]
+    for i in range(outputs):
+        lo = at[i]
+        if lo:
+            name, _, n, dtype = specs[i]
+            hi = lo + n * dtype.itemsize
+            for j in range(i + 1, len(at)):
+                b = at[j]
+                if b and b < hi and lo < b + specs[j][2] * specs[j][3].itemsize:
+                    raise MuonError(MUON_ERR_INVALID_ARG,
+                                    f"{name} shares memory with {specs[j][0]}")
+    return at
 
 
-def _mask(t, n: int):
+def _scratch(workspace):
+    """The caller's workspace as _flat takes it."""
+    if workspace is None:
+        return "workspace", None, 0, None
+    _buf(workspace, "workspace")
+    return "workspace", workspace, workspace.numel(), workspace.dtype
+
+
+def _mask_dtype(mask):
+    if mask is None:
+        return None
     import torch
-    if t is None:
-        return
-    _buf(t, "mask")
-    if t.dtype not in (torch.bool, torch.uint8):
-        raise MuonError(MUON_ERR_BAD_DTYPE, f"mask must be bool or uint8, has {t.dtype}")
-    if t.numel() != n:
-        raise MuonError(MUON_ERR_BAD_SHAPE, f"mask has {t.numel()} elements, expected {n}")
+    if mask.dtype not in (torch.bool, torch.uint8):
+        raise MuonError(MUON_ERR_BAD_DTYPE, f"mask must be bool or uint8, has {mask.dtype}")
+    return mask.dtype
+
+
+def _tokens(nll, offsets):
+    """Number of tokens, of sequences, and the GPU's index."""
+    if nll is None or not nll.is_cuda:
+        raise MuonError(MUON_ERR_INVALID_ARG, "nll must be a GPU tensor")
+    return nll.numel(), _sequences(offsets), nll.get_device()
 
 
 def _sequences(offsets) -> int:
-    import torch
-    _buf(offsets, "offsets")
-    if offsets.dtype != torch.int32:
-        raise MuonError(MUON_ERR_BAD_DTYPE, f"offsets must be int32, has {offsets.dtype}")
-    if offsets.numel() < 1:
+    if offsets is None or offsets.numel() < 1:
         raise MuonError(MUON_ERR_BAD_SHAPE, "offsets must have sequences + 1 elements")
     return offsets.numel() - 1
 
 
-def _policy_args(nll, old_nll, advantages, offsets, ref_nll, mask, clip_low, clip_high, kl_weight,
-                 mean, per_token):
-    """Checks the inputs that forward and backward share.  Returns n, the
-    number of sequences, the call's leading C arguments and the inputs."""
-    _buf(nll, "nll", dtypes=F32)
-    n, sequences = nll.numel(), _sequences(offsets)
-    _values(old_nll, "old_nll", n)
-    _values(advantages, "advantages", n if per_token else sequences)
-    if ref_nll is not None:
-        _values(ref_nll, "ref_nll", n)
-    elif kl_weight:
+def _policy_inputs(nll, old_nll, advantages, offsets, ref_nll, mask, kl_weight, per_token):
+    """What _tokens says, and the inputs that forward and backward share as
+    _flat takes them."""
+    import torch
+    f32 = torch.float32
+    n, sequences, device = _tokens(nll, offsets)
+    if old_nll is None or advantages is None:
+        raise MuonError(MUON_ERR_INVALID_ARG, "old_nll or advantages is None")
+    if ref_nll is None and kl_weight:
         raise MuonError(MUON_ERR_INVALID_ARG, "kl_weight needs ref_nll")
-    _mask(mask, n)
-    ins = {"nll": nll, "old_nll": old_nll, "advantages": advantages, "offsets": offsets,
-           "ref_nll": ref_nll, "mask": mask}
-
-    def args():
-        return (_ptr(nll), _ptr(old_nll), _ptr(ref_nll), _ptr(mask), _ptr(advantages),
-                int(bool(per_token)), _ptr(offsets), sequences, n, float(clip_low),
-                float(clip_high), float(kl_weight), int(bool(mean)))
-
-    return n, sequences, args, ins
-
-
-def _vectors_apart(outs, ins, workspace):
-    """_outputs_apart for contiguous tensors, None among them."""
-    outs = {k: _vector(t) for k, t in outs.items() if t is not None}
-    if outs or workspace is not None:
-        _outputs_apart(outs, {k: _vector(t) for k, t in ins.items() if t is not None}, workspace)
+    return n, sequences, device, (("nll", nll, n, f32), ("old_nll", old_nll, n, f32),
+                                  ("ref_nll", ref_nll, n, f32),
+                                  ("mask", mask, n, _mask_dtype(mask)),
+                                  ("advantages", advantages, n if per_token else sequences, f32),
+                                  ("offsets", offsets, sequences + 1, torch.int32))
 
 
 def policy_loss_forward(nll, old_nll, advantages, offsets, ref_nll=None, mask=None,
@@ -1256,28 +1269,28 @@ def policy_loss_forward(nll, old_nll, advantages, offsets, ref_nll=None, mask=No
     sequence: fp32, the mean or sum of k (0 without ref_nll), int32 numbers
     of tokens that count and of those that the clip holds."""
     import torch
-    n, sequences, args, ins = _policy_args(nll, old_nll, advantages, offsets, ref_nll, mask,
-                                           clip_low, clip_high, kl_weight, mean, per_token)
-    outs = {"loss": loss, "kl": kl, "count": count, "clipped": clipped}
-    for name, t in outs.items():
-        if t is not None:
-            _values(t, name, sequences, torch.int32 if name[0] == "c" else None)
-    dev = _one_device(**ins, **outs, workspace=workspace)
-    _vectors_apart(outs, ins, workspace)
-    with _Launch(dev, stream) as on:
+    n, sequences, device, ins = _policy_inputs(nll, old_nll, advantages, offsets, ref_nll, mask,
+                                               kl_weight, per_token)
+    f32, i32 = torch.float32, torch.int32
+    at = _flat(device, (("loss", loss, sequences, f32), ("kl", kl, sequences, f32),
+                        ("count", count, sequences, i32), ("clipped", clipped, sequences, i32),
+                        _scratch(workspace), *ins), 5)
+    with _Launch(nll.device, stream) as on:
         if loss is None:
-            loss = torch.empty(sequences, dtype=torch.float32, device=dev)
+            loss = nll.new_empty(sequences)
         if kl is None:
-            kl = torch.empty(sequences, dtype=torch.float32, device=dev)
+            kl = nll.new_empty(sequences)
         if count is None:
-            count = torch.empty(sequences, dtype=torch.int32, device=dev)
+            count = offsets.new_empty(sequences)
         if clipped is None:
-            clipped = torch.empty(sequences, dtype=torch.int32, device=dev)
-        ws = workspace
-        if ws is None:
-            ws = _workspace(None, sequence_loss_workspace_size(n, sequences), dev)
-        _check(lib().policy_loss_forward(*args(), _ptr(loss), _ptr(kl), _ptr(count), _ptr(clipped),
-                                         _ptr(ws), _nbytes(ws), on.handle))
+            clipped = offsets.new_empty(sequences)
+        if workspace is None:
+            workspace = _workspace(None, sequence_loss_workspace_size(n, sequences), nll.device)
+        _check(lib().policy_loss_forward(
+            at[5], at[6], at[7], at[8], at[9], 1 if per_token else 0, at[10], sequences, n,
+            clip_low, clip_high, kl_weight, 1 if mean else 0, loss.data_ptr(), kl.data_ptr(),
+            count.data_ptr(), clipped.data_ptr(), workspace.data_ptr(), _nbytes(workspace),
+            on.handle))
     return loss, kl, count, clipped
 
 
@@ -1290,19 +1303,20 @@ def policy_loss_backward(nll, old_nll, advantages, offsets, count, dloss, ref_nl
     to no sequence are left as they were.  Without it a tensor is allocated,
     with zeros there.  Returns dnll."""
     import torch
-    n, sequences, args, ins = _policy_args(nll, old_nll, advantages, offsets, ref_nll, mask,
-                                           clip_low, clip_high, kl_weight, mean, per_token)
-    _values(count, "count", sequences, torch.int32)
-    _values(dloss, "dloss", sequences)
-    ins.update(count=count, dloss=dloss)
-    if dnll is not None:
-        _values(dnll, "dnll", n)
-    dev = _one_device(**ins, dnll=dnll)
-    _vectors_apart({"dnll": dnll}, ins, None)
-    with _Launch(dev, stream) as on:
+    n, sequences, device, ins = _policy_inputs(nll, old_nll, advantages, offsets, ref_nll, mask,
+                                               kl_weight, per_token)
+    if count is None or dloss is None:
+        raise MuonError(MUON_ERR_INVALID_ARG, "count or dloss is None")
+    f32 = torch.float32
+    at = _flat(device, (("dnll", dnll, n, f32), *ins, ("count", count, sequences, torch.int32),
+                        ("dloss", dloss, sequences, f32)), 1)
+    with _Launch(nll.device, stream) as on:
         if dnll is None:
-            dnll = torch.zeros(nll.shape, dtype=torch.float32, device=dev)
-        _check(lib().policy_loss_backward(*args(), _ptr(count), _ptr(dloss), _ptr(dnll), on.handle))
+            dnll = torch.zeros(nll.shape, dtype=f32, device=nll.device)
+        _check(lib().policy_loss_backward(
+            at[1], at[2], at[3], at[4], at[5], 1 if per_token else 0, at[6], sequences, n,
+            clip_low, clip_high, kl_weight, 1 if mean else 0, at[7], at[8], dnll.data_ptr(),
+            on.handle))
     return dnll
 
 
@@ -1329,38 +1343,31 @@ def preference_loss_forward(nll, offsets, ref_nll=None, mask=None, beta: float =
     reward, count): fp32 of pairs (margins: the x), fp32 and int32 of
     sequences."""
     import torch
-    _buf(nll, "nll", dtypes=F32)
-    n, sequences = nll.numel(), _sequences(offsets)
+    n, sequences, device = _tokens(nll, offsets)
     if sequences % 2:
         raise MuonError(MUON_ERR_BAD_SHAPE, f"{sequences} sequences: two to a pair")
-    code = _preference_kind(kind)
-    if ref_nll is not None:
-        _values(ref_nll, "ref_nll", n)
-    _mask(mask, n)
-    ins = {"nll": nll, "offsets": offsets, "ref_nll": ref_nll, "mask": mask}
-    outs = {"loss": loss, "margins": margins, "reward": reward, "count": count}
-    for name, t in outs.items():
-        if t is not None:
-            _values(t, name, sequences // (2 if name in ("loss", "margins") else 1),
-                    torch.int32 if name == "count" else None)
-    dev = _one_device(**ins, **outs, workspace=workspace)
-    _vectors_apart(outs, ins, workspace)
-    with _Launch(dev, stream) as on:
+    code, pairs = _preference_kind(kind), sequences // 2
+    f32, i32 = torch.float32, torch.int32
+    at = _flat(device, (("loss", loss, pairs, f32), ("margins", margins, pairs, f32),
+                        ("reward", reward, sequences, f32), ("count", count, sequences, i32),
+                        _scratch(workspace), ("nll", nll, n, f32), ("ref_nll", ref_nll, n, f32),
+                        ("mask", mask, n, _mask_dtype(mask)),
+                        ("offsets", offsets, sequences + 1, i32)), 5)
+    with _Launch(nll.device, stream) as on:
         if loss is None:
-            loss = torch.empty(sequences // 2, dtype=torch.float32, device=dev)
+            loss = nll.new_empty(pairs)
         if margins is None:
-            margins = torch.empty(sequences // 2, dtype=torch.float32, device=dev)
+            margins = nll.new_empty(pairs)
         if reward is None:
-            reward = torch.empty(sequences, dtype=torch.float32, device=dev)
+            reward = nll.new_empty(sequences)
         if count is None:
-            count = torch.empty(sequences, dtype=torch.int32, device=dev)
-        ws = workspace
-        if ws is None:
-            ws = _workspace(None, sequence_loss_workspace_size(n, sequences), dev)
+            count = offsets.new_empty(sequences)
+        if workspace is None:
+            workspace = _workspace(None, sequence_loss_workspace_size(n, sequences), nll.device)
         _check(lib().preference_loss_forward(
-            _ptr(nll), _ptr(ref_nll), _ptr(mask), _ptr(offsets), sequences, n, code, float(beta),
-            float(margin), float(smoothing), int(bool(mean)), _ptr(loss), _ptr(margins),
-            _ptr(reward), _ptr(count), _ptr(ws), _nbytes(ws), on.handle))
+            at[5], at[6], at[7], at[8], sequences, n, code, beta, margin, smoothing,
+            1 if mean else 0, loss.data_ptr(), margins.data_ptr(), reward.data_ptr(),
+            count.data_ptr(), workspace.data_ptr(), _nbytes(workspace), on.handle))
     return loss, margins, reward, count
 
 
@@ -1382,23 +1389,24 @@ def preference_loss_backward(offsets, margins, count, dloss, n=None, mask=None, 
     if n is None:
         raise MuonError(MUON_ERR_INVALID_ARG, "n, mask or dnll must say how many tokens there are")
     n = int(n)
-    _values(margins, "margins", sequences // 2)
-    _values(count, "count", sequences, torch.int32)
-    _values(dloss, "dloss", sequences // 2)
-    _mask(mask, n)
-    if dnll is not None:
-        _values(dnll, "dnll", n)
-    ins = {"offsets": offsets, "margins": margins, "count": count, "dloss": dloss, "mask": mask}
-    dev = _one_device(**ins, dnll=dnll)
-    _vectors_apart({"dnll": dnll}, ins, None)
+    if margins is None or count is None or dloss is None:
+        raise MuonError(MUON_ERR_INVALID_ARG, "margins, count or dloss is None")
+    if not offsets.is_cuda:
+        raise MuonError(MUON_ERR_INVALID_ARG, "offsets must be a GPU tensor")
+    dev, f32 = offsets.device, torch.float32
+    at = _flat(offsets.get_device(), (("dnll", dnll, n, f32), ("mask", mask, n, _mask_dtype(mask)),
+                                      ("offsets", offsets, sequences + 1, torch.int32),
+                                      ("margins", margins, sequences // 2, f32),
+                                      ("count", count, sequences, torch.int32),
+                                      ("dloss", dloss, sequences // 2, f32)), 1)
     with _Launch(dev, stream) as on:
         if dnll is None:
             if not 0 <= n < 1 << 26:
                 raise MuonError(MUON_ERR_BAD_SHAPE, "n must be in [0, 2^26)")
-            dnll = torch.zeros(n, dtype=torch.float32, device=dev)
+            dnll = torch.zeros(n, dtype=f32, device=dev)
         _check(lib().preference_loss_backward(
-            _ptr(mask), _ptr(offsets), sequences, n, code, float(beta), float(smoothing),
-            int(bool(mean)), _ptr(margins), _ptr(count), _ptr(dloss), _ptr(dnll), on.handle))
+            at[1], at[2], sequences, n, code, beta, smoothing, 1 if mean else 0, at[3], at[4],
+            at[5], dnll.data_ptr(), on.handle))
     return dnll
 
 

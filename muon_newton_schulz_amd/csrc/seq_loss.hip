@@ -26,6 +26,7 @@
 // every time.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "train_common.h"
 
@@ -43,33 +44,89 @@ struct Offsets {
   __device__ __forceinline__ int at(int s) const { return min(max(p[s], 0), n); }
 };
 
-// The sequences of a lane's eight tokens, tile by tile.
-struct Walk {
-  int next;  // the first sequence (count: the end) that starts at the tile or later
+// A lane's value from a lane before it (dpp: in registers, without the LDS
+// trip of a shuffle); `none` where there is none.
+enum : int { kShr1 = 0x111, kShr2 = 0x112, kShr4 = 0x114, kShr8 = 0x118, kWaveShr1 = 0x138,
+             kBcast15 = 0x142, kBcast31 = 0x143 };
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp(int x, int none) {
+  return __builtin_amdgcn_update_dpp(none, x, CTRL, ROWS, 0xf, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp(double x) {
+  const int2 v = __builtin_bit_cast(int2, x);
+  return __builtin_bit_cast(double, int2{dpp<CTRL, ROWS>(v.x, 0), dpp<CTRL, ROWS>(v.y, 0)});
+}
+// f over the steps of an inclusive scan of the wave: 1, 2, 4 and 8 lanes within
+// rows of 16, then rows 0 and 2 into the next, then the first half into the
+// second.
+template <typename F>
+__device__ __forceinline__ void scan_steps(F&& f) {
+  f(std::integral_constant<int, kShr1>{}, std::integral_constant<int, 0xf>{});
+  f(std::integral_constant<int, kShr2>{}, std::integral_constant<int, 0xf>{});
+  f(std::integral_constant<int, kShr4>{}, std::integral_constant<int, 0xf>{});
+  f(std::integral_constant<int, kShr8>{}, std::integral_constant<int, 0xf>{});
+  f(std::integral_constant<int, kBcast15>{}, std::integral_constant<int, 0xa>{});
+  f(std::integral_constant<int, kBcast31>{}, std::integral_constant<int, 0xc>{});
+}
+__device__ __forceinline__ double last_lane(double x) {
+  const int2 v = __builtin_bit_cast(int2, x);
+  return __builtin_bit_cast(double, int2{__builtin_amdgcn_readlane(v.x, 63),
+                                         __builtin_amdgcn_readlane(v.y, 63)});
+}
 
-  // 64-way search: the number of offsets below `token`
-  __device__ __forceinline__ void find(const Offsets& off, int token, int lane) {
+// The sequences of a lane's eight tokens, tile by tile.  A wave keeps 64
+// offsets, one a lane, and what Source::of gives for their sequences, and loads
+// others only when its tiles have passed them: a load a tile would be most of
+// the time of a short span.
+template <typename Source>
+struct Walk {
+  using Value = typename Source::Value;
+  int next;      // the first sequence (count: the end) that starts at the tile or later
+  int batch;     // lane's offset and value are those of sequence batch + lane
+  int offset;
+  Value value, prior;  // prior: of sequence batch - 1
+  bool moved;          // whether the last tile went past the batch
+
+  __device__ __forceinline__ static bool valid(const Offsets& off, int s) {
+    return s >= 0 && s < off.count;
+  }
+  __device__ __forceinline__ void load(const Offsets& off, const Source& w, int first, int lane) {
+    batch = first;
+    offset = first + lane <= off.count ? off.at(first + lane) : off.n + kTile;
+    value = valid(off, first + lane) ? w.of(first + lane) : Value{};
+  }
+  // 64-way search for the number of offsets below `token`
+  __device__ __forceinline__ void find(const Offsets& off, const Source& w, int token, int lane) {
     int lo = 0, len = off.count + 1;
-    while (len > 0) {
+    while (len > 64) {
       const int step = (len + 63) >> 6, q = lane * step + step - 1;
       const bool below = q < len && off.at(lo + q) < token;
       const int c = __popcll(__ballot(below));
       lo += c * step;
       len = min(step - 1, len - c * step);
     }
-    next = __builtin_amdgcn_readfirstlane(lo);
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    load(off, w, lo, lane);
+    prior = valid(off, lo - 1) ? w.of(lo - 1) : Value{};
+    next = lo + __popcll(__ballot(lane < len && offset < token));
   }
   // Marks the starts in the tile: start[j] is the sequence that starts at the
-  // lane's token j, or -1; before: the one its first token is in unless it
+  // lane's token j, or -1; s: the one its first token is in unless it
   // starts there (-1 and count: none).  Returns whether any starts.
-  __device__ __forceinline__ bool tile(const Offsets& off, int tile0, int lane, int* lds,
-                                       int (&start)[kPer], int& before) {
-    before = next - 1;
+  __device__ __forceinline__ bool tile(const Offsets& off, const Source& w, int tile0, int lane,
+                                       int* lds, int (&start)[kPer], int& s) {
+    s = next - 1;
+    moved = false;
     bool any = false;
-    for (;;) {
-      const int s = next + lane;
-      const int o = s <= off.count ? off.at(s) - tile0 : kTile;
-      const uint64_t in = __ballot(o < kTile);
+    while (next <= off.count) {
+      if (next >= batch + 64) {
+        prior = value.lane(63);
+        load(off, w, next, lane);
+        moved = any;
+      }
+      const int o = offset - tile0;
+      const uint64_t in = __ballot(batch + lane >= next && o < kTile);
       if (in == 0) break;
       if (!any) {
         any = true;
@@ -78,10 +135,9 @@ struct Walk {
         wave_sync();
       }
       // of several that start at a token all but the last are empty
-      if (o >= 0 && o < kTile) atomicMax(&lds[o], s);
-      const int c = __popcll(in);
-      next += c;
-      if (c < 64) break;
+      if ((in >> lane & 1) != 0 && o >= 0) atomicMax(&lds[o], batch + lane);
+      next += __popcll(in);
+      if (next < batch + 64) break;
     }
 #pragma unroll
     for (int j = 0; j < kPer; ++j) start[j] = -1;
@@ -94,15 +150,31 @@ struct Walk {
       last = max(last, start[j]);
     }
     wave_sync();  // read before the next tile's marks
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int u = __shfl_up(last, o, 64);
-      if (lane >= o) last = max(last, u);
-    }
-    const int u = __shfl_up(last, 1, 64);
-    if (lane > 0) before = max(before, u);
+    scan_steps([&](auto ctrl, auto rows) {
+      last = max(last, dpp<decltype(ctrl)::value, decltype(rows)::value>(last, -1));
+    });
+    s = max(s, dpp<kWaveShr1, 0xf>(last, -1));
     return true;
   }
+  // the value of a sequence of the last tile; every lane of the wave calls it
+  __device__ __forceinline__ Value of(const Offsets& off, const Source& w, int s) const {
+    if (moved) return valid(off, s) ? w.of(s) : Value{};
+    const Value v = value.lane(max(s - batch, 0));
+    return s < batch ? prior : v;
+  }
+};
+
+// What a walk keeps of a sequence: nothing, or some fp32 values.
+struct Nothing {
+  __device__ __forceinline__ Nothing lane(int) const { return {}; }
+};
+struct One {
+  float a;
+  __device__ __forceinline__ One lane(int l) const { return {__shfl(a, l, 64)}; }
+};
+struct Two {
+  float a, b;
+  __device__ __forceinline__ Two lane(int l) const { return {__shfl(a, l, 64), __shfl(b, l, 64)}; }
 };
 
 // Eight values from token i on, those below n; 0 past it.
@@ -126,16 +198,20 @@ struct Sums {
     c += o.c;
     d += o.d;
   }
-  __device__ __forceinline__ Sums up(int o) const {
-    return {__shfl_up(a, o, 64), __shfl_up(b, o, 64), __shfl_up(c, o, 64), __shfl_up(d, o, 64)};
+  // those of a lane before, 0 where there is none
+  template <int CTRL, int ROWS>
+  __device__ __forceinline__ Sums before() const {
+    return {dpp<CTRL, ROWS>(a), dpp<CTRL, ROWS>(b), dpp<CTRL, ROWS>(c, 0), dpp<CTRL, ROWS>(d, 0)};
   }
-  __device__ __forceinline__ Sums other(int o) const {
-    return {__shfl_xor(a, o, 64), __shfl_xor(b, o, 64), __shfl_xor(c, o, 64), __shfl_xor(d, o, 64)};
+  __device__ __forceinline__ Sums last() const {
+    return {last_lane(a), last_lane(b), __builtin_amdgcn_readlane(c, 63),
+            __builtin_amdgcn_readlane(d, 63)};
   }
   template <int G>
   __device__ __forceinline__ void join() {
 #pragma unroll
-    for (int o = G / 2; o > 0; o >>= 1) add(other(o));
+    for (int o = G / 2; o > 0; o >>= 1)
+      add({__shfl_xor(a, o, 64), __shfl_xor(b, o, 64), __shfl_xor(c, o, 64), __shfl_xor(d, o, 64)});
   }
 };
 
@@ -159,113 +235,160 @@ __device__ __forceinline__ void exp_terms(float x, float& em1, float& k) {
   }
 }
 
+// A lane's tokens.
+struct Tokens {
+  float nll[kPer], old_nll[kPer], ref[kPer], adv[kPer];
+  uint8_t mask[kPer];
+};
+
 struct PolicyArgs {
   const float *nll, *old_nll, *ref, *adv;
   const uint8_t* mask;
-  // The clip as bounds of d: r > 1 + hi where d > log(1 + hi).  Compared in
-  // fp64, where the difference of two fp32 values is exact but for the last bits
-  // of very unlike ones: a ratio next to the border is on its own side of it.
+  // The clip as bounds of d: r > 1 + hi where d > log(1 + hi).  (The exact
+  // difference against the fp64 bound: a ratio next to the border is on its own
+  // side of it.)
   double d_low, d_high;
+  float f_low, f_high;  // the bounds rounded to fp32
   float r_low, r_high, kl_weight;
   int per_token;
 
-  __device__ __forceinline__ bool clipped(float a, double d) const {
-    return (a > 0.0f && d > d_high) || (a < 0.0f && d < d_low);
+  __device__ __forceinline__ void load(int64_t i, int64_t n, Tokens& t) const {
+    load_tokens(nll, i, n, t.nll);
+    load_tokens(old_nll, i, n, t.old_nll);
+    if (ref != nullptr) load_tokens(ref, i, n, t.ref);
+    if (mask != nullptr) load_tokens(mask, i, n, t.mask);
+    if (per_token) load_tokens(adv, i, n, t.adv);
+  }
+  // Rounding keeps the order, so unless d rounds to what the bound rounds to,
+  // fp32 decides as the exact difference does.
+  __device__ __forceinline__ bool clipped(float a, float nll_j, float old_j, float d) const {
+    bool cut = a > 0.0f ? d > f_high : a < 0.0f && d < f_low;
+    if (d == (a > 0.0f ? f_high : f_low)) {
+      const double e = static_cast<double>(old_j) - static_cast<double>(nll_j);
+      cut = a > 0.0f ? e > d_high : a < 0.0f && e < d_low;
+    }
+    return cut;
   }
   // r A; no 0 inf where an advantage of 0 meets a ratio beyond fp32
-  static __device__ __forceinline__ float ratio(float a, double d) {
-    return a == 0.0f ? 0.0f : expf(static_cast<float>(d)) * a;
+  static __device__ __forceinline__ float ratio(float a, float d) {
+    return a == 0.0f ? 0.0f : expf(d) * a;
   }
 };
 
 struct PolicyTerms {
   PolicyArgs p;
-  float nll[kPer], old_nll[kPer], ref[kPer], adv[kPer];
-  uint8_t mask[kPer];
-  __device__ __forceinline__ void load(int64_t i, int64_t n) {
-    load_tokens(p.nll, i, n, nll);
-    load_tokens(p.old_nll, i, n, old_nll);
-    if (p.ref != nullptr) load_tokens(p.ref, i, n, ref);
-    if (p.mask != nullptr) load_tokens(p.mask, i, n, mask);
-    if (p.per_token) load_tokens(p.adv, i, n, adv);
-  }
-  float a;  // of the sequence
-  __device__ __forceinline__ void sequence(int s) {
-    if (!p.per_token) a = p.adv[s];
-  }
-  __device__ __forceinline__ void add(int j, Sums& sum) const {
-    if (p.mask != nullptr && !mask[j]) return;
-    const float at = p.per_token ? adv[j] : a;
-    const double d = static_cast<double>(old_nll[j]) - static_cast<double>(nll[j]);
-    const bool cut = p.clipped(at, d);
-    float token = cut ? -(at > 0.0f ? p.r_high : p.r_low) * at : -PolicyArgs::ratio(at, d);
-    if (p.ref != nullptr) {
-      float em1, k;
-      exp_terms(nll[j] - ref[j], em1, k);
-      if (p.kl_weight != 0.0f) token = __builtin_fmaf(p.kl_weight, k, token);
-      sum.b += k;
+  using Value = One;  // the sequence's advantage
+  __device__ __forceinline__ Value of(int s) const { return {p.per_token ? 0.0f : p.adv[s]}; }
+  __device__ __forceinline__ void load(int64_t i, int64_t n, Tokens& t) const { p.load(i, n, t); }
+  // what a token adds to its sequence's sums
+  struct Term {
+    float a, b;
+    int c, d;
+    __device__ __forceinline__ Sums sums() const { return {a, b, c, d}; }
+    __device__ __forceinline__ Term operator+(const Term& o) const {
+      return {a + o.a, b + o.b, c + o.c, d + o.d};
     }
-    sum.a += token;
-    sum.c += 1;
-    sum.d += cut;
+  };
+  __device__ __forceinline__ Term term(const Tokens& t, int j, bool in, Value v) const {
+    const float at = p.per_token ? t.adv[j] : v.a;
+    const float d = t.old_nll[j] - t.nll[j];
+    const bool cut = p.clipped(at, t.nll[j], t.old_nll[j], d);
+    Term r{cut ? -(at > 0.0f ? p.r_high : p.r_low) * at : -PolicyArgs::ratio(at, d), 0.0f, 1, cut};
+    if (p.ref != nullptr) {
+      float em1;
+      exp_terms(t.nll[j] - t.ref[j], em1, r.b);
+      if (p.kl_weight != 0.0f) r.a = __builtin_fmaf(p.kl_weight, r.b, r.a);
+    }
+    return in && (p.mask == nullptr || t.mask[j]) ? r : Term{0.0f, 0.0f, 0, 0};
   }
 };
 
 struct PreferenceTerms {
-  const float *nll_p, *ref_p;
-  const uint8_t* mask_p;
-  float nll[kPer], ref[kPer];
-  uint8_t mask[kPer];
-  __device__ __forceinline__ void load(int64_t i, int64_t n) {
-    load_tokens(nll_p, i, n, nll);
-    if (ref_p != nullptr) load_tokens(ref_p, i, n, ref);
-    if (mask_p != nullptr) load_tokens(mask_p, i, n, mask);
+  const float *nll, *ref;
+  const uint8_t* mask;
+  using Value = Nothing;
+  __device__ __forceinline__ Value of(int) const { return {}; }
+  __device__ __forceinline__ void load(int64_t i, int64_t n, Tokens& t) const {
+    load_tokens(nll, i, n, t.nll);
+    if (ref != nullptr) load_tokens(ref, i, n, t.ref);
+    if (mask != nullptr) load_tokens(mask, i, n, t.mask);
   }
-  __device__ __forceinline__ void sequence(int) {}
-  __device__ __forceinline__ void add(int j, Sums& sum) const {
-    if (mask_p != nullptr && !mask[j]) return;
-    sum.a += (ref_p != nullptr ? static_cast<double>(ref[j]) : 0.0) - static_cast<double>(nll[j]);
-    sum.c += 1;
+  // fp64 throughout: the sum is multiplied by beta and stands in an exponent
+  struct Term {
+    double a;
+    int c;
+    __device__ __forceinline__ Sums sums() const { return {a, 0.0, c, 0}; }
+    __device__ __forceinline__ Term operator+(const Term& o) const { return {a + o.a, c + o.c}; }
+  };
+  __device__ __forceinline__ Term term(const Tokens& t, int j, bool in, Value) const {
+    const double a = (ref != nullptr ? static_cast<double>(t.ref[j]) : 0.0) -
+                     static_cast<double>(t.nll[j]);
+    return in && (mask == nullptr || t.mask[j]) ? Term{a, 1} : Term{0.0, 0};
   }
 };
 
+// The sums of span `at`, by a wave.
 template <typename Terms>
-__global__ __launch_bounds__(kThreads) void k_seq_sums(Terms w, Offsets off, int64_t span,
-                                                       Sums* __restrict__ head,
-                                                       Sums* __restrict__ carry) {
-  __shared__ int marks[kWaves][kTile];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * kWaves + wave;
+__device__ __forceinline__ void span_sums(const Terms& w, const Offsets& off, int64_t span,
+                                          int64_t at, int lane, int* marks, Sums* head,
+                                          Sums* carry) {
   const int64_t n = off.n, t0 = at * span, t1 = min(t0 + span, n);
   if (t0 >= n) return;
   const Sums none{0.0, 0.0, 0, 0};
-  Sums open = none;    // the lane's part of the sequence that the tile starts within
+  // the part of the sequence that the tile starts within: spread over the
+  // lanes, or the last lane's alone
+  Sums open = none;
+  bool spread = false;
   bool fresh = false;  // whether that sequence started in this span
-  Walk walk;
-  walk.find(off, static_cast<int>(t0), lane);
   auto valid = [&](int s) { return s >= 0 && s < off.count; };
+  auto whole = [&]() {  // open as a whole, in every lane
+    if (spread)
+      scan_steps([&](auto ctrl, auto rows) {
+        open.add(open.template before<decltype(ctrl)::value, decltype(rows)::value>());
+      });
+    open = open.last();
+  };
+  Tokens tok, ahead;
+  w.load(t0 + lane * kPer, n, tok);
+  Walk<Terms> walk;
+  walk.find(off, w, static_cast<int>(t0), lane);
   for (int64_t tile0 = t0; tile0 < t1; tile0 += kTile) {
-    w.load(tile0 + lane * kPer, n);
+    if (tile0 + kTile < t1) w.load(tile0 + kTile + lane * kPer, n, ahead);
     int start[kPer], s;
-    const bool any = walk.tile(off, static_cast<int>(tile0), lane, marks[wave], start, s);
+    const bool any = walk.tile(off, w, static_cast<int>(tile0), lane, marks, start, s);
     // tokens past n are in no sequence: off.n ends the last one at the latest
     const int left = static_cast<int>(min(n - tile0, static_cast<int64_t>(kTile))) - lane * kPer;
+    typename Terms::Term r[kPer];
     if (!any) {
       if (valid(s)) {
-        w.sequence(s);
+        const auto v = walk.of(off, w, s);
 #pragma unroll
-        for (int j = 0; j < kPer; ++j)
-          if (j < left) w.add(j, open);
+        for (int j = 0; j < kPer; ++j) r[j] = w.term(tok, j, j < left, v);
+        // pairwise in the terms' type (fp32: each addition is off by half a
+        // step of what it adds, as a term is of itself), then in fp64
+#pragma unroll
+        for (int o = 1; o < kPer; o <<= 1)
+#pragma unroll
+          for (int j = 0; j < kPer; j += 2 * o) r[j] = r[j] + r[j + o];
+        open.add(r[0].sums());
+        spread = true;
       }
+      tok = ahead;
       continue;
+    }
+    const int first = s;
+    {
+      int q = s;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        q = max(q, start[j]);
+        r[j] = w.term(tok, j, j < left && valid(q), walk.of(off, w, q));
+      }
     }
     // the lane's tokens before its first start, those behind its last, and
     // the sequences between them, whole
     Sums lead = none, sum = none;
     bool has = false;
-    int first = s;
-    if (valid(s)) w.sequence(s);
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       if (start[j] >= 0) {
@@ -274,35 +397,24 @@ __global__ __launch_bounds__(kThreads) void k_seq_sums(Terms w, Offsets off, int
         has = true;
         sum = none;
         s = start[j];
-        if (valid(s)) w.sequence(s);
       }
-      if (j < left && valid(s)) w.add(j, sum);
+      sum.add(r[j].sums());
     }
-    open.template join<64>();
+    whole();
     // inclusive scan of the parts since the last start
     Sums scan = sum;
-    bool seen = has;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const Sums u = scan.up(o);
-      const bool us = __shfl_up(static_cast<int>(seen), o, 64);
-      if (lane >= o && !seen) {
-        scan.add(u);
-        seen = us;
-      }
-    }
+    int seen = has;
+    scan_steps([&](auto ctrl, auto rows) {
+      constexpr int C = decltype(ctrl)::value, R = decltype(rows)::value;
+      const Sums u = scan.template before<C, R>();
+      const int us = dpp<C, R>(seen, 0);
+      if (!seen) scan.add(u);
+      seen |= us;
+    });
     // what the lane's first start ends
-    Sums end = scan.up(1);
-    bool inside = __shfl_up(static_cast<int>(seen), 1, 64);
-    if (lane == 0) {
-      end = none;
-      inside = false;
-    }
-    if (!inside) {
-      Sums o = open;
-      o.add(end);
-      end = o;
-    }
+    Sums end = scan.template before<kWaveShr1, 0xf>();
+    const bool inside = dpp<kWaveShr1, 0xf>(seen, 0) != 0;
+    if (!inside) end.add(open);
     end.add(lead);
     if (has) {
       if (inside || fresh) {
@@ -311,22 +423,33 @@ __global__ __launch_bounds__(kThreads) void k_seq_sums(Terms w, Offsets off, int
         carry[at] = end;
       }
     }
-    // (a start in the tile: the last lane has seen one)
+    // (with a start in the tile, the last lane has seen one)
     open = lane == 63 ? scan : none;
+    spread = false;
     fresh = true;
+    tok = ahead;
   }
-  open.template join<64>();
+  whole();
   if (lane != 0) return;
   if (!fresh) carry[at] = open;
   else if (valid(walk.next - 1)) head[walk.next - 1] = open;
+}
+
+template <typename Terms>
+__global__ __launch_bounds__(kThreads) void k_seq_sums(Terms w, Offsets off, int64_t span,
+                                                       Sums* __restrict__ head,
+                                                       Sums* __restrict__ carry) {
+  __shared__ int marks[kWaves][kTile];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  span_sums(w, off, span, static_cast<int64_t>(blockIdx.x) * kWaves + wave, threadIdx.x & 63,
+            marks[wave], head, carry);
 }
 
 // A sequence's sums: its part in the span where it starts and the carries of
 // the spans behind, G lanes.
 template <int G>
 __device__ __forceinline__ Sums sequence_sums(const Offsets& off, int s, int64_t span,
-                                              const Sums* __restrict__ head,
-                                              const Sums* __restrict__ carry) {
+                                              const Sums* head, const Sums* carry) {
   Sums sum{0.0, 0.0, 0, 0};
   const int l = threadIdx.x % G;
   if (s < off.count) {
@@ -345,21 +468,20 @@ struct PolicyOut {
   float *loss, *kl;
   int32_t *count, *clipped;
   int mean;
+  // of results: sequences
+  __device__ __forceinline__ int results(const Offsets& off) const { return off.count; }
+  template <int G>
+  __device__ __forceinline__ void finish(const Offsets& off, int s, int64_t span, const Sums* head,
+                                         const Sums* carry) const {
+    const Sums sum = sequence_sums<G>(off, s, span, head, carry);
+    if (s >= off.count || threadIdx.x % G != 0) return;
+    const double part = mean ? 1.0 / max(sum.c, 1) : 1.0;
+    loss[s] = static_cast<float>(sum.a * part);
+    kl[s] = static_cast<float>(sum.b * part);
+    count[s] = sum.c;
+    clipped[s] = sum.d;
+  }
 };
-template <int G>
-__global__ __launch_bounds__(kThreads) void k_policy_join(Offsets off, int64_t span,
-                                                          const Sums* __restrict__ head,
-                                                          const Sums* __restrict__ carry,
-                                                          PolicyOut o) {
-  const int s = blockIdx.x * (kThreads / G) + threadIdx.x / G;
-  const Sums sum = sequence_sums<G>(off, s, span, head, carry);
-  if (s >= off.count || threadIdx.x % G != 0) return;
-  const double part = o.mean ? 1.0 / max(sum.c, 1) : 1.0;
-  o.loss[s] = static_cast<float>(sum.a * part);
-  o.kl[s] = static_cast<float>(sum.b * part);
-  o.count[s] = sum.c;
-  o.clipped[s] = sum.d;
-}
 
 struct PreferenceHow {
   int kind, mean;
@@ -386,88 +508,107 @@ __device__ __forceinline__ float preference_slope(const PreferenceHow& h, float 
 struct PreferenceOut {
   float *loss, *margin, *reward;
   int32_t* count;
+  PreferenceHow h;
+  // of results: pairs
+  __device__ __forceinline__ int results(const Offsets& off) const { return off.count / 2; }
+  template <int G>
+  __device__ __forceinline__ void finish(const Offsets& off, int i, int64_t span, const Sums* head,
+                                         const Sums* carry) const {
+    double value[2];
+    int tokens[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const Sums sum =
+          sequence_sums<G>(off, i < off.count / 2 ? 2 * i + k : off.count, span, head, carry);
+      value[k] = h.beta * sum.a;
+      if (h.mean) value[k] /= max(sum.c, 1);
+      tokens[k] = sum.c;
+    }
+    if (i >= off.count / 2 || threadIdx.x % G != 0) return;
+    const double x = value[0] - value[1] - h.margin;
+    margin[i] = static_cast<float>(x);
+    loss[i] = tokens[0] > 0 && tokens[1] > 0 ? static_cast<float>(preference(h, x)) : 0.0f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      reward[2 * i + k] = static_cast<float>(value[k]);
+      count[2 * i + k] = tokens[k];
+    }
+  }
 };
-template <int G>
-__global__ __launch_bounds__(kThreads) void k_preference_join(Offsets off, int64_t span,
-                                                              const Sums* __restrict__ head,
-                                                              const Sums* __restrict__ carry,
-                                                              PreferenceHow h, PreferenceOut o) {
-  const int i = blockIdx.x * (kThreads / G) + threadIdx.x / G;
-  const int pairs = off.count / 2;
-  double reward[2];
-  int count[2];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const Sums sum = sequence_sums<G>(off, i < pairs ? 2 * i + k : off.count, span, head, carry);
-    reward[k] = h.beta * sum.a;
-    if (h.mean) reward[k] /= max(sum.c, 1);
-    count[k] = sum.c;
-  }
-  if (i >= pairs || threadIdx.x % G != 0) return;
-  const double x = reward[0] - reward[1] - h.margin;
-  o.margin[i] = static_cast<float>(x);
-  o.loss[i] = count[0] > 0 && count[1] > 0 ? static_cast<float>(preference(h, x)) : 0.0f;
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    o.reward[2 * i + k] = static_cast<float>(reward[k]);
-    o.count[2 * i + k] = count[k];
-  }
+
+template <int G, typename Out>
+__global__ __launch_bounds__(kThreads) void k_seq_join(Offsets off, int64_t span,
+                                                       const Sums* __restrict__ head,
+                                                       const Sums* __restrict__ carry, Out out) {
+  out.template finish<G>(off, blockIdx.x * (kThreads / G) + threadIdx.x / G, span, head, carry);
+}
+
+// Few tokens and few sequences: the sums and their join in one workgroup, with
+// a wave for each span, the parts in LDS.
+constexpr int kSmallThreads = 1024, kSmallWaves = kSmallThreads / 64;
+constexpr int kSmallTokens = 16384, kSmallSequences = 1024;
+template <typename Terms, typename Out>
+__global__ __launch_bounds__(kSmallThreads) void k_seq_small(Terms w, Offsets off, int64_t span,
+                                                             Out out) {
+  __shared__ int marks[kSmallWaves][kTile];
+  __shared__ Sums head[kSmallSequences], carry[kSmallWaves];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  span_sums(w, off, span, static_cast<int64_t>(wave), threadIdx.x & 63, marks[wave], head, carry);
+  __syncthreads();
+  constexpr int G = kSmallWaves;  // as many lanes as there can be spans
+  for (int r0 = 0; r0 < out.results(off); r0 += blockDim.x / G)
+    out.template finish<G>(off, r0 + threadIdx.x / G, span, head, carry);
 }
 
 struct PolicySlope {
-  PolicyTerms w;
+  PolicyArgs p;
   const float* dloss;
   const int32_t* count;
   int mean;
-  float each;
-  __device__ __forceinline__ void load(int64_t i, int64_t n) { w.load(i, n); }
-  __device__ __forceinline__ void sequence(int s) {
-    w.sequence(s);
-    each = dloss[s];
-    if (mean) each /= static_cast<float>(max(count[s], 1));
+  using Value = Two;  // the sequence's advantage, and its factor of a token's slope
+  __device__ __forceinline__ void load(int64_t i, int64_t n, Tokens& t) const { p.load(i, n, t); }
+  __device__ __forceinline__ Value of(int s) const {
+    Value v{p.per_token ? 0.0f : p.adv[s], dloss[s]};
+    if (mean) v.b /= static_cast<float>(max(count[s], 1));
+    return v;
   }
-  __device__ __forceinline__ float slope(int j) const {
-    if (w.p.mask != nullptr && !w.mask[j]) return 0.0f;
-    const float at = w.p.per_token ? w.adv[j] : w.a;
-    const double d = static_cast<double>(w.old_nll[j]) - static_cast<double>(w.nll[j]);
-    float g = w.p.clipped(at, d) ? 0.0f : PolicyArgs::ratio(at, d);
-    if (w.p.kl_weight != 0.0f) {
+  __device__ __forceinline__ float slope(const Tokens& t, int j, Value v) const {
+    const float at = p.per_token ? t.adv[j] : v.a;
+    const float d = t.old_nll[j] - t.nll[j];
+    float g = p.clipped(at, t.nll[j], t.old_nll[j], d) ? 0.0f : PolicyArgs::ratio(at, d);
+    if (p.kl_weight != 0.0f) {
       float em1, k;
-      exp_terms(w.nll[j] - w.ref[j], em1, k);
-      g = __builtin_fmaf(w.p.kl_weight, em1, g);
+      exp_terms(t.nll[j] - t.ref[j], em1, k);
+      g = __builtin_fmaf(p.kl_weight, em1, g);
     }
-    return each * g;
+    return p.mask == nullptr || t.mask[j] ? v.b * g : 0.0f;
   }
 };
 
 struct PreferenceSlope {
   const float *margin, *dloss;
   const int32_t* count;
-  const uint8_t* mask_p;
+  const uint8_t* mask;
   PreferenceHow h;
-  float each;
-  uint8_t mask[kPer];
-  __device__ __forceinline__ void load(int64_t i, int64_t n) {
-    if (mask_p != nullptr) load_tokens(mask_p, i, n, mask);
+  using Value = One;  // a token's slope
+  __device__ __forceinline__ void load(int64_t i, int64_t n, Tokens& t) const {
+    if (mask != nullptr) load_tokens(mask, i, n, t.mask);
   }
-  __device__ __forceinline__ void sequence(int s) {
-    const int i = s >> 1, mine = count[s];
-    if (mine <= 0 || count[s ^ 1] <= 0) {
-      each = 0.0f;
-      return;
-    }
+  __device__ __forceinline__ Value of(int s) const {
+    const int i = s >> 1, mine = count[s], other = count[s ^ 1];
     const float g = h.beta * dloss[i] * preference_slope(h, margin[i]);
-    each = (s & 1) != 0 ? g : -g;
-    if (h.mean) each /= static_cast<float>(mine);
+    if (mine <= 0 || other <= 0) return {0.0f};
+    const float v = (s & 1) != 0 ? g : -g;
+    return {h.mean ? v / static_cast<float>(mine) : v};
   }
-  __device__ __forceinline__ float slope(int j) const {
-    return mask_p != nullptr && !mask[j] ? 0.0f : each;
+  __device__ __forceinline__ float slope(const Tokens& t, int j, Value v) const {
+    return mask != nullptr && !t.mask[j] ? 0.0f : v.a;
   }
 };
 
 // dnll of the tokens that are in a sequence.
 template <typename Slope>
-__global__ __launch_bounds__(kThreads) void k_seq_slopes(Slope w, Offsets off, int64_t span,
+__global__ __launch_bounds__(kThreads) void k_seq_slopes(const Slope w, Offsets off, int64_t span,
                                                          float* __restrict__ dnll) {
   __shared__ int marks[kWaves][kTile];
   const int lane = threadIdx.x & 63;
@@ -475,26 +616,34 @@ __global__ __launch_bounds__(kThreads) void k_seq_slopes(Slope w, Offsets off, i
   const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWaves + wave) * span;
   const int64_t n = off.n, t1 = min(t0 + span, n);
   if (t0 >= n) return;
-  Walk walk;
-  walk.find(off, static_cast<int>(t0), lane);
+  Tokens tok, ahead;
+  w.load(t0 + lane * kPer, n, tok);
+  Walk<Slope> walk;
+  walk.find(off, w, static_cast<int>(t0), lane);
   auto valid = [&](int s) { return s >= 0 && s < off.count; };
   for (int64_t tile0 = t0; tile0 < t1; tile0 += kTile) {
     const int64_t i = tile0 + lane * kPer;
-    w.load(i, n);
+    if (tile0 + kTile < t1) w.load(i + kTile, n, ahead);
     int start[kPer], s;
-    walk.tile(off, static_cast<int>(tile0), lane, marks[wave], start, s);
+    const bool any = walk.tile(off, w, static_cast<int>(tile0), lane, marks[wave], start, s);
     float g[kPer];
     bool write[kPer], all = i + kPer <= n;
-    if (valid(s)) w.sequence(s);
+    if (!any) {
+      const auto v = walk.of(off, w, s);
+      all &= valid(s);
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      if (start[j] >= 0) {
-        s = start[j];
-        if (valid(s)) w.sequence(s);
+      for (int j = 0; j < kPer; ++j) {
+        write[j] = i + j < n && valid(s);
+        g[j] = w.slope(tok, j, v);
       }
-      write[j] = i + j < n && valid(s);
-      all &= write[j];
-      g[j] = write[j] ? w.slope(j) : 0.0f;
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        s = max(s, start[j]);
+        write[j] = i + j < n && valid(s);
+        all &= write[j];
+        g[j] = w.slope(tok, j, walk.of(off, w, s));
+      }
     }
     if (all) {
       __builtin_memcpy(dnll + i, g, sizeof(g));
@@ -503,6 +652,7 @@ __global__ __launch_bounds__(kThreads) void k_seq_slopes(Slope w, Offsets off, i
       for (int j = 0; j < kPer; ++j)
         if (write[j]) dnll[i + j] = g[j];
     }
+    tok = ahead;
   }
 }
 
@@ -563,6 +713,8 @@ PolicyArgs policy_args(const float* nll, const float* old_nll, const float* ref_
   p.mask = mask;
   p.d_low = std::log1p(-clip_low);  // -inf for 1
   p.d_high = std::log1p(clip_high);
+  p.f_low = static_cast<float>(p.d_low);
+  p.f_high = static_cast<float>(p.d_high);
   p.r_low = static_cast<float>(1.0 - clip_low);
   p.r_high = static_cast<float>(1.0 + clip_high);
   p.kl_weight = kl_weight;
@@ -583,12 +735,23 @@ int check_preference(int64_t sequences, int32_t kind, float beta, float margin, 
   return MUON_OK;
 }
 
-template <typename Terms>
-void launch_sums(const Terms& w, const Offsets& off, Sums* head, Sums* carry, hipStream_t s) {
+template <typename Terms, typename Out>
+void launch_sums(const Terms& w, const Offsets& off, int64_t results, Sums* head, Sums* carry,
+                 const Out& out, hipStream_t s) {
+  if (off.n <= kSmallTokens && off.count <= kSmallSequences) {
+    const int span = std::max((off.n + kSmallWaves * kTile - 1) / (kSmallWaves * kTile), 1) * kTile;
+    const int waves = std::max((off.n + span - 1) / span, 4);
+    hipLaunchKernelGGL((k_seq_small<Terms, Out>), dim3(1), dim3(64 * waves), 0, s, w, off, span,
+                       out);
+    return;
+  }
   const int64_t blocks = (spans_of(off.n) + kWaves - 1) / kWaves;
   if (blocks > 0)
     hipLaunchKernelGGL(k_seq_sums<Terms>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, s,
                        w, off, span_of(off.n), head, carry);
+  hipLaunchKernelGGL((k_seq_join<64, Out>),
+                     dim3(static_cast<unsigned>((results + kWaves - 1) / kWaves)), dim3(kThreads),
+                     0, s, off, std::max<int64_t>(span_of(off.n), 1), head, carry, out);
 }
 template <typename Slope>
 void launch_slopes(const Slope& w, const Offsets& off, float* dnll, hipStream_t s) {
@@ -631,11 +794,8 @@ int policy_loss_forward(const float* nll, const float* old_nll, const float* ref
   const Offsets off{offsets, static_cast<int>(sequences), static_cast<int>(n)};
   PolicyTerms terms{};
   terms.p = p;
-  launch_sums(terms, off, head, carry, stream);
-  const unsigned blocks = static_cast<unsigned>((sequences + kWaves - 1) / kWaves);
-  hipLaunchKernelGGL(k_policy_join<64>, dim3(blocks), dim3(kThreads), 0, stream, off,
-                     std::max<int64_t>(span_of(n), 1), head, carry,
-                     PolicyOut{loss, kl, count, clipped, mean != 0});
+  launch_sums(terms, off, sequences, head, carry, PolicyOut{loss, kl, count, clipped, mean != 0},
+              stream);
   return check_launch("policy loss launch");
 }
 
@@ -653,8 +813,8 @@ int policy_loss_backward(const float* nll, const float* old_nll, const float* re
   if (count == nullptr || dloss == nullptr || dnll == nullptr)
     return set_error(MUON_ERR_INVALID_ARG, "count, dloss or dnll is null");
   PolicySlope slope{};
-  slope.w.p = p;
-  if (kl_weight == 0.0f) slope.w.p.ref = nullptr;
+  slope.p = p;
+  if (kl_weight == 0.0f) slope.p.ref = nullptr;
   slope.dloss = dloss;
   slope.count = count;
   slope.mean = mean != 0;
@@ -683,15 +843,13 @@ int preference_loss_forward(const float* nll, const float* ref_nll, const uint8_
   Sums* carry = reinterpret_cast<Sums*>(static_cast<char*>(workspace) + w.carry);
   const Offsets off{offsets, static_cast<int>(sequences), static_cast<int>(n)};
   PreferenceTerms terms{};
-  terms.nll_p = nll;
-  terms.ref_p = ref_nll;
-  terms.mask_p = mask;
-  launch_sums(terms, off, head, carry, stream);
-  const unsigned blocks = static_cast<unsigned>((sequences / 2 + kWaves - 1) / kWaves);
-  hipLaunchKernelGGL(k_preference_join<64>, dim3(blocks), dim3(kThreads), 0, stream, off,
-                     std::max<int64_t>(span_of(n), 1), head, carry,
-                     PreferenceHow{kind, mean != 0, beta, margin, smoothing},
-                     PreferenceOut{loss, margins, reward, count});
+  terms.nll = nll;
+  terms.ref = ref_nll;
+  terms.mask = mask;
+  launch_sums(terms, off, sequences / 2, head, carry,
+              PreferenceOut{loss, margins, reward, count,
+                            PreferenceHow{kind, mean != 0, beta, margin, smoothing}},
+              stream);
   return check_launch("preference loss launch");
 }
 
@@ -710,7 +868,7 @@ int preference_loss_backward(const uint8_t* mask, const int32_t* offsets, int64_
   slope.margin = margins;
   slope.dloss = dloss;
   slope.count = count;
-  slope.mask_p = mask;
+  slope.mask = mask;
   slope.h = PreferenceHow{kind, mean != 0, beta, 0.0f, smoothing};
   launch_slopes(slope, Offsets{offsets, static_cast<int>(sequences), static_cast<int>(n)}, dnll,
                 stream);
