@@ -156,11 +156,34 @@ struct Walk {
     s = max(s, dpp<kWaveShr1, 0xf>(last, -1));
     return true;
   }
-  // the value of a sequence of the last tile; every lane of the wave calls it
-  __device__ __forceinline__ Value of(const Offsets& off, const Source& w, int s) const {
-    if (moved) return valid(off, s) ? w.of(s) : Value{};
-    const Value v = value.lane(max(s - batch, 0));
-    return s < batch ? prior : v;
+  // The values of the sequences that the lane's tokens of the last tile are
+  // in, and which of the tokens are in one.  any, s, start: tile's.
+  __device__ __forceinline__ int values(const Offsets& off, const Source& w, bool any, int s,
+                                        const int (&start)[kPer], Value (&v)[kPer]) const {
+    if (!any) {
+      const Value x = value.lane(max(s - batch, 0)), y = s < batch ? prior : x;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) v[j] = y;
+      return valid(off, s) ? 0xff : 0;
+    }
+    int in = 0;
+    if (!moved) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        s = max(s, start[j]);
+        const Value x = value.lane(max(s - batch, 0));
+        v[j] = s < batch ? prior : x;
+        in |= static_cast<int>(valid(off, s)) << j;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        s = max(s, start[j]);
+        v[j] = valid(off, s) ? w.of(s) : Value{};
+        in |= static_cast<int>(valid(off, s)) << j;
+      }
+    }
+    return in;
   }
 };
 
@@ -177,15 +200,37 @@ struct Two {
   __device__ __forceinline__ Two lane(int l) const { return {__shfl(a, l, 64), __shfl(b, l, 64)}; }
 };
 
-// Eight values from token i on, those below n; 0 past it.
-template <typename T>
-__device__ __forceinline__ void load_tokens(const T* p, int64_t i, int64_t n, T (&v)[kPer]) {
-  if (i + kPer <= n) {
-    __builtin_memcpy(v, p + i, sizeof(v));
+// A lane's tokens.
+struct Tokens {
+  float nll[kPer], old_nll[kPer], ref[kPer], adv[kPer];
+  uint8_t mask[kPer];
+};
+// Eight values from token i on; WHOLE: all of them below n, else the last one
+// in place of those past it.
+template <bool WHOLE, typename T>
+__device__ __forceinline__ void load_values(const T* p, int i, int n, T (&v)[kPer]) {
+  if constexpr (WHOLE) {
+    __builtin_memcpy(v, p + static_cast<uint32_t>(i), sizeof(v));
   } else {
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) v[j] = i + j < n ? p[i + j] : T{};
+    for (int j = 0; j < kPer; ++j) v[j] = p[static_cast<uint32_t>(min(i + j, n - 1))];
   }
+}
+template <typename Source>
+__device__ __forceinline__ void load_tile(const Source& w, int tile0, int lane, int n, Tokens& t) {
+  if (tile0 + kTile <= n) w.template load<true>(tile0 + lane * kPer, n, t);
+  else w.template load<false>(tile0 + lane * kPer, n, t);
+}
+// Which of eight tokens from i on are below n and not masked.
+__device__ __forceinline__ int counting(const Tokens& t, const uint8_t* mask, int i, int n) {
+  int in = i + kPer <= n ? 0xff : (1 << max(n - i, 0)) - 1;
+  if (mask != nullptr) {
+    int m = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) m |= (t.mask[j] != 0 ? 1 : 0) << j;
+    in &= m;
+  }
+  return in;
 }
 
 // Sums over tokens.
@@ -215,31 +260,35 @@ struct Sums {
   }
 };
 
-// e^x - 1 and e^x - 1 - x, whose difference of near values a polynomial
-// replaces below |x| = 1/2: x^2 (1/2 + x / 6 + ... + x^6 / 40320), off by
-// 2 x^7 / 9! < 2^-24 of itself.
-__device__ __forceinline__ void exp_terms(float x, float& em1, float& k) {
-  if (fabsf(x) < 0.5f) {
+// e^x - 1 and e^x - 1 - x of eight values.  The second is a difference of near
+// values, which a polynomial replaces below |x| = 1/2: x^2 (1/2 + x / 6 + ... +
+// x^6 / 40320), off by 2 x^7 / 9! < 2^-24 of itself.
+__device__ __forceinline__ void exp_terms(const float (&x)[kPer], float (&em1)[kPer],
+                                          float (&k)[kPer]) {
+  bool far = false;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
     float p = 1.0f / 40320.0f;
-    p = __builtin_fmaf(p, x, 1.0f / 5040.0f);
-    p = __builtin_fmaf(p, x, 1.0f / 720.0f);
-    p = __builtin_fmaf(p, x, 1.0f / 120.0f);
-    p = __builtin_fmaf(p, x, 1.0f / 24.0f);
-    p = __builtin_fmaf(p, x, 1.0f / 6.0f);
-    p = __builtin_fmaf(p, x, 0.5f);
-    k = x * x * p;
-    em1 = x + k;
-  } else {
-    em1 = expf(x) - 1.0f;
-    k = em1 - x;
+    p = __builtin_fmaf(p, x[j], 1.0f / 5040.0f);
+    p = __builtin_fmaf(p, x[j], 1.0f / 720.0f);
+    p = __builtin_fmaf(p, x[j], 1.0f / 120.0f);
+    p = __builtin_fmaf(p, x[j], 1.0f / 24.0f);
+    p = __builtin_fmaf(p, x[j], 1.0f / 6.0f);
+    p = __builtin_fmaf(p, x[j], 0.5f);
+    k[j] = x[j] * x[j] * p;
+    em1[j] = x[j] + k[j];
+    far |= !(fabsf(x[j]) < 0.5f);
+  }
+  if (__ballot(far) == 0) return;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const float e = expf(x[j]) - 1.0f;
+    if (!(fabsf(x[j]) < 0.5f)) {
+      em1[j] = e;
+      k[j] = e - x[j];
+    }
   }
 }
-
-// A lane's tokens.
-struct Tokens {
-  float nll[kPer], old_nll[kPer], ref[kPer], adv[kPer];
-  uint8_t mask[kPer];
-};
 
 struct PolicyArgs {
   const float *nll, *old_nll, *ref, *adv;
@@ -252,26 +301,44 @@ struct PolicyArgs {
   float r_low, r_high, kl_weight;
   int per_token;
 
-  __device__ __forceinline__ void load(int64_t i, int64_t n, Tokens& t) const {
-    load_tokens(nll, i, n, t.nll);
-    load_tokens(old_nll, i, n, t.old_nll);
-    if (ref != nullptr) load_tokens(ref, i, n, t.ref);
-    if (mask != nullptr) load_tokens(mask, i, n, t.mask);
-    if (per_token) load_tokens(adv, i, n, t.adv);
+  template <bool WHOLE>
+  __device__ __forceinline__ void load(int i, int n, Tokens& t) const {
+    load_values<WHOLE>(nll, i, n, t.nll);
+    load_values<WHOLE>(old_nll, i, n, t.old_nll);
+    if (ref != nullptr) load_values<WHOLE>(ref, i, n, t.ref);
+    if (mask != nullptr) load_values<WHOLE>(mask, i, n, t.mask);
+    if (per_token) load_values<WHOLE>(adv, i, n, t.adv);
   }
-  // Rounding keeps the order, so unless d rounds to what the bound rounds to,
-  // fp32 decides as the exact difference does.
-  __device__ __forceinline__ bool clipped(float a, float nll_j, float old_j, float d) const {
-    bool cut = a > 0.0f ? d > f_high : a < 0.0f && d < f_low;
-    if (d == (a > 0.0f ? f_high : f_low)) {
-      const double e = static_cast<double>(old_j) - static_cast<double>(nll_j);
-      cut = a > 0.0f ? e > d_high : a < 0.0f && e < d_low;
+  // Which of the tokens the clip holds, and the ratios (0 where A is, so
+  // that no 0 inf comes of a ratio beyond fp32).  Rounding keeps the order, so
+  // unless d rounds to what the bound rounds to, fp32 decides as the exact
+  // difference does.
+  __device__ __forceinline__ int ratios(const Tokens& t, const float (&a)[kPer],
+                                        float (&r)[kPer]) const {
+    int cut = 0;
+    bool border = false;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const float d = t.old_nll[j] - t.nll[j];
+      const bool up = a[j] > 0.0f;
+      cut |= static_cast<int>(up ? d > f_high : a[j] < 0.0f && d < f_low) << j;
+      border |= d == (up ? f_high : f_low);
+      r[j] = a[j] == 0.0f ? 0.0f : expf(d);
+    }
+    if (__ballot(border) == 0) return cut;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const double e = static_cast<double>(t.old_nll[j]) - static_cast<double>(t.nll[j]);
+      const bool c = a[j] > 0.0f ? e > d_high : a[j] < 0.0f && e < d_low;
+      cut = (cut & ~(1 << j)) | static_cast<int>(c) << j;
     }
     return cut;
   }
-  // r A; no 0 inf where an advantage of 0 meets a ratio beyond fp32
-  static __device__ __forceinline__ float ratio(float a, float d) {
-    return a == 0.0f ? 0.0f : expf(d) * a;
+  __device__ __forceinline__ void kl(const Tokens& t, float (&em1)[kPer], float (&k)[kPer]) const {
+    float x[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) x[j] = t.nll[j] - t.ref[j];
+    exp_terms(x, em1, k);
   }
 };
 
@@ -279,60 +346,84 @@ struct PolicyTerms {
   PolicyArgs p;
   using Value = One;  // the sequence's advantage
   __device__ __forceinline__ Value of(int s) const { return {p.per_token ? 0.0f : p.adv[s]}; }
-  __device__ __forceinline__ void load(int64_t i, int64_t n, Tokens& t) const { p.load(i, n, t); }
-  // what a token adds to its sequence's sums
+  __device__ __forceinline__ const uint8_t* mask() const { return p.mask; }
+  template <bool WHOLE>
+  __device__ __forceinline__ void load(int i, int n, Tokens& t) const {
+    p.load<WHOLE>(i, n, t);
+  }
+  // What a token adds to its sequence's sums; of at most a lane's eight.
   struct Term {
     float a, b;
-    int c, d;
-    __device__ __forceinline__ Sums sums() const { return {a, b, c, d}; }
+    int n;  // tokens, and << 16 those that the clip holds
+    __device__ __forceinline__ Sums sums() const { return {a, b, n & 0xffff, n >> 16}; }
     __device__ __forceinline__ Term operator+(const Term& o) const {
-      return {a + o.a, b + o.b, c + o.c, d + o.d};
+      return {a + o.a, b + o.b, n + o.n};
     }
   };
-  __device__ __forceinline__ Term term(const Tokens& t, int j, bool in, Value v) const {
-    const float at = p.per_token ? t.adv[j] : v.a;
-    const float d = t.old_nll[j] - t.nll[j];
-    const bool cut = p.clipped(at, t.nll[j], t.old_nll[j], d);
-    Term r{cut ? -(at > 0.0f ? p.r_high : p.r_low) * at : -PolicyArgs::ratio(at, d), 0.0f, 1, cut};
-    if (p.ref != nullptr) {
-      float em1;
-      exp_terms(t.nll[j] - t.ref[j], em1, r.b);
-      if (p.kl_weight != 0.0f) r.a = __builtin_fmaf(p.kl_weight, r.b, r.a);
+  __device__ __forceinline__ void terms(const Tokens& t, int in, const Value (&v)[kPer],
+                                        Term (&r)[kPer]) const {
+    float a[kPer], ratio[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) a[j] = p.per_token ? t.adv[j] : v[j].a;
+    const int cut = p.ratios(t, a, ratio);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const bool c = (cut >> j) & 1;
+      r[j].a = -(c ? (a[j] > 0.0f ? p.r_high : p.r_low) : ratio[j]) * a[j];
+      r[j].b = 0.0f;
+      r[j].n = c ? 0x10001 : 1;
     }
-    return in && (p.mask == nullptr || t.mask[j]) ? r : Term{0.0f, 0.0f, 0, 0};
+    if (p.ref != nullptr) {
+      float em1[kPer], k[kPer];
+      p.kl(t, em1, k);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        r[j].b = k[j];
+        if (p.kl_weight != 0.0f) r[j].a = __builtin_fmaf(p.kl_weight, k[j], r[j].a);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (((in >> j) & 1) == 0) r[j] = Term{0.0f, 0.0f, 0};
   }
 };
 
 struct PreferenceTerms {
   const float *nll, *ref;
-  const uint8_t* mask;
+  const uint8_t* mask_p;
   using Value = Nothing;
   __device__ __forceinline__ Value of(int) const { return {}; }
-  __device__ __forceinline__ void load(int64_t i, int64_t n, Tokens& t) const {
-    load_tokens(nll, i, n, t.nll);
-    if (ref != nullptr) load_tokens(ref, i, n, t.ref);
-    if (mask != nullptr) load_tokens(mask, i, n, t.mask);
+  __device__ __forceinline__ const uint8_t* mask() const { return mask_p; }
+  template <bool WHOLE>
+  __device__ __forceinline__ void load(int i, int n, Tokens& t) const {
+    load_values<WHOLE>(nll, i, n, t.nll);
+    if (ref != nullptr) load_values<WHOLE>(ref, i, n, t.ref);
+    if (mask_p != nullptr) load_values<WHOLE>(mask_p, i, n, t.mask);
   }
   // fp64 throughout: the sum is multiplied by beta and stands in an exponent
   struct Term {
     double a;
-    int c;
-    __device__ __forceinline__ Sums sums() const { return {a, 0.0, c, 0}; }
-    __device__ __forceinline__ Term operator+(const Term& o) const { return {a + o.a, c + o.c}; }
+    int n;
+    __device__ __forceinline__ Sums sums() const { return {a, 0.0, n, 0}; }
+    __device__ __forceinline__ Term operator+(const Term& o) const { return {a + o.a, n + o.n}; }
   };
-  __device__ __forceinline__ Term term(const Tokens& t, int j, bool in, Value) const {
-    const double a = (ref != nullptr ? static_cast<double>(t.ref[j]) : 0.0) -
-                     static_cast<double>(t.nll[j]);
-    return in && (mask == nullptr || t.mask[j]) ? Term{a, 1} : Term{0.0, 0};
+  __device__ __forceinline__ void terms(const Tokens& t, int in, const Value (&)[kPer],
+                                        Term (&r)[kPer]) const {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const double a = (ref != nullptr ? static_cast<double>(t.ref[j]) : 0.0) -
+                       static_cast<double>(t.nll[j]);
+      r[j] = ((in >> j) & 1) != 0 ? Term{a, 1} : Term{0.0, 0};
+    }
   }
 };
 
 // The sums of span `at`, by a wave.
 template <typename Terms>
-__device__ __forceinline__ void span_sums(const Terms& w, const Offsets& off, int64_t span,
-                                          int64_t at, int lane, int* marks, Sums* head,
-                                          Sums* carry) {
-  const int64_t n = off.n, t0 = at * span, t1 = min(t0 + span, n);
+__device__ __forceinline__ void span_sums(const Terms& w, const Offsets& off, int span, int at,
+                                          int lane, int* marks, Sums* head, Sums* carry) {
+  using Term = typename Terms::Term;
+  const int n = off.n, t0 = at * span, t1 = min(t0 + span, n);
   if (t0 >= n) return;
   const Sums none{0.0, 0.0, 0, 0};
   // the part of the sequence that the tile starts within: spread over the
@@ -348,62 +439,60 @@ __device__ __forceinline__ void span_sums(const Terms& w, const Offsets& off, in
       });
     open = open.last();
   };
-  Tokens tok, ahead;
-  w.load(t0 + lane * kPer, n, tok);
+  Tokens tok;
+  load_tile(w, t0, lane, n, tok);
   Walk<Terms> walk;
-  walk.find(off, w, static_cast<int>(t0), lane);
-  for (int64_t tile0 = t0; tile0 < t1; tile0 += kTile) {
-    if (tile0 + kTile < t1) w.load(tile0 + kTile + lane * kPer, n, ahead);
+  walk.find(off, w, t0, lane);
+  for (int tile0 = t0; tile0 < t1; tile0 += kTile) {
     int start[kPer], s;
-    const bool any = walk.tile(off, w, static_cast<int>(tile0), lane, marks, start, s);
-    // tokens past n are in no sequence: off.n ends the last one at the latest
-    const int left = static_cast<int>(min(n - tile0, static_cast<int64_t>(kTile))) - lane * kPer;
-    typename Terms::Term r[kPer];
+    const bool any = walk.tile(off, w, tile0, lane, marks, start, s);
+    typename Terms::Value v[kPer];
+    Term r[kPer];
+    const int in = walk.values(off, w, any, s, start, v) &
+                   counting(tok, w.mask(), tile0 + lane * kPer, n);
+    w.terms(tok, in, v, r);
+    // (the next tile's loads run during the sums below)
+    if (tile0 + kTile < t1) load_tile(w, tile0 + kTile, lane, n, tok);
     if (!any) {
-      if (valid(s)) {
-        const auto v = walk.of(off, w, s);
+      // pairwise in the terms' type (fp32: each addition is off by half a
+      // step of what it adds, as a term is of itself), then in fp64
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) r[j] = w.term(tok, j, j < left, v);
-        // pairwise in the terms' type (fp32: each addition is off by half a
-        // step of what it adds, as a term is of itself), then in fp64
+      for (int o = 1; o < kPer; o <<= 1)
 #pragma unroll
-        for (int o = 1; o < kPer; o <<= 1)
-#pragma unroll
-          for (int j = 0; j < kPer; j += 2 * o) r[j] = r[j] + r[j + o];
-        open.add(r[0].sums());
-        spread = true;
-      }
-      tok = ahead;
+        for (int j = 0; j < kPer; j += 2 * o) r[j] = r[j] + r[j + o];
+      open.add(r[0].sums());
+      spread = true;
       continue;
     }
-    const int first = s;
-    {
-      int q = s;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        q = max(q, start[j]);
-        r[j] = w.term(tok, j, j < left && valid(q), walk.of(off, w, q));
-      }
-    }
-    // the lane's tokens before its first start, those behind its last, and
-    // the sequences between them, whole
-    Sums lead = none, sum = none;
-    bool has = false;
+    // the lane's tokens before its first start, and those from its last on
+    Term lead{}, sum{};
+    int starts = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      if (start[j] >= 0) {
-        if (!has) lead = sum;
-        else if (valid(s)) head[s] = sum;
-        has = true;
-        sum = none;
-        s = start[j];
+      const bool here = start[j] >= 0;
+      if (here && starts == 0) lead = sum;
+      if (here) sum = Term{};
+      starts += here;
+      sum = sum + r[j];
+    }
+    // the sequences between them, whole
+    if (__ballot(starts > 1) != 0) {
+      Term part{};
+      int q = -1;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        if (start[j] >= 0) {
+          if (valid(q)) head[q] = part.sums();
+          q = start[j];
+          part = Term{};
+        }
+        part = part + r[j];
       }
-      sum.add(r[j].sums());
     }
     whole();
     // inclusive scan of the parts since the last start
-    Sums scan = sum;
-    int seen = has;
+    Sums scan = sum.sums();
+    int seen = starts > 0;
     scan_steps([&](auto ctrl, auto rows) {
       constexpr int C = decltype(ctrl)::value, R = decltype(rows)::value;
       const Sums u = scan.template before<C, R>();
@@ -415,10 +504,10 @@ __device__ __forceinline__ void span_sums(const Terms& w, const Offsets& off, in
     Sums end = scan.template before<kWaveShr1, 0xf>();
     const bool inside = dpp<kWaveShr1, 0xf>(seen, 0) != 0;
     if (!inside) end.add(open);
-    end.add(lead);
-    if (has) {
+    end.add(lead.sums());
+    if (starts > 0) {
       if (inside || fresh) {
-        if (valid(first)) head[first] = end;
+        if (valid(s)) head[s] = end;
       } else {
         carry[at] = end;
       }
@@ -427,7 +516,6 @@ __device__ __forceinline__ void span_sums(const Terms& w, const Offsets& off, in
     open = lane == 63 ? scan : none;
     spread = false;
     fresh = true;
-    tok = ahead;
   }
   whole();
   if (lane != 0) return;
@@ -436,19 +524,19 @@ __device__ __forceinline__ void span_sums(const Terms& w, const Offsets& off, in
 }
 
 template <typename Terms>
-__global__ __launch_bounds__(kThreads) void k_seq_sums(Terms w, Offsets off, int64_t span,
+__global__ __launch_bounds__(kThreads) void k_seq_sums(Terms w, Offsets off, int span,
                                                        Sums* __restrict__ head,
                                                        Sums* __restrict__ carry) {
   __shared__ int marks[kWaves][kTile];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  span_sums(w, off, span, static_cast<int64_t>(blockIdx.x) * kWaves + wave, threadIdx.x & 63,
+  span_sums(w, off, span, static_cast<int>(blockIdx.x) * kWaves + wave, threadIdx.x & 63,
             marks[wave], head, carry);
 }
 
 // A sequence's sums: its part in the span where it starts and the carries of
 // the spans behind, G lanes.
 template <int G>
-__device__ __forceinline__ Sums sequence_sums(const Offsets& off, int s, int64_t span,
+__device__ __forceinline__ Sums sequence_sums(const Offsets& off, int s, int span,
                                               const Sums* head, const Sums* carry) {
   Sums sum{0.0, 0.0, 0, 0};
   const int l = threadIdx.x % G;
@@ -456,8 +544,8 @@ __device__ __forceinline__ Sums sequence_sums(const Offsets& off, int s, int64_t
     const int lo = off.at(s), hi = off.at(s + 1);
     if (lo < hi) {
       if (l == 0) sum = head[s];
-      const int64_t last = (hi - 1) / span;
-      for (int64_t k = lo / span + 1 + l; k <= last; k += G) sum.add(carry[k]);
+      const int last = (hi - 1) / span;
+      for (int k = lo / span + 1 + l; k <= last; k += G) sum.add(carry[k]);
     }
   }
   sum.template join<G>();
@@ -471,7 +559,7 @@ struct PolicyOut {
   // of results: sequences
   __device__ __forceinline__ int results(const Offsets& off) const { return off.count; }
   template <int G>
-  __device__ __forceinline__ void finish(const Offsets& off, int s, int64_t span, const Sums* head,
+  __device__ __forceinline__ void finish(const Offsets& off, int s, int span, const Sums* head,
                                          const Sums* carry) const {
     const Sums sum = sequence_sums<G>(off, s, span, head, carry);
     if (s >= off.count || threadIdx.x % G != 0) return;
@@ -512,7 +600,7 @@ struct PreferenceOut {
   // of results: pairs
   __device__ __forceinline__ int results(const Offsets& off) const { return off.count / 2; }
   template <int G>
-  __device__ __forceinline__ void finish(const Offsets& off, int i, int64_t span, const Sums* head,
+  __device__ __forceinline__ void finish(const Offsets& off, int i, int span, const Sums* head,
                                          const Sums* carry) const {
     double value[2];
     int tokens[2];
@@ -537,7 +625,7 @@ struct PreferenceOut {
 };
 
 template <int G, typename Out>
-__global__ __launch_bounds__(kThreads) void k_seq_join(Offsets off, int64_t span,
+__global__ __launch_bounds__(kThreads) void k_seq_join(Offsets off, int span,
                                                        const Sums* __restrict__ head,
                                                        const Sums* __restrict__ carry, Out out) {
   out.template finish<G>(off, blockIdx.x * (kThreads / G) + threadIdx.x / G, span, head, carry);
@@ -548,12 +636,12 @@ __global__ __launch_bounds__(kThreads) void k_seq_join(Offsets off, int64_t span
 constexpr int kSmallThreads = 1024, kSmallWaves = kSmallThreads / 64;
 constexpr int kSmallTokens = 16384, kSmallSequences = 1024;
 template <typename Terms, typename Out>
-__global__ __launch_bounds__(kSmallThreads) void k_seq_small(Terms w, Offsets off, int64_t span,
+__global__ __launch_bounds__(kSmallThreads) void k_seq_small(Terms w, Offsets off, int span,
                                                              Out out) {
   __shared__ int marks[kSmallWaves][kTile];
   __shared__ Sums head[kSmallSequences], carry[kSmallWaves];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  span_sums(w, off, span, static_cast<int64_t>(wave), threadIdx.x & 63, marks[wave], head, carry);
+  span_sums(w, off, span, wave, threadIdx.x & 63, marks[wave], head, carry);
   __syncthreads();
   constexpr int G = kSmallWaves;  // as many lanes as there can be spans
   for (int r0 = 0; r0 < out.results(off); r0 += blockDim.x / G)
@@ -566,33 +654,45 @@ struct PolicySlope {
   const int32_t* count;
   int mean;
   using Value = Two;  // the sequence's advantage, and its factor of a token's slope
-  __device__ __forceinline__ void load(int64_t i, int64_t n, Tokens& t) const { p.load(i, n, t); }
+  __device__ __forceinline__ const uint8_t* mask() const { return p.mask; }
+  template <bool WHOLE>
+  __device__ __forceinline__ void load(int i, int n, Tokens& t) const {
+    p.load<WHOLE>(i, n, t);
+  }
   __device__ __forceinline__ Value of(int s) const {
     Value v{p.per_token ? 0.0f : p.adv[s], dloss[s]};
     if (mean) v.b /= static_cast<float>(max(count[s], 1));
     return v;
   }
-  __device__ __forceinline__ float slope(const Tokens& t, int j, Value v) const {
-    const float at = p.per_token ? t.adv[j] : v.a;
-    const float d = t.old_nll[j] - t.nll[j];
-    float g = p.clipped(at, t.nll[j], t.old_nll[j], d) ? 0.0f : PolicyArgs::ratio(at, d);
+  __device__ __forceinline__ void slopes(const Tokens& t, int in, const Value (&v)[kPer],
+                                         float (&g)[kPer]) const {
+    float a[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) a[j] = p.per_token ? t.adv[j] : v[j].a;
+    const int cut = p.ratios(t, a, g);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) g[j] = ((cut >> j) & 1) != 0 ? 0.0f : g[j] * a[j];
     if (p.kl_weight != 0.0f) {
-      float em1, k;
-      exp_terms(t.nll[j] - t.ref[j], em1, k);
-      g = __builtin_fmaf(p.kl_weight, em1, g);
+      float em1[kPer], k[kPer];
+      p.kl(t, em1, k);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) g[j] = __builtin_fmaf(p.kl_weight, em1[j], g[j]);
     }
-    return p.mask == nullptr || t.mask[j] ? v.b * g : 0.0f;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) g[j] = ((in >> j) & 1) != 0 ? v[j].b * g[j] : 0.0f;
   }
 };
 
 struct PreferenceSlope {
   const float *margin, *dloss;
   const int32_t* count;
-  const uint8_t* mask;
+  const uint8_t* mask_p;
   PreferenceHow h;
   using Value = One;  // a token's slope
-  __device__ __forceinline__ void load(int64_t i, int64_t n, Tokens& t) const {
-    if (mask != nullptr) load_tokens(mask, i, n, t.mask);
+  __device__ __forceinline__ const uint8_t* mask() const { return mask_p; }
+  template <bool WHOLE>
+  __device__ __forceinline__ void load(int i, int n, Tokens& t) const {
+    if (mask_p != nullptr) load_values<WHOLE>(mask_p, i, n, t.mask);
   }
   __device__ __forceinline__ Value of(int s) const {
     const int i = s >> 1, mine = count[s], other = count[s ^ 1];
@@ -601,58 +701,43 @@ struct PreferenceSlope {
     const float v = (s & 1) != 0 ? g : -g;
     return {h.mean ? v / static_cast<float>(mine) : v};
   }
-  __device__ __forceinline__ float slope(const Tokens& t, int j, Value v) const {
-    return mask != nullptr && !t.mask[j] ? 0.0f : v.a;
+  __device__ __forceinline__ void slopes(const Tokens&, int in, const Value (&v)[kPer],
+                                         float (&g)[kPer]) const {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) g[j] = ((in >> j) & 1) != 0 ? v[j].a : 0.0f;
   }
 };
 
 // dnll of the tokens that are in a sequence.
 template <typename Slope>
-__global__ __launch_bounds__(kThreads) void k_seq_slopes(const Slope w, Offsets off, int64_t span,
+__global__ __launch_bounds__(kThreads) void k_seq_slopes(const Slope w, Offsets off, int span,
                                                          float* __restrict__ dnll) {
   __shared__ int marks[kWaves][kTile];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWaves + wave) * span;
-  const int64_t n = off.n, t1 = min(t0 + span, n);
+  const int t0 = (static_cast<int>(blockIdx.x) * kWaves + wave) * span;
+  const int n = off.n, t1 = min(t0 + span, n);
   if (t0 >= n) return;
-  Tokens tok, ahead;
-  w.load(t0 + lane * kPer, n, tok);
+  Tokens tok;
+  load_tile(w, t0, lane, n, tok);
   Walk<Slope> walk;
-  walk.find(off, w, static_cast<int>(t0), lane);
-  auto valid = [&](int s) { return s >= 0 && s < off.count; };
-  for (int64_t tile0 = t0; tile0 < t1; tile0 += kTile) {
-    const int64_t i = tile0 + lane * kPer;
-    if (tile0 + kTile < t1) w.load(i + kTile, n, ahead);
+  walk.find(off, w, t0, lane);
+  for (int tile0 = t0; tile0 < t1; tile0 += kTile) {
+    const int i = tile0 + lane * kPer;
     int start[kPer], s;
-    const bool any = walk.tile(off, w, static_cast<int>(tile0), lane, marks[wave], start, s);
+    const bool any = walk.tile(off, w, tile0, lane, marks[wave], start, s);
+    typename Slope::Value v[kPer];
     float g[kPer];
-    bool write[kPer], all = i + kPer <= n;
-    if (!any) {
-      const auto v = walk.of(off, w, s);
-      all &= valid(s);
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        write[j] = i + j < n && valid(s);
-        g[j] = w.slope(tok, j, v);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        s = max(s, start[j]);
-        write[j] = i + j < n && valid(s);
-        all &= write[j];
-        g[j] = w.slope(tok, j, walk.of(off, w, s));
-      }
-    }
-    if (all) {
+    const int inside = walk.values(off, w, any, s, start, v);
+    w.slopes(tok, inside & counting(tok, w.mask(), i, n), v, g);
+    if (tile0 + kTile < t1) load_tile(w, tile0 + kTile, lane, n, tok);
+    if (inside == 0xff && i + kPer <= n) {
       __builtin_memcpy(dnll + i, g, sizeof(g));
     } else {
 #pragma unroll
       for (int j = 0; j < kPer; ++j)
-        if (write[j]) dnll[i + j] = g[j];
+        if (((inside >> j) & 1) != 0 && i + j < n) dnll[i + j] = g[j];
     }
-    tok = ahead;
   }
 }
 
@@ -662,7 +747,9 @@ __global__ __launch_bounds__(kThreads) void k_seq_slopes(const Slope w, Offsets 
 constexpr int64_t kSpans = 8192;
 constexpr int64_t kMaxSequences = static_cast<int64_t>(1) << 24;
 
-int64_t span_of(int64_t n) { return (n + kSpans * kTile - 1) / (kSpans * kTile) * kTile; }
+int span_of(int64_t n) {
+  return static_cast<int>((n + kSpans * kTile - 1) / (kSpans * kTile)) * kTile;
+}
 int64_t spans_of(int64_t n) { return n == 0 ? 0 : (n + span_of(n) - 1) / span_of(n); }
 
 struct SeqWs {
@@ -751,7 +838,7 @@ void launch_sums(const Terms& w, const Offsets& off, int64_t results, Sums* head
                        w, off, span_of(off.n), head, carry);
   hipLaunchKernelGGL((k_seq_join<64, Out>),
                      dim3(static_cast<unsigned>((results + kWaves - 1) / kWaves)), dim3(kThreads),
-                     0, s, off, std::max<int64_t>(span_of(off.n), 1), head, carry, out);
+                     0, s, off, std::max(span_of(off.n), 1), head, carry, out);
 }
 template <typename Slope>
 void launch_slopes(const Slope& w, const Offsets& off, float* dnll, hipStream_t s) {
@@ -845,7 +932,7 @@ int preference_loss_forward(const float* nll, const float* ref_nll, const uint8_
   PreferenceTerms terms{};
   terms.nll = nll;
   terms.ref = ref_nll;
-  terms.mask = mask;
+  terms.mask_p = mask;
   launch_sums(terms, off, sequences / 2, head, carry,
               PreferenceOut{loss, margins, reward, count,
                             PreferenceHow{kind, mean != 0, beta, margin, smoothing}},
@@ -868,7 +955,7 @@ int preference_loss_backward(const uint8_t* mask, const int32_t* offsets, int64_
   slope.margin = margins;
   slope.dloss = dloss;
   slope.count = count;
-  slope.mask = mask;
+  slope.mask_p = mask;
   slope.h = PreferenceHow{kind, mean != 0, beta, 0.0f, smoothing};
   launch_slopes(slope, Offsets{offsets, static_cast<int>(sequences), static_cast<int>(n)}, dnll,
                 stream);

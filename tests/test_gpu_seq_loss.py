@@ -4,10 +4,10 @@ Bounds, with U = 2^-24 (half a step of fp32).  A term's ratio r = exp(d) is off
 by d's rounding, U |d|, and exp's 2^-22, relative to itself, and two roundings
 of r A; k = e^x - 1 - x and e^x - 1 by x's rounding, U |x| e^x, 8 U of
 themselves below |x| = 1/2, and 2^-22 e^x + 2 U of themselves above.  The
-policy loss's terms round twice more and are added in fp32 in eights, pairwise
-(three additions, each off by U of the sum of what it adds), and those in fp64,
-so a sequence's value is off by its terms' errors, 5 U of the sum of their
-sizes and one rounding of the result; the preference loss's terms are exact but for fp64's
+policy loss's terms round twice more and are added in fp32 by eights, in at most
+seven additions (each off by U of what it adds up), and those in fp64, so a
+sequence's value is off by its terms' errors, 9 U of the sum of their sizes
+and one rounding of the result; the preference loss's terms are exact but for fp64's
 roundings, and its results are rounded once (x before f' in the backward, where
 it is off by U |x|, f' by 2^-21 and 4 roundings)."""
 
@@ -135,8 +135,8 @@ def _policy_ref(off, n, nll, old, ref, mask, adv, per_token, lo, hi, w, mean, dl
     part = 1.0 / count.clamp(min=1) if mean else torch.ones_like(count)
     c64 = counts.double()
     loss, kl = _by(token * c64, s, seqs) * part, _by(k * c64, s, seqs) * part
-    loss_err = _by((err + 5 * U * (token.abs() + abs(w) * k)) * c64, s, seqs) * part + U * loss.abs()
-    kl_err = _by((k_err + 3 * U * k) * c64, s, seqs) * part + U * kl
+    loss_err = _by((err + 9 * U * (token.abs() + abs(w) * k)) * c64, s, seqs) * part + U * loss.abs()
+    kl_err = _by((k_err + 7 * U * k) * c64, s, seqs) * part + U * kl
     clipped = _by(cut.double(), s, seqs)
     out = dict(loss=loss, loss_err=1.01 * loss_err + 1e-37, kl=kl, kl_err=1.01 * kl_err + 1e-37,
                count=count.int(), clipped=clipped.int(), inside=inside)
