@@ -1177,79 +1177,80 @@ def sequence_loss_workspace_size(n: int, sequences: int) -> int:
 
 def _flat(device: int, specs, outputs: int = 0):
     """The addresses (None for None) of contiguous tensors of GPU ``device``,
-    given as (name, tensor, elements, dtype), after all of them have been
-    checked; the first ``outputs`` of them share memory with no other.  (One
-    pass without a call per check: most of a small call's time is the
+    given as (name, tensor, elements, dtype), of which the first ``outputs``
+    share memory with no other.  dtype None: bool or uint8.  (One pass without a
+    call per check: most of the time of a call on few tokens is the
     binding's.)"""
+    at = []
     for name, t, n, dtype in specs:
-        if t is not None and (t.dtype is not dtype or t.numel() != n or t.get_device() != device
-                              or not t.is_contiguous()):
-            _buf(t, name)
-            if t.dtype is not dtype:
-                raise MuonError(MUON_ERR_BAD_DTYPE, f"{name} has dtype {t.dtype}, not {dtype}")
-            if t.numel() != n:
-                raise MuonError(MUON_ERR_BAD_SHAPE,
-                                f"{name} has {t.numel()} elements, expected {n}")
-            raise MuonError(MUON_ERR_INVALID_ARG, f"{name} is on {t.device}, others on {device}")
-    at = [None if s[1] is None else s[1].data_ptr() for s in specs]
+        if t is None:
+            at.append(None)
+        elif (t.dtype is dtype and t.numel() == n and t.get_device() == device
+              and t.is_contiguous()):
+            at.append(t.data_ptr())
+        else:
+            at.append(_flat_slow(device, name, t, n, dtype))
     for i in range(outputs):
         lo = at[i]
         if lo:
-            name, _, n, dtype = specs[i]
-            hi = lo + n * dtype.itemsize
+            name, t, n, _ = specs[i]
+            hi = lo + n * t.element_size()
             for j in range(i + 1, len(at)):
                 b = at[j]
-                if b and b < hi and lo < b + specs[j][2] * specs[j][3].itemsize:
+                if b and b < hi and (lo <= b or lo < b + specs[j][2] * specs[j][1].element_size()):
                     raise MuonError(MUON_ERR_INVALID_ARG,
                                     f"{name} shares memory with {specs[j][0]}")
     return at
 
 
-def _scratch(workspace):
-    """The caller's workspace as _flat takes it."""
-    if workspace is None:
-        return "workspace", None, 0, None
-    _buf(workspace, "workspace")
-    return "workspace", workspace, workspace.numel(), workspace.dtype
-
-
-def _mask_dtype(mask):
-    if mask is None:
-        return None
+def _flat_slow(device: int, name: str, t, n: int, dtype):
+    """The address of a mask, or what is wrong with a tensor."""
     import torch
-    if mask.dtype not in (torch.bool, torch.uint8):
-        raise MuonError(MUON_ERR_BAD_DTYPE, f"mask must be bool or uint8, has {mask.dtype}")
-    return mask.dtype
+    _buf(t, name)
+    if t.dtype is not dtype and (dtype is not None or t.dtype not in (torch.bool, torch.uint8)):
+        raise MuonError(MUON_ERR_BAD_DTYPE,
+                        f"{name} has dtype {t.dtype}, not {dtype or 'bool or uint8'}")
+    if t.numel() != n:
+        raise MuonError(MUON_ERR_BAD_SHAPE, f"{name} has {t.numel()} elements, expected {n}")
+    if t.get_device() != device:
+        raise MuonError(MUON_ERR_INVALID_ARG, f"{name} is on {t.device}, others on GPU {device}")
+    return t.data_ptr()
 
 
-def _tokens(nll, offsets):
-    """Number of tokens, of sequences, and the GPU's index."""
+class _Here:
+    """Stands for a _Launch where a call's GPU and stream are the current ones."""
+    handle = None
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        pass
+
+
+_HERE = _Here()
+
+
+def _on(device: int, stream):
+    import torch
+    if stream is None and torch.cuda.current_device() == device:
+        return _HERE
+    return _Launch(torch.device("cuda", device), stream)
+
+
+def _packed(nll, offsets, name: str = "nll"):
+    """GPU index, number of tokens and of sequences."""
     if nll is None or not nll.is_cuda:
-        raise MuonError(MUON_ERR_INVALID_ARG, "nll must be a GPU tensor")
-    return nll.numel(), _sequences(offsets), nll.get_device()
-
-
-def _sequences(offsets) -> int:
+        raise MuonError(MUON_ERR_INVALID_ARG, f"{name} must be a GPU tensor")
     if offsets is None or offsets.numel() < 1:
         raise MuonError(MUON_ERR_BAD_SHAPE, "offsets must have sequences + 1 elements")
-    return offsets.numel() - 1
+    return nll.get_device(), nll.numel(), offsets.numel() - 1
 
 
-def _policy_inputs(nll, old_nll, advantages, offsets, ref_nll, mask, kl_weight, per_token):
-    """What _tokens says, and the inputs that forward and backward share as
-    _flat takes them."""
-    import torch
-    f32 = torch.float32
-    n, sequences, device = _tokens(nll, offsets)
-    if old_nll is None or advantages is None:
-        raise MuonError(MUON_ERR_INVALID_ARG, "old_nll or advantages is None")
-    if ref_nll is None and kl_weight:
-        raise MuonError(MUON_ERR_INVALID_ARG, "kl_weight needs ref_nll")
-    return n, sequences, device, (("nll", nll, n, f32), ("old_nll", old_nll, n, f32),
-                                  ("ref_nll", ref_nll, n, f32),
-                                  ("mask", mask, n, _mask_dtype(mask)),
-                                  ("advantages", advantages, n if per_token else sequences, f32),
-                                  ("offsets", offsets, sequences + 1, torch.int32))
+def _some(**tensors):
+    for name, t in tensors.items():
+        if t is None:
+            raise MuonError(MUON_ERR_INVALID_ARG, f"{name} is None")
 
 
 def policy_loss_forward(nll, old_nll, advantages, offsets, ref_nll=None, mask=None,
@@ -1269,13 +1270,21 @@ def policy_loss_forward(nll, old_nll, advantages, offsets, ref_nll=None, mask=No
     sequence: fp32, the mean or sum of k (0 without ref_nll), int32 numbers
     of tokens that count and of those that the clip holds."""
     import torch
-    n, sequences, device, ins = _policy_inputs(nll, old_nll, advantages, offsets, ref_nll, mask,
-                                               kl_weight, per_token)
     f32, i32 = torch.float32, torch.int32
-    at = _flat(device, (("loss", loss, sequences, f32), ("kl", kl, sequences, f32),
-                        ("count", count, sequences, i32), ("clipped", clipped, sequences, i32),
-                        _scratch(workspace), *ins), 5)
-    with _Launch(nll.device, stream) as on:
+    device, n, sequences = _packed(nll, offsets)
+    if old_nll is None or advantages is None:
+        _some(old_nll=old_nll, advantages=advantages)
+    if ref_nll is None and kl_weight:
+        raise MuonError(MUON_ERR_INVALID_ARG, "kl_weight needs ref_nll")
+    at = _flat(device, (
+        ("loss", loss, sequences, f32), ("kl", kl, sequences, f32),
+        ("count", count, sequences, i32), ("clipped", clipped, sequences, i32),
+        ("workspace", workspace, *((0, None) if workspace is None else
+                                   (workspace.numel(), workspace.dtype))),
+        ("nll", nll, n, f32), ("old_nll", old_nll, n, f32), ("ref_nll", ref_nll, n, f32),
+        ("mask", mask, n, None), ("advantages", advantages, n if per_token else sequences, f32),
+        ("offsets", offsets, sequences + 1, i32)), 5)
+    with _on(device, stream) as on:
         if loss is None:
             loss = nll.new_empty(sequences)
         if kl is None:
@@ -1290,7 +1299,7 @@ def policy_loss_forward(nll, old_nll, advantages, offsets, ref_nll=None, mask=No
             at[5], at[6], at[7], at[8], at[9], 1 if per_token else 0, at[10], sequences, n,
             clip_low, clip_high, kl_weight, 1 if mean else 0, loss.data_ptr(), kl.data_ptr(),
             count.data_ptr(), clipped.data_ptr(), workspace.data_ptr(), _nbytes(workspace),
-            on.handle))
+            on.handle or _current_handle(nll.device)))
     return loss, kl, count, clipped
 
 
@@ -1303,20 +1312,25 @@ def policy_loss_backward(nll, old_nll, advantages, offsets, count, dloss, ref_nl
     to no sequence are left as they were.  Without it a tensor is allocated,
     with zeros there.  Returns dnll."""
     import torch
-    n, sequences, device, ins = _policy_inputs(nll, old_nll, advantages, offsets, ref_nll, mask,
-                                               kl_weight, per_token)
-    if count is None or dloss is None:
-        raise MuonError(MUON_ERR_INVALID_ARG, "count or dloss is None")
-    f32 = torch.float32
-    at = _flat(device, (("dnll", dnll, n, f32), *ins, ("count", count, sequences, torch.int32),
-                        ("dloss", dloss, sequences, f32)), 1)
-    with _Launch(nll.device, stream) as on:
+    f32, i32 = torch.float32, torch.int32
+    device, n, sequences = _packed(nll, offsets)
+    if old_nll is None or advantages is None or count is None or dloss is None:
+        _some(old_nll=old_nll, advantages=advantages, count=count, dloss=dloss)
+    if ref_nll is None and kl_weight:
+        raise MuonError(MUON_ERR_INVALID_ARG, "kl_weight needs ref_nll")
+    at = _flat(device, (
+        ("dnll", dnll, n, f32), ("nll", nll, n, f32), ("old_nll", old_nll, n, f32),
+        ("ref_nll", ref_nll, n, f32), ("mask", mask, n, None),
+        ("advantages", advantages, n if per_token else sequences, f32),
+        ("offsets", offsets, sequences + 1, i32), ("count", count, sequences, i32),
+        ("dloss", dloss, sequences, f32)), 1)
+    with _on(device, stream) as on:
         if dnll is None:
             dnll = torch.zeros(nll.shape, dtype=f32, device=nll.device)
         _check(lib().policy_loss_backward(
             at[1], at[2], at[3], at[4], at[5], 1 if per_token else 0, at[6], sequences, n,
             clip_low, clip_high, kl_weight, 1 if mean else 0, at[7], at[8], dnll.data_ptr(),
-            on.handle))
+            on.handle or _current_handle(nll.device)))
     return dnll
 
 
@@ -1343,17 +1357,19 @@ def preference_loss_forward(nll, offsets, ref_nll=None, mask=None, beta: float =
     reward, count): fp32 of pairs (margins: the x), fp32 and int32 of
     sequences."""
     import torch
-    n, sequences, device = _tokens(nll, offsets)
+    f32, i32 = torch.float32, torch.int32
+    device, n, sequences = _packed(nll, offsets)
     if sequences % 2:
         raise MuonError(MUON_ERR_BAD_SHAPE, f"{sequences} sequences: two to a pair")
     code, pairs = _preference_kind(kind), sequences // 2
-    f32, i32 = torch.float32, torch.int32
-    at = _flat(device, (("loss", loss, pairs, f32), ("margins", margins, pairs, f32),
-                        ("reward", reward, sequences, f32), ("count", count, sequences, i32),
-                        _scratch(workspace), ("nll", nll, n, f32), ("ref_nll", ref_nll, n, f32),
-                        ("mask", mask, n, _mask_dtype(mask)),
-                        ("offsets", offsets, sequences + 1, i32)), 5)
-    with _Launch(nll.device, stream) as on:
+    at = _flat(device, (
+        ("loss", loss, pairs, f32), ("margins", margins, pairs, f32),
+        ("reward", reward, sequences, f32), ("count", count, sequences, i32),
+        ("workspace", workspace, *((0, None) if workspace is None else
+                                   (workspace.numel(), workspace.dtype))),
+        ("nll", nll, n, f32), ("ref_nll", ref_nll, n, f32), ("mask", mask, n, None),
+        ("offsets", offsets, sequences + 1, i32)), 5)
+    with _on(device, stream) as on:
         if loss is None:
             loss = nll.new_empty(pairs)
         if margins is None:
@@ -1367,7 +1383,8 @@ def preference_loss_forward(nll, offsets, ref_nll=None, mask=None, beta: float =
         _check(lib().preference_loss_forward(
             at[5], at[6], at[7], at[8], sequences, n, code, beta, margin, smoothing,
             1 if mean else 0, loss.data_ptr(), margins.data_ptr(), reward.data_ptr(),
-            count.data_ptr(), workspace.data_ptr(), _nbytes(workspace), on.handle))
+            count.data_ptr(), workspace.data_ptr(), _nbytes(workspace),
+            on.handle or _current_handle(nll.device)))
     return loss, margins, reward, count
 
 
@@ -1379,34 +1396,31 @@ def preference_loss_backward(offsets, margins, count, dloss, n=None, mask=None, 
     a pair.  dnll as for policy_loss_backward; without it, ``n`` (the mask's
     size by default) is the number of tokens.  Returns dnll."""
     import torch
-    sequences = _sequences(offsets)
+    f32, i32 = torch.float32, torch.int32
+    device, _, sequences = _packed(offsets, offsets, "offsets")
     if sequences % 2:
         raise MuonError(MUON_ERR_BAD_SHAPE, f"{sequences} sequences: two to a pair")
-    code = _preference_kind(kind)
-    for t in (dnll, mask):
-        if n is None and t is not None:
-            n = t.numel()
-    if n is None:
-        raise MuonError(MUON_ERR_INVALID_ARG, "n, mask or dnll must say how many tokens there are")
-    n = int(n)
+    code, pairs = _preference_kind(kind), sequences // 2
     if margins is None or count is None or dloss is None:
-        raise MuonError(MUON_ERR_INVALID_ARG, "margins, count or dloss is None")
-    if not offsets.is_cuda:
-        raise MuonError(MUON_ERR_INVALID_ARG, "offsets must be a GPU tensor")
-    dev, f32 = offsets.device, torch.float32
-    at = _flat(offsets.get_device(), (("dnll", dnll, n, f32), ("mask", mask, n, _mask_dtype(mask)),
-                                      ("offsets", offsets, sequences + 1, torch.int32),
-                                      ("margins", margins, sequences // 2, f32),
-                                      ("count", count, sequences, torch.int32),
-                                      ("dloss", dloss, sequences // 2, f32)), 1)
-    with _Launch(dev, stream) as on:
+        _some(margins=margins, count=count, dloss=dloss)
+    if n is None:
+        given = mask if dnll is None else dnll
+        if given is None:
+            raise MuonError(MUON_ERR_INVALID_ARG,
+                            "n, mask or dnll must say how many tokens there are")
+        n = given.numel()
+    at = _flat(device, (
+        ("dnll", dnll, n, f32), ("mask", mask, n, None), ("offsets", offsets, sequences + 1, i32),
+        ("margins", margins, pairs, f32), ("count", count, sequences, i32),
+        ("dloss", dloss, pairs, f32)), 1)
+    with _on(device, stream) as on:
         if dnll is None:
             if not 0 <= n < 1 << 26:
                 raise MuonError(MUON_ERR_BAD_SHAPE, "n must be in [0, 2^26)")
-            dnll = torch.zeros(n, dtype=f32, device=dev)
+            dnll = torch.zeros(n, dtype=f32, device=offsets.device)
         _check(lib().preference_loss_backward(
             at[1], at[2], sequences, n, code, beta, smoothing, 1 if mean else 0, at[3], at[4],
-            at[5], dnll.data_ptr(), on.handle))
+            at[5], dnll.data_ptr(), on.handle or _current_handle(offsets.device)))
     return dnll
 
 

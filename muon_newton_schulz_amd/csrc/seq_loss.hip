@@ -534,7 +534,7 @@ __global__ __launch_bounds__(kThreads) void k_seq_sums(Terms w, Offsets off, int
 }
 
 // A sequence's sums: its part in the span where it starts and the carries of
-// the spans behind, G lanes.
+// the spans behind, G lanes (256: a workgroup).  The first lane has them.
 template <int G>
 __device__ __forceinline__ Sums sequence_sums(const Offsets& off, int s, int span,
                                               const Sums* head, const Sums* carry) {
@@ -545,10 +545,20 @@ __device__ __forceinline__ Sums sequence_sums(const Offsets& off, int s, int spa
     if (lo < hi) {
       if (l == 0) sum = head[s];
       const int last = (hi - 1) / span;
+#pragma unroll 4
       for (int k = lo / span + 1 + l; k <= last; k += G) sum.add(carry[k]);
     }
   }
-  sum.template join<G>();
+  sum.template join<(G < 64 ? G : 64)>();
+  if constexpr (G > 64) {
+    __shared__ Sums red[G / 64];
+    __syncthreads();  // (a second sequence's: the first's are read)
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
+    __syncthreads();
+    sum = red[0];
+#pragma unroll
+    for (int k = 1; k < G / 64; ++k) sum.add(red[k]);
+  }
   return sum;
 }
 
@@ -743,8 +753,13 @@ __global__ __launch_bounds__(kThreads) void k_seq_slopes(const Slope w, Offsets 
 
 // -------------------------------------------------------------------- host
 
-// Waves of a launch: eight to a SIMD.
-constexpr int64_t kSpans = 8192;
+// Most waves of a launch.  Spans of a few tiles: fewer, longer ones leave
+// loads waiting, single tiles pay for the search and the carry each time
+// (policy step of 33.5 M tokens and preference step of 16.8 M, us: 8192 spans
+// 227 and 62, 16384 217 and 63, 24576 214 and 63, 32768 213 and 68, 65536 227
+// and 68).
+constexpr int64_t kSpans = 24576;
+constexpr int64_t kFewResults = 512;
 constexpr int64_t kMaxSequences = static_cast<int64_t>(1) << 24;
 
 int span_of(int64_t n) {
@@ -836,9 +851,16 @@ void launch_sums(const Terms& w, const Offsets& off, int64_t results, Sums* head
   if (blocks > 0)
     hipLaunchKernelGGL(k_seq_sums<Terms>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, s,
                        w, off, span_of(off.n), head, carry);
-  hipLaunchKernelGGL((k_seq_join<64, Out>),
-                     dim3(static_cast<unsigned>((results + kWaves - 1) / kWaves)), dim3(kThreads),
-                     0, s, off, std::max(span_of(off.n), 1), head, carry, out);
+  // a wave a result, or a workgroup where there are few, whose sequences can
+  // have thousands of carries
+  const int span = std::max(span_of(off.n), 1);
+  if (results <= kFewResults)
+    hipLaunchKernelGGL((k_seq_join<kThreads, Out>), dim3(static_cast<unsigned>(results)),
+                       dim3(kThreads), 0, s, off, span, head, carry, out);
+  else
+    hipLaunchKernelGGL((k_seq_join<64, Out>),
+                       dim3(static_cast<unsigned>((results + kWaves - 1) / kWaves)), dim3(kThreads),
+                       0, s, off, span, head, carry, out);
 }
 template <typename Slope>
 void launch_slopes(const Slope& w, const Offsets& off, float* dnll, hipStream_t s) {
