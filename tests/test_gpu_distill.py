@@ -180,6 +180,9 @@ def test_loss_and_gradients(gpu, n, vocab, dim, top, dt, zt, T, hd, wd, off, pad
 # one for each tile core of the statistics: Thin, Medium, Half, Large; any
 # operands bf16 and fp32, 64 and 128 (test_tile_core_coverage.py's sizes)
 @pytest.mark.parametrize("n,vocab,dim,top,dt,off", [
+    (128, 2000, 1032, 64, "bf16", 0), (128, 20011, 264, 65, "bf16", 0),
+    (129, 20011, 264, 64, "bf16", 0), (100, 8000, 1541, 33, "bf16", 1),
+    (128, 8000, 1541, 64, "fp32", 0), (40, 300, 261, 50, "fp32", 0),
     (130, 2000, 1032, 20, "bf16", 0), (40, 20011, 264, 64, "bf16", 0),
     (600, 20011, 520, 70, "bf16", 0), (4000, 4000, 840, 33, "bf16", 0),
     (8200, 20011, 1032, 16, "bf16", 0), (130, 8000, 1541, 40, "bf16", 1),
