@@ -1242,7 +1242,9 @@ def _packed(nll, offsets, name: str = "nll"):
     """GPU index, number of tokens and of sequences."""
     if nll is None or not nll.is_cuda:
         raise MuonError(MUON_ERR_INVALID_ARG, f"{name} must be a GPU tensor")
-    if offsets is None or offsets.numel() < 1:
+    if offsets is None:
+        raise MuonError(MUON_ERR_INVALID_ARG, "offsets is None")
+    if offsets.numel() < 1:
         raise MuonError(MUON_ERR_BAD_SHAPE, "offsets must have sequences + 1 elements")
     return nll.get_device(), nll.numel(), offsets.numel() - 1
 
