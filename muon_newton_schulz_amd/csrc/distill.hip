@@ -26,14 +26,14 @@
 #include <algorithm>
 #include <cmath>
 
-#include "lm_loss.h"
+#include "lm_loss_kernels.h"
 
 namespace muon {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr uint32_t kNoKey = ~0u;
 constexpr int kMaxTop = 1 << kPlaceBits;
+constexpr int kMostSplits = 64;
 
 // The teacher's lists, [n][top] with row strides.
 struct Lists {
@@ -80,12 +80,21 @@ __device__ __forceinline__ void teacher_stats(const float (&z)[E], float scale, 
   log_sum = logf(s);
 }
 
+// For the backward: of row t the first listed column or -1, the largest z and
+// log sum, and (rows not null) hidden, zeros for a row without a list.
+struct Marks {
+  int32_t* column;
+  f32x2_t* stats;
+  const char* hidden;
+  char* rows;
+  int64_t stride, bytes;  // of a row
+};
+
 // One wave a row: keys [n][top] in ascending order (a bitonic network over
-// 64 E keys, element lane E + e in register e).  For the backward also
-// marks[t], the first column or -1, and stats[t] = (largest z, log sum).
+// 64 E keys, element lane E + e in register e), and what marks asks for.
 template <int E>
 __global__ __launch_bounds__(kThreads) void k_distill_sort(Lists a, int64_t n, uint32_t* keys,
-                                                           int32_t* marks, f32x2_t* stats) {
+                                                           Marks marks) {
   const int lane = threadIdx.x & 63;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / 64) + (threadIdx.x >> 6);
   if (t >= n) return;
@@ -102,10 +111,10 @@ __global__ __launch_bounds__(kThreads) void k_distill_sort(Lists a, int64_t n, u
       if (x[e] != kNoKey) z[e] = zk;
     }
   }
-  if (stats != nullptr) {
+  if (marks.column != nullptr) {
     float top, log_sum;
     teacher_stats<E>(z, a.scale, top, log_sum);
-    if (lane == 0) stats[t] = f32x2_t{top, log_sum};
+    if (lane == 0) marks.stats[t] = f32x2_t{top, log_sum};
   }
 #pragma unroll
   for (int k = 2; k <= 64 * E; k <<= 1) {
@@ -136,8 +145,25 @@ __global__ __launch_bounds__(kThreads) void k_distill_sort(Lists a, int64_t n, u
     const int i = lane * E + e;
     if (i < a.top) keys[t * a.top + i] = x[e];
   }
-  if (marks != nullptr && lane == 0)
-    marks[t] = x[0] == kNoKey ? -1 : static_cast<int32_t>(x[0] >> kPlaceBits);
+  if (marks.column == nullptr) return;
+  const bool listed = __builtin_amdgcn_readfirstlane(x[0]) != kNoKey;
+  if (lane == 0) marks.column[t] = listed ? static_cast<int32_t>(x[0] >> kPlaceBits) : -1;
+  if (marks.rows == nullptr) return;
+  const char* from = marks.hidden + t * marks.stride;
+  char* to = marks.rows + t * marks.bytes;
+  for (int64_t i = lane * 16; i < marks.bytes; i += 64 * 16) {
+    if (i + 16 <= marks.bytes) {
+      u32x4_t v = {0, 0, 0, 0};
+      if (listed) __builtin_memcpy(&v, from + i, 16);
+      __builtin_memcpy(to + i, &v, 16);
+    } else {  // elements of two bytes or four
+      for (int64_t k = i; k < marks.bytes; k += 2) {
+        uint16_t v = 0;
+        if (listed) __builtin_memcpy(&v, from + k, 2);
+        __builtin_memcpy(to + k, &v, 2);
+      }
+    }
+  }
 }
 
 // Joins a row's tiles (R rows a workgroup) and turns its listed logits into
@@ -261,12 +287,11 @@ void for_list(int top, F&& f) {
   else f(std::integral_constant<int, 16>{});
 }
 
-void sort_lists(const Lists& a, int64_t n, uint32_t* keys, int32_t* marks, f32x2_t* stats,
-                hipStream_t s) {
+void sort_lists(const Lists& a, int64_t n, uint32_t* keys, const Marks& marks, hipStream_t s) {
   const unsigned blocks = static_cast<unsigned>((n + 3) / 4);
   for_list(a.top, [&](auto e) {
     hipLaunchKernelGGL(k_distill_sort<decltype(e)::value>, dim3(blocks), dim3(kThreads), 0, s, a,
-                       n, keys, marks, stats);
+                       n, keys, marks);
   });
 }
 
@@ -283,6 +308,37 @@ void store_points(const void* context, void* g, int64_t ldg, const float* c, int
                        static_cast<uint16_t*>(g), ldg, c, v0, len);
 }
 
+// Shares of dh's sum, which each piece of g takes: the least estimated time of
+// the products (their tile core as run_dh picks it) and of the fp32 sums that
+// the shares are added up in, at 2.5 TB/s, once more than there are pieces.
+// (The step, us, with the cross entropy's rule, as many shares as fill the GPU
+// with 128 x 128 tiles, 16 at most, and with this one: 930 x 13715 x 5376 987 and
+// 833, 2048 x 32000 x 2048 1532 and 1440, 62 x 60045 x 416 104 and 94, 122 x 55297
+// x 960 180 and 158.)
+int pick_splits(int64_t n, int64_t dim, int64_t piece, int64_t pieces, int32_t dtype) {
+  const bool half = dtype == MUON_DTYPE_BF16;
+  int best = 1;
+  double least = 0.0;
+  for (int s = 1; s <= kMostSplits && (s == 1 || piece / s >= 512); ++s) {
+    const int64_t k = (half ? 2 : 1) * ceil_div(piece, s);
+    auto time = [&](const auto& table) {
+      double t = 0.0;
+      for (const ShapeCost& c : table) {
+        const double e = shape_time(c, dh_tiles(n, s)(c.bm), dim, k);
+        if (t == 0.0 || e < t) t = e;
+      }
+      return t;
+    };
+    double t = half && dim % 8 == 0 ? time(kShapeNN) : half ? time(kShapeAnyBf16) : time(kShapeAnyFp32);
+    if (s > 1) t += 8.0 * static_cast<double>(n * dim) * s / 2.5e6 * (1.0 + 1.0 / pieces) + 4.0 / pieces;
+    if (s == 1 || t < least) {
+      best = s;
+      least = t;
+    }
+  }
+  return best;
+}
+
 // The cross entropy's workspace and, behind it, the lists'.
 struct DistillWs {
   LossWs loss;
@@ -292,6 +348,15 @@ DistillWs distill_ws(int64_t n, int64_t vocab, int64_t dim, int64_t top, int32_t
                      bool backward) {
   DistillWs w{};
   w.loss = loss_ws(n, vocab, dim, dtype, backward);
+  if (backward) {
+    const int64_t pieces = ceil_div(vocab, w.loss.piece);
+    w.loss.splits = pick_splits(n, dim, w.loss.piece, pieces, dtype);
+    // (dh's fp32 sums stand last)
+    size_t o = w.loss.part;
+    if (w.loss.splits > 1 || pieces > 1)
+      o += align256(static_cast<size_t>(w.loss.splits) * static_cast<size_t>(n * dim) * 4);
+    w.loss.total = std::max(o, loss_ws(n, vocab, dim, dtype, false).total);
+  }
   const int64_t rows = backward ? n : w.loss.stats_rows;
   size_t o = align256(w.loss.total);
   w.keys = o;
@@ -372,7 +437,7 @@ int distill_loss_forward(const void* hidden, int64_t ld_hidden, const void* weig
         lists_of(static_cast<const char*>(ids) + static_cast<size_t>(r0 * ld_ids) * isz, ids_64,
                  ld_ids, static_cast<const char*>(teacher) + static_cast<size_t>(r0 * ld_teacher) * zsz,
                  teacher_dtype, ld_teacher, vocab, top, temperature);
-    sort_lists(lists, rows, keys, nullptr, nullptr, stream);
+    sort_lists(lists, rows, keys, Marks{}, stream);
     StatsArgs a{};
     a.h = static_cast<const char*>(hidden) + static_cast<size_t>(r0 * ld_hidden) * sz;
     a.w = weight;
@@ -386,7 +451,7 @@ int distill_loss_forward(const void* hidden, int64_t ld_hidden, const void* weig
     a.dim = static_cast<int>(dim);
     a.top = static_cast<int>(top);
     a.scale = lists.scale;
-    const int tiles = loss_stats(a, dtype, stream);
+    const int tiles = loss_stats<true>(a, dtype, stream);
     const int per = join_rows(rows);
     for_list(a.top, [&](auto e) {
       auto* kernel = per == 4 ? k_distill_join<4, decltype(e)::value>
@@ -431,9 +496,13 @@ int distill_loss_backward(const void* hidden, int64_t ld_hidden, const void* wei
   uint32_t* keys = reinterpret_cast<uint32_t*>(ws + w.keys);
   int32_t* marks = reinterpret_cast<int32_t*>(ws + w.marks);
   f32x2_t* stats = reinterpret_cast<f32x2_t*>(ws + w.stats);
+  const int64_t sz = static_cast<int64_t>(train_dtype_size(dtype));
   const Lists lists = lists_of(ids, ids_64, ld_ids, teacher, teacher_dtype, ld_teacher, vocab, top,
                                temperature);
-  sort_lists(lists, n, keys, marks, stats, stream);
+  sort_lists(lists, n, keys,
+             Marks{marks, stats, static_cast<const char*>(hidden),
+                   dweight != nullptr ? ws + w.loss.rows : nullptr, ld_hidden * sz, dim * sz},
+             stream);
   const PointArgs points{lists, keys, stats, logp, dloss, n, dtype == MUON_DTYPE_FP32};
   BackwardArgs b{};
   b.h = hidden;
@@ -453,7 +522,7 @@ int distill_loss_backward(const void* hidden, int64_t ld_hidden, const void* wei
   b.scale = lists.scale;
   b.after_g = store_points;
   b.context = &points;
-  loss_backward(b, w.loss, dtype, dhidden_dtype, dweight_dtype, stream);
+  loss_backward<true>(b, w.loss, dtype, dhidden_dtype, dweight_dtype, stream);
   return check_launch("distillation loss gradient launch");
 }
 

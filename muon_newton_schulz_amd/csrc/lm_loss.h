@@ -1,6 +1,6 @@
-// What losses of a linear head over a large vocabulary share: the cross
+// What losses of a linear head over a large vocabulary share, the cross
 // entropy (lm_loss.hip, which defines the functions) and the distillation loss
-// (distill.hip).
+// (distill.hip), besides their kernels (lm_loss_kernels.h).
 #pragma once
 
 #include "train_common.h"
@@ -96,14 +96,12 @@ struct StatsArgs {
   int n, dim, t64, top;
   float scale;           // of the logits, > 0
 };
-// Row statistics of scale * h W^T, and what targets or keys name.  Returns the
-// number of tiles along the vocabulary.
-int loss_stats(const StatsArgs& a, int32_t dtype, hipStream_t s);
 
 // Gradients with g = (exp(scale l - lse) - [v = target]) dloss scale.  after_g
 // is called when a piece's g / (scale c) is stored ([n][ldg], columns
 // [v0, v0 + len); bf16: a low plane, then a high plane), to put other values
-// into it.
+// into it.  The distillation loss has put hidden, with zeros in the rows
+// without a target, into the workspace already.
 struct BackwardArgs {
   const void *h, *w, *targets;
   const float *lse, *dloss;
@@ -116,8 +114,6 @@ struct BackwardArgs {
                   hipStream_t s);
   const void* context;
 };
-void loss_backward(const BackwardArgs& b, const LossWs& w, int32_t dtype, int32_t dh_dtype,
-                   int32_t dw_dtype, hipStream_t s);
 // dw (+)= nothing, for calls without rows
 int loss_no_rows(void* dw, int32_t dw_dtype, int64_t vocab, int64_t dim, int accumulate,
                  hipStream_t s);

@@ -695,9 +695,12 @@ struct DmaCore {
 
   static constexpr int DPS = NP + NQ;  // a wave's DMA instructions per stage
 
-  template <bool ADD = false>
+  // PLANES = 2: the sum runs over P's two planes, `plane` elements apart, in
+  // turns, a stage of each against the same stage of Q.
+  template <bool ADD = false, int PLANES = 1>
   static __device__ __forceinline__ void run(const TileArgs<uint16_t>& w,
-                                             f32x16_t (&acc)[NJ][MI]) {
+                                             f32x16_t (&acc)[NJ][MI], int64_t plane = 0) {
+    static_assert(PLANES == 1 || PLANES == 2, "");
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int ri = (wave % WM) * 32 * MI, rj = (wave / WM) * 32 * NJ;
@@ -709,17 +712,22 @@ struct DmaCore {
     qo.init(w.Q, w.ldq, w.qn, wave, lane);
     // stage 0 is the sum's ragged end, if it has one; the others are whole,
     // and stage kt starts at k = (kt + shift) BK
-    const int kleft = w.K % BK, nk = w.K / BK + (kleft != 0);
+    const int kleft = w.K % BK, nk = (w.K / BK + (kleft != 0)) * PLANES;
     const int shift = kleft != 0 ? -1 : 0;
+    // P's first byte, and the stage of k, of stage kt
+    auto first = [&](int kt) {
+      return PLANES == 2 && (kt & 1) != 0 ? po.base + 2 * plane : po.base;
+    };
+    auto of_k = [](int kt) { return PLANES == 2 ? kt >> 1 : kt; };
 
     // DMA instruction D (P's first) of a whole stage
     auto issue1 = [&](int kt, auto slot_c, auto d_c) {
       char* tile = slot<decltype(slot_c)::value>();
       constexpr int d = decltype(d_c)::value;
       if constexpr (d < NP)
-        dma16(po.base + (kt + shift) * po.step, po.off[d], tile + (wave * NP + d) * 1024);
+        dma16(first(kt) + (of_k(kt) + shift) * po.step, po.off[d], tile + (wave * NP + d) * 1024);
       else
-        dma16(qo.base + (kt + shift) * qo.step, qo.off[d - NP],
+        dma16(qo.base + (of_k(kt) + shift) * qo.step, qo.off[d - NP],
               tile + PB + (wave * NQ + d - NP) * 1024);
     };
     auto issue = [&](int kt, auto slot_c) {
@@ -736,16 +744,21 @@ struct DmaCore {
 
     if (kleft != 0) {
       const int64_t kf = w.K / BK;
-      static_for<0, NP>([&](auto d) {
-        po.template issue_tail<decltype(d)::value>(kf, slot<0>(), wave, lane, kleft);
-      });
-      static_for<0, NQ>([&](auto d) {
-        qo.template issue_tail<decltype(d)::value>(kf, slot<0>() + PB, wave, lane, kleft);
+      static_for<0, PLANES>([&](auto s) {
+        constexpr int S = decltype(s)::value;
+        Operand<PKS, BM> p = po;
+        p.base = first(S);
+        static_for<0, NP>([&](auto d) {
+          p.template issue_tail<decltype(d)::value>(kf, slot<S>(), wave, lane, kleft);
+        });
+        static_for<0, NQ>([&](auto d) {
+          qo.template issue_tail<decltype(d)::value>(kf, slot<S>() + PB, wave, lane, kleft);
+        });
       });
     } else {
-      issue(0, Int<0>{});
+      static_for<0, PLANES>([&](auto s) { issue(decltype(s)::value, s); });
     }
-    static_for<1, NS>([&](auto s) {
+    static_for<PLANES, NS>([&](auto s) {
       if (decltype(s)::value < nk) issue(decltype(s)::value, s);
     });
     if (nk >= NS) wait_counts<(NS - 1) * DPS>();
