@@ -310,12 +310,13 @@ void store_points(const void* context, void* g, int64_t ldg, const float* c, int
 
 // Shares of dh's sum, which each piece of g takes: the least estimated time of
 // the products (their tile core as run_dh picks it) and of the fp32 sums that
-// the shares are added up in, at 2.5 TB/s, once more than there are pieces.
+// the shares are added up in, written and read at 2.5 TB/s.  Tiles past 256 count
+// up to as many on every CU: the one with the most decides.
 // (The step, us, with the cross entropy's rule, as many shares as fill the GPU
 // with 128 x 128 tiles, 16 at most, and with this one: 930 x 13715 x 5376 987 and
 // 833, 2048 x 32000 x 2048 1532 and 1440, 62 x 60045 x 416 104 and 94, 122 x 55297
 // x 960 180 and 158.)
-int pick_splits(int64_t n, int64_t dim, int64_t piece, int64_t pieces, int32_t dtype) {
+int pick_splits(int64_t n, int64_t dim, int64_t piece, int32_t dtype) {
   const bool half = dtype == MUON_DTYPE_BF16;
   int best = 1;
   double least = 0.0;
@@ -324,13 +325,16 @@ int pick_splits(int64_t n, int64_t dim, int64_t piece, int64_t pieces, int32_t d
     auto time = [&](const auto& table) {
       double t = 0.0;
       for (const ShapeCost& c : table) {
-        const double e = shape_time(c, dh_tiles(n, s)(c.bm), dim, k);
+        const double columns = static_cast<double>(ceil_div(dim, c.bn));
+        const double tiles = dh_tiles(n, s)(c.bm) * columns;
+        const double even = tiles <= 256.0 ? tiles : std::ceil(tiles / 256.0) * 256.0;
+        const double e = shape_time(c, even / columns, dim, k);
         if (t == 0.0 || e < t) t = e;
       }
       return t;
     };
     double t = half && dim % 8 == 0 ? time(kShapeNN) : half ? time(kShapeAnyBf16) : time(kShapeAnyFp32);
-    if (s > 1) t += 8.0 * static_cast<double>(n * dim) * s / 2.5e6 * (1.0 + 1.0 / pieces) + 4.0 / pieces;
+    if (s > 1) t += 8.0 * static_cast<double>(n * dim) * s / 2.5e6 + 4.0;
     if (s == 1 || t < least) {
       best = s;
       least = t;
@@ -350,7 +354,7 @@ DistillWs distill_ws(int64_t n, int64_t vocab, int64_t dim, int64_t top, int32_t
   w.loss = loss_ws(n, vocab, dim, dtype, backward);
   if (backward) {
     const int64_t pieces = ceil_div(vocab, w.loss.piece);
-    w.loss.splits = pick_splits(n, dim, w.loss.piece, pieces, dtype);
+    w.loss.splits = pick_splits(n, dim, w.loss.piece, dtype);
     // (dh's fp32 sums stand last)
     size_t o = w.loss.part;
     if (w.loss.splits > 1 || pieces > 1)
