@@ -641,21 +641,23 @@ __global__ __launch_bounds__(kThreads) void k_seq_join(Offsets off, int span,
   out.template finish<G>(off, blockIdx.x * (kThreads / G) + threadIdx.x / G, span, head, carry);
 }
 
-// Few tokens and few sequences: the sums and their join in one workgroup, with
-// a wave for each span, the parts in LDS.
+// Few tokens and few sequences: the sums and their join in one workgroup, a
+// tile a wave, the parts in LDS.  (Policy forward, us, this way and with two
+// launches: 8192 tokens of 16 sequences 14.2 and 17.3, 16384 of 64, two tiles a
+// wave, 17.2 and 17.3, 32768 29.1 and 16.8.)
 constexpr int kSmallThreads = 1024, kSmallWaves = kSmallThreads / 64;
-constexpr int kSmallTokens = 16384, kSmallSequences = 1024;
+constexpr int kSmallTokens = kSmallWaves * kTile, kSmallSequences = 1024;
 template <typename Terms, typename Out>
-__global__ __launch_bounds__(kSmallThreads) void k_seq_small(Terms w, Offsets off, int span,
+__global__ __launch_bounds__(kSmallThreads) void k_seq_small(Terms w, Offsets off,
                                                              Out out) {
   __shared__ int marks[kSmallWaves][kTile];
   __shared__ Sums head[kSmallSequences], carry[kSmallWaves];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  span_sums(w, off, span, wave, threadIdx.x & 63, marks[wave], head, carry);
+  span_sums(w, off, kTile, wave, threadIdx.x & 63, marks[wave], head, carry);
   __syncthreads();
   constexpr int G = kSmallWaves;  // as many lanes as there can be spans
   for (int r0 = 0; r0 < out.results(off); r0 += blockDim.x / G)
-    out.template finish<G>(off, r0 + threadIdx.x / G, span, head, carry);
+    out.template finish<G>(off, r0 + threadIdx.x / G, kTile, head, carry);
 }
 
 struct PolicySlope {
@@ -841,10 +843,8 @@ template <typename Terms, typename Out>
 void launch_sums(const Terms& w, const Offsets& off, int64_t results, Sums* head, Sums* carry,
                  const Out& out, hipStream_t s) {
   if (off.n <= kSmallTokens && off.count <= kSmallSequences) {
-    const int span = std::max((off.n + kSmallWaves * kTile - 1) / (kSmallWaves * kTile), 1) * kTile;
-    const int waves = std::max((off.n + span - 1) / span, 4);
-    hipLaunchKernelGGL((k_seq_small<Terms, Out>), dim3(1), dim3(64 * waves), 0, s, w, off, span,
-                       out);
+    const int waves = std::max((off.n + kTile - 1) / kTile, 4);
+    hipLaunchKernelGGL((k_seq_small<Terms, Out>), dim3(1), dim3(64 * waves), 0, s, w, off, out);
     return;
   }
   const int64_t blocks = (spans_of(off.n) + kWaves - 1) / kWaves;

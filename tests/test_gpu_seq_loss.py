@@ -97,6 +97,10 @@ CASES = [
     ("even", 4, 2048, 512, 512),
     ("ragged", 13, 1537, 9, 0),
     ("gaps", 300, 5000, 1, 700),
+    ("ragged", 30, 8192, 0, 0),         # the most tokens of one workgroup, and one more
+    ("ragged", 30, 8192, 1, 0),
+    ("gaps", 1024, 7000, 0, 5),         # the most sequences, and one more
+    ("gaps", 1025, 7000, 0, 5),
     ("one", 900, 40001, 0, 3),
     ("ragged", 5000, 70000, 0, 0),
     ("gaps", 5000, 3000, 2, 2),
