@@ -564,8 +564,10 @@ int lm_loss_backward(const void* hidden, int64_t ld_hidden, const void* weight, 
  * teacher values that count, or a NaN or +infinity in its logits, makes its
  * loss NaN. */
 
-/* Device workspace of the two calls below, as lm_loss_workspace_size, with
- * 4 bytes an entry more (for the forward, of at most 16384 rows). */
+/* Device workspace of the two calls below, as lm_loss_workspace_size, with 4
+ * bytes an entry more (for the forward, of at most 16384 rows), and a copy of a
+ * bf16 weight (the forward's: of hidden too) whose rows are no multiple of 16
+ * bytes, for calls of hundreds of rows.  Host-only. */
 size_t distill_loss_workspace_size(int64_t n, int64_t vocab, int64_t dim, int64_t top,
                                    int32_t dtype, int32_t backward);
 

@@ -80,15 +80,34 @@ __device__ __forceinline__ void teacher_stats(const float (&z)[E], float scale, 
   log_sum = logf(s);
 }
 
-// For the backward: of row t the first listed column or -1, the largest z and
-// log sum, and (rows not null) hidden, zeros for a row without a list.
+// What the sort leaves besides: (column not null) of row t the first listed
+// column or -1, the largest z and log sum; (rows not null) hidden, with column
+// zeros for a row without a list, in rows of `room` bytes, zeros behind its own.
 struct Marks {
   int32_t* column;
   f32x2_t* stats;
   const char* hidden;
   char* rows;
-  int64_t stride, bytes;  // of a row
+  int64_t stride, bytes, room;  // of a row
 };
+// One wave copies a row of `bytes` bytes, elements of two or four, into one of
+// `room`; not `some`: zeros.
+__device__ __forceinline__ void lay_row(const char* from, char* to, int64_t bytes, int64_t room,
+                                        bool some, int lane) {
+  for (int64_t i = lane * 16; i < room; i += 64 * 16) {
+    if (i + 16 <= bytes) {
+      u32x4_t v = {0, 0, 0, 0};
+      if (some) __builtin_memcpy(&v, from + i, 16);
+      __builtin_memcpy(to + i, &v, 16);
+    } else {
+      for (int64_t k = i; k < min(i + 16, room); k += 2) {
+        uint16_t v = 0;
+        if (some && k < bytes) __builtin_memcpy(&v, from + k, 2);
+        __builtin_memcpy(to + k, &v, 2);
+      }
+    }
+  }
+}
 
 // One wave a row: keys [n][top] in ascending order (a bitonic network over
 // 64 E keys, element lane E + e in register e), and what marks asks for.
@@ -145,25 +164,21 @@ __global__ __launch_bounds__(kThreads) void k_distill_sort(Lists a, int64_t n, u
     const int i = lane * E + e;
     if (i < a.top) keys[t * a.top + i] = x[e];
   }
-  if (marks.column == nullptr) return;
-  const bool listed = __builtin_amdgcn_readfirstlane(x[0]) != kNoKey;
-  if (lane == 0) marks.column[t] = listed ? static_cast<int32_t>(x[0] >> kPlaceBits) : -1;
-  if (marks.rows == nullptr) return;
-  const char* from = marks.hidden + t * marks.stride;
-  char* to = marks.rows + t * marks.bytes;
-  for (int64_t i = lane * 16; i < marks.bytes; i += 64 * 16) {
-    if (i + 16 <= marks.bytes) {
-      u32x4_t v = {0, 0, 0, 0};
-      if (listed) __builtin_memcpy(&v, from + i, 16);
-      __builtin_memcpy(to + i, &v, 16);
-    } else {  // elements of two bytes or four
-      for (int64_t k = i; k < marks.bytes; k += 2) {
-        uint16_t v = 0;
-        if (listed) __builtin_memcpy(&v, from + k, 2);
-        __builtin_memcpy(to + k, &v, 2);
-      }
-    }
-  }
+  const bool listed =
+      marks.column == nullptr || __builtin_amdgcn_readfirstlane(x[0]) != kNoKey;
+  if (marks.column != nullptr && lane == 0)
+    marks.column[t] = listed ? static_cast<int32_t>(x[0] >> kPlaceBits) : -1;
+  if (marks.rows != nullptr)
+    lay_row(marks.hidden + t * marks.stride, marks.rows + t * marks.room, marks.bytes, marks.room,
+            listed, lane);
+}
+
+// The weight's rows laid out in rows of `room` bytes, a wave a row.
+__global__ __launch_bounds__(kThreads) void k_distill_lay(const char* w, int64_t rows,
+                                                          int64_t bytes, int64_t room, char* out) {
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * (kThreads / 64) + (threadIdx.x >> 6);
+       r < rows; r += static_cast<int64_t>(gridDim.x) * (kThreads / 64))
+    lay_row(w + r * bytes, out + r * room, bytes, room, true, threadIdx.x & 63);
 }
 
 // Joins a row's tiles (R rows a workgroup) and turns its listed logits into
@@ -343,36 +358,64 @@ int pick_splits(int64_t n, int64_t dim, int64_t piece, int32_t dtype) {
   return best;
 }
 
-// The cross entropy's workspace and, behind it, the lists'.
+// bf16 rows off the 16-byte grid are laid out on it, padded with zeros, where
+// there are rows enough for the DMA cores to gain what the copy of the weight
+// costs (us, laid out and not: backward 64 x 32000 x 2001 214 and 194, 96 218 and
+// 264, 192 283 and 388, step of 8192 5750 and 13700; forward 384 x 32000 x 2001
+// 150 and 109, 600 x 100003 x 777 241 and 250, 2048 x 32000 x 2001 335 and 506).
+constexpr int64_t kLayForward = 512, kLayBackward = 96;
+bool lay_out(int64_t n, int64_t dim, int32_t dtype, bool backward) {
+  return dtype == MUON_DTYPE_BF16 && dim % 8 != 0 && n >= (backward ? kLayBackward : kLayForward);
+}
+
+// The cross entropy's workspace and, behind it, the lists'; hidden and the
+// weight laid out in rows of dim elements.
 struct DistillWs {
   LossWs loss;
-  size_t keys, marks, stats, total;
+  int64_t dim;
+  size_t keys, marks, stats, hidden, weight, total;
 };
 DistillWs distill_ws(int64_t n, int64_t vocab, int64_t dim, int64_t top, int32_t dtype,
                      bool backward) {
   DistillWs w{};
-  w.loss = loss_ws(n, vocab, dim, dtype, backward);
+  const bool laid = lay_out(n, dim, dtype, backward);
+  w.dim = laid ? ceil_div(dim, 8) * 8 : dim;
+  w.loss = loss_ws(n, vocab, w.dim, dtype, backward);
   if (backward) {
-    const int64_t pieces = ceil_div(vocab, w.loss.piece);
-    w.loss.splits = pick_splits(n, dim, w.loss.piece, dtype);
+    w.loss.splits = pick_splits(n, w.dim, w.loss.piece, dtype);
     // (dh's fp32 sums stand last)
     size_t o = w.loss.part;
-    if (w.loss.splits > 1 || pieces > 1)
-      o += align256(static_cast<size_t>(w.loss.splits) * static_cast<size_t>(n * dim) * 4);
-    w.loss.total = std::max(o, loss_ws(n, vocab, dim, dtype, false).total);
+    if (w.loss.splits > 1 || w.loss.piece < vocab || laid)
+      o += align256(static_cast<size_t>(w.loss.splits) * static_cast<size_t>(n * w.dim) * 4);
+    w.loss.total = o;
   }
   const int64_t rows = backward ? n : w.loss.stats_rows;
   size_t o = align256(w.loss.total);
-  w.keys = o;
-  o += align256(static_cast<size_t>(rows * top) * 4);
+  auto take = [&o](size_t& at, int64_t bytes) {
+    at = o;
+    o += align256(static_cast<size_t>(bytes));
+  };
+  take(w.keys, rows * top * 4);
   if (backward) {
-    w.marks = o;
-    o += align256(static_cast<size_t>(n) * 4);
-    w.stats = o;
-    o += align256(static_cast<size_t>(n) * 8);
+    take(w.marks, n * 4);
+    take(w.stats, n * 8);
+    w.hidden = w.loss.rows;
+  } else if (laid) {
+    take(w.hidden, rows * w.dim * 2);
   }
+  if (laid) take(w.weight, vocab * w.dim * 2);
   w.total = o;
   return w;
+}
+// The weight laid out, if it has to be.
+const void* laid_weight(const void* weight, int64_t vocab, int64_t dim, const DistillWs& w,
+                        char* ws, hipStream_t s) {
+  if (w.dim == dim) return weight;
+  hipLaunchKernelGGL(k_distill_lay,
+                     dim3(static_cast<unsigned>(std::min<int64_t>(ceil_div(vocab, 4), 16384))),
+                     dim3(kThreads), 0, s, static_cast<const char*>(weight), vocab, dim * 2,
+                     w.dim * 2, ws + w.weight);
+  return ws + w.weight;
 }
 
 int check_distill(int64_t n, int64_t vocab, int64_t dim, int64_t ldh, int32_t dtype, int64_t top) {
@@ -435,24 +478,35 @@ int distill_loss_forward(const void* hidden, int64_t ld_hidden, const void* weig
   uint32_t* keys = reinterpret_cast<uint32_t*>(ws + w.keys);
   const size_t sz = train_dtype_size(dtype), isz = ids_64 ? 8 : 4;
   const size_t zsz = train_dtype_size(teacher_dtype);
+  const bool laid = w.dim != dim;
+  const void* laid_w = laid_weight(weight, vocab, dim, w, ws, stream);
   for (int64_t r0 = 0; r0 < n; r0 += w.loss.stats_rows) {
     const int rows = static_cast<int>(std::min(w.loss.stats_rows, n - r0));
+    const char* h = static_cast<const char*>(hidden) + static_cast<size_t>(r0 * ld_hidden) * sz;
     const Lists lists =
         lists_of(static_cast<const char*>(ids) + static_cast<size_t>(r0 * ld_ids) * isz, ids_64,
                  ld_ids, static_cast<const char*>(teacher) + static_cast<size_t>(r0 * ld_teacher) * zsz,
                  teacher_dtype, ld_teacher, vocab, top, temperature);
-    sort_lists(lists, rows, keys, Marks{}, stream);
+    Marks marks{};
+    if (laid) {
+      marks.hidden = h;
+      marks.rows = ws + w.hidden;
+      marks.stride = ld_hidden * 2;
+      marks.bytes = dim * 2;
+      marks.room = w.dim * 2;
+    }
+    sort_lists(lists, rows, keys, marks, stream);
     StatsArgs a{};
-    a.h = static_cast<const char*>(hidden) + static_cast<size_t>(r0 * ld_hidden) * sz;
-    a.w = weight;
+    a.h = laid ? ws + w.hidden : h;
+    a.w = laid_w;
     a.tile_m = reinterpret_cast<float*>(ws + w.loss.tile_m);
     a.tile_s = reinterpret_cast<float*>(ws + w.loss.tile_s);
     a.keys = keys;
     a.points = logp + r0 * top;
-    a.ldh = ld_hidden;
+    a.ldh = laid ? w.dim : ld_hidden;
     a.vocab = vocab;
     a.n = rows;
-    a.dim = static_cast<int>(dim);
+    a.dim = static_cast<int>(w.dim);
     a.top = static_cast<int>(top);
     a.scale = lists.scale;
     const int tiles = loss_stats<true>(a, dtype, stream);
@@ -503,14 +557,17 @@ int distill_loss_backward(const void* hidden, int64_t ld_hidden, const void* wei
   const int64_t sz = static_cast<int64_t>(train_dtype_size(dtype));
   const Lists lists = lists_of(ids, ids_64, ld_ids, teacher, teacher_dtype, ld_teacher, vocab, top,
                                temperature);
+  const bool laid = w.dim != dim;
   sort_lists(lists, n, keys,
              Marks{marks, stats, static_cast<const char*>(hidden),
-                   dweight != nullptr ? ws + w.loss.rows : nullptr, ld_hidden * sz, dim * sz},
+                   dweight != nullptr || laid ? ws + w.hidden : nullptr, ld_hidden * sz, dim * sz,
+                   w.dim * sz},
              stream);
   const PointArgs points{lists, keys, stats, logp, dloss, n, dtype == MUON_DTYPE_FP32};
   BackwardArgs b{};
-  b.h = hidden;
-  b.w = weight;
+  // (a row without a list has no gradient: its zeros will do)
+  b.h = laid ? ws + w.hidden : static_cast<const char*>(hidden);
+  b.w = laid_weight(weight, vocab, dim, w, ws, stream);
   b.targets = marks;  // rows with a list; the marked column is stored again
   b.lse = lse;
   b.dloss = dloss;
@@ -518,9 +575,10 @@ int distill_loss_backward(const void* hidden, int64_t ld_hidden, const void* wei
   b.dw = dweight;
   b.n = n;
   b.vocab = vocab;
-  b.dim = dim;
-  b.ldh = ld_hidden;
+  b.dim = w.dim;
+  b.ldh = laid ? w.dim : ld_hidden;
   b.ld_dh = ld_dhidden;
+  b.cols = dim;
   b.accumulate = accumulate != 0;
   b.ws = ws;
   b.scale = lists.scale;

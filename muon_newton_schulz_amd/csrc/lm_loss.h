@@ -107,6 +107,7 @@ struct BackwardArgs {
   const float *lse, *dloss;
   void *dh, *dw;  // either may be null
   int64_t n, vocab, dim, ldh, ld_dh;
+  int64_t cols;   // of dh and dw, at most dim: operands may be laid out with more
   int t64, accumulate;
   char* ws;
   float scale;

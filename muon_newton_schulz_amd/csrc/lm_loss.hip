@@ -254,6 +254,7 @@ int lm_loss_backward(const void* hidden, int64_t ld_hidden, const void* weight, 
   b.dim = dim;
   b.ldh = ld_hidden;
   b.ld_dh = ld_dhidden;
+  b.cols = dim;
   b.t64 = targets_64 != 0;
   b.accumulate = accumulate != 0;
   b.ws = static_cast<char*>(workspace);

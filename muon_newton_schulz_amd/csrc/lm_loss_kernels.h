@@ -407,18 +407,21 @@ __global__ __launch_bounds__(kThreads, Core::kWaves) void k_loss_dh(DhArgs a, in
                 w.pn, w.qn);
 }
 
-// dhidden = sum of the splits, in order.
+// dhidden = sum of the splits, in order; of the sums' dim columns the first
+// cols.
 template <typename TO>
 __global__ __launch_bounds__(kThreads) void k_loss_dh_join(const float* __restrict__ part,
-                                                           int splits, int n, int dim, TO* out,
-                                                           int64_t ld) {
+                                                           int splits, int n, int dim, int cols,
+                                                           TO* out, int64_t ld) {
   const int64_t total = static_cast<int64_t>(n) * dim;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total;
        i += static_cast<int64_t>(gridDim.x) * kThreads) {
     float v = part[i];
 #pragma unroll 8
     for (int s = 1; s < splits; ++s) v += part[s * total + i];
-    from_f32(v, out + i / dim * ld + i % dim);
+    const int64_t t = i / dim;
+    const int d = static_cast<int>(i - t * dim);
+    if (d < cols) from_f32(v, out + t * ld + d);
   }
 }
 
@@ -428,11 +431,14 @@ struct DwArgs {
   const float* c;
   void* dw;  // the piece's first row
   int64_t ldg, ldh, vocab;
-  int n, dim, len, accumulate;
+  int n, dim, len, accumulate, cols;  // cols: of dw, at most dim
   float scale;
 };
 
-template <bool TURNS, typename Core, bool STREAM, typename T, typename TO>
+// How a tile of dw is stored: in rows on the grid, past the caches (kStream) or
+// not, or (kOff) quad by quad.
+enum Store { kRows, kStream, kOff };
+template <bool TURNS, typename Core, Store STORE, typename T, typename TO>
 __global__ __launch_bounds__(kThreads, Core::kWaves) void k_loss_dw(DwArgs a, int nx, int ny) {
   using W = LossTile<T>;
   int x, y;
@@ -450,9 +456,12 @@ __global__ __launch_bounds__(kThreads, Core::kWaves) void k_loss_dw(DwArgs a, in
   f32x16_t acc[Core::NJ][Core::MI];
   run_planes<TURNS, Core, T>(w, a.n * a.ldg, acc);
   scale_acc(acc, *a.c * a.scale);
-  TO* C = static_cast<TO*>(a.dw) + static_cast<int64_t>(w.i0) * a.dim + w.j0;
-  Core::template write<STREAM>(acc, C, a.dim, a.accumulate ? C : static_cast<const TO*>(nullptr),
-                               a.dim, w.pn, w.qn);
+  TO* C = static_cast<TO*>(a.dw) + static_cast<int64_t>(w.i0) * a.cols + w.j0;
+  const TO* add = a.accumulate ? C : nullptr;
+  if constexpr (STORE == kOff)
+    write_quads<Core>(acc, C, a.cols, add, a.cols, w.pn, a.cols - w.j0);
+  else
+    Core::template write<STORE == kStream>(acc, C, a.cols, add, a.cols, w.pn, a.cols - w.j0);
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -549,10 +558,13 @@ template <bool TURNS, typename Core, typename T, typename TO>
 void launch_dw(const DwArgs& a, hipStream_t s) {
   const int nx = static_cast<int>(ceil_div(a.len, Core::BM));
   const int ny = static_cast<int>(ceil_div(a.dim, Core::BN));
-  auto* kernel = k_loss_dw<TURNS, Core, false, T, TO>;
+  auto* kernel = k_loss_dw<TURNS, Core, kRows, T, TO>;
   if constexpr (Core::kGrid) {
-    if (stream_gradient(static_cast<const TO*>(a.dw), a.vocab, a.dim))
-      kernel = k_loss_dw<TURNS, Core, true, T, TO>;
+    if (stream_gradient(static_cast<const TO*>(a.dw), a.vocab, a.cols))
+      kernel = k_loss_dw<TURNS, Core, kStream, T, TO>;
+    if constexpr (TURNS) {
+      if (!on_grid(a.dw, a.cols, a.cols)) kernel = k_loss_dw<TURNS, Core, kOff, T, TO>;
+    }
   }
   hipLaunchKernelGGL(kernel, dim3(tile_blocks(nx, ny)), dim3(kThreads), 0, s, a, nx, ny);
 }
@@ -588,6 +600,9 @@ void run_backward(const BackwardArgs& b, const LossWs& w, hipStream_t s) {
                        static_cast<int>(b.n), static_cast<int>(b.dim), b.vocab, rows);
   }
   const bool grid = on_grid(b.h, b.ldh, b.dim) && on_grid(b.w, b.dim, b.dim);
+  // operands laid out on the grid for results that are not: dh leaves the fp32
+  // sums in the join alone, dw's tiles are stored quad by quad
+  const bool laid = LISTS && b.cols != b.dim;
   for (int64_t v0 = 0; v0 < b.vocab; v0 += w.piece) {
     const int len = static_cast<int>(std::min(w.piece, b.vocab - v0));
     const T* wp = static_cast<const T*>(b.w) + v0 * b.dim;
@@ -597,23 +612,25 @@ void run_backward(const BackwardArgs& b, const LossWs& w, hipStream_t s) {
     if (b.after_g != nullptr) b.after_g(b.context, g, w.ldg, c, v0, len, s);
     if (b.dh != nullptr) {
       const bool last = v0 + len == b.vocab;
-      run_dh<LISTS, T, TH>(DhArgs{g, wp, b.targets, c, part, last && w.splits == 1 ? b.dh : nullptr,
-                           w.ldg, b.ld_dh, b.vocab, static_cast<int>(b.n),
-                           static_cast<int>(b.dim), len, w.splits, v0 == 0 ? 1 : 0, b.t64,
-                           b.scale},
-                    grid && on_grid(b.dh, b.ld_dh, b.dim), s);
+      run_dh<LISTS, T, TH>(
+          DhArgs{g, wp, b.targets, c, part, last && w.splits == 1 && !laid ? b.dh : nullptr, w.ldg,
+                 b.ld_dh, b.vocab, static_cast<int>(b.n), static_cast<int>(b.dim), len, w.splits,
+                 v0 == 0 ? 1 : 0, b.t64, b.scale},
+          grid && (laid || on_grid(b.dh, b.ld_dh, b.dim)), s);
     }
     if (b.dw != nullptr)
-      run_dw<LISTS, T, TW>(DwArgs{g, rows, c, static_cast<TW*>(b.dw) + v0 * b.dim, w.ldg, b.dim, b.vocab,
-                           static_cast<int>(b.n), static_cast<int>(b.dim), len, b.accumulate,
-                           b.scale},
-                    grid && on_grid(b.dw, b.dim, b.dim), s);
+      run_dw<LISTS, T, TW>(
+          DwArgs{g, rows, c, static_cast<TW*>(b.dw) + v0 * b.cols, w.ldg, b.dim, b.vocab,
+                 static_cast<int>(b.n), static_cast<int>(b.dim), len, b.accumulate,
+                 static_cast<int>(b.cols), b.scale},
+          grid && (laid || on_grid(b.dw, b.dim, b.dim)), s);
   }
-  if (b.dh != nullptr && w.splits > 1)
+  if (b.dh != nullptr && (w.splits > 1 || laid))
     hipLaunchKernelGGL(k_loss_dh_join<TH>,
                        dim3(static_cast<unsigned>(std::min<int64_t>(4096, ceil_div(b.n * b.dim, kThreads)))),
                        dim3(kThreads), 0, s, part, w.splits, static_cast<int>(b.n),
-                       static_cast<int>(b.dim), static_cast<TH*>(b.dh), b.ld_dh);
+                       static_cast<int>(b.dim), static_cast<int>(b.cols), static_cast<TH*>(b.dh),
+                       b.ld_dh);
 }
 
 // Row statistics of scale * h W^T, and what targets or keys name.  Returns the

@@ -126,6 +126,12 @@ CASES = [
     (300, 777, 101, 300, "bf16", "bf16", 2.0, "fp32", "bf16", 1, 0, 1, 1, "spread"),
     (513, 1025, 512, 8, "bf16", "fp32", 1.0, "bf16", "bf16", 0, 16, 1, 0, "spread"),
     (257, 2048, 40, 1024, "bf16", "fp32", 1.0, "bf16", "bf16", 0, 0, 1, 0, "spread"),
+    # rows off the grid that are laid out on it: backward, and both
+    (95, 500, 205, 12, "bf16", "fp32", 1.0, "bf16", "bf16", 0, 0, 1, 0, "spread"),
+    (96, 500, 205, 12, "bf16", "fp32", 1.0, "bf16", "fp32", 1, 5, 1, 1, "spread"),
+    (511, 300, 1, 12, "bf16", "fp32", 1.0, "fp32", "bf16", 0, 0, 1, 0, "near"),
+    (512, 1000, 1001, 7, "bf16", "bf16", 2.0, "bf16", "bf16", 3, 1, 0, 0, "spread"),
+    (700, 900, 262, 40, "bf16", "fp32", 1.0, "fp32", "bf16", 0, 0, 1, 1, "near"),
 ]
 
 
@@ -185,8 +191,9 @@ def test_loss_and_gradients(gpu, n, vocab, dim, top, dt, zt, T, hd, wd, off, pad
     (128, 8000, 1541, 64, "fp32", 0), (40, 300, 261, 50, "fp32", 0),
     (130, 2000, 1032, 20, "bf16", 0), (40, 20011, 264, 64, "bf16", 0),
     (600, 20011, 520, 70, "bf16", 0), (4000, 4000, 840, 33, "bf16", 0),
-    (8200, 20011, 1032, 16, "bf16", 0), (130, 8000, 1541, 40, "bf16", 1),
-    (2100, 2000, 261, 12, "bf16", 1), (130, 8000, 1541, 30, "fp32", 0),
+    (8200, 20011, 1032, 16, "bf16", 0), (130, 8000, 1544, 40, "bf16", 1),
+    (2100, 2000, 264, 12, "bf16", 1), (130, 8000, 1541, 40, "bf16", 1),
+    (2100, 2000, 261, 12, "bf16", 1), (8200, 20011, 133, 9, "bf16", 0), (130, 8000, 1541, 30, "fp32", 0),
     (2100, 2000, 261, 64, "fp32", 0)])
 def test_tile_cores(gpu, n, vocab, dim, top, dt, off):
     h, w, ids, z, dl = _inputs(gpu, n, vocab, dim, top, dt, "fp32", off)
