@@ -325,8 +325,9 @@ void store_points(const void* context, void* g, int64_t ldg, const float* c, int
 
 // Shares of dh's sum, which each piece of g takes: the least estimated time of
 // the products (their tile core as run_dh picks it) and of the fp32 sums that
-// the shares are added up in, written and read at 2.5 TB/s.  Tiles past 256 count
-// up to as many on every CU: the one with the most decides.
+// the shares are added up in, written and read at 2.5 TB/s.  Where CUs take more
+// than one tile at a time, those past 256 count up to as many on every CU: the
+// one with the most decides.
 // (The step, us, with the cross entropy's rule, as many shares as fill the GPU
 // with 128 x 128 tiles, 16 at most, and with this one: 930 x 13715 x 5376 987 and
 // 833, 2048 x 32000 x 2048 1532 and 1440, 62 x 60045 x 416 104 and 94, 122 x 55297
@@ -342,7 +343,8 @@ int pick_splits(int64_t n, int64_t dim, int64_t piece, int32_t dtype) {
       for (const ShapeCost& c : table) {
         const double columns = static_cast<double>(ceil_div(dim, c.bn));
         const double tiles = dh_tiles(n, s)(c.bm) * columns;
-        const double even = tiles <= 256.0 ? tiles : std::ceil(tiles / 256.0) * 256.0;
+        const double even =
+            c.per_cu == 1 || tiles <= 256.0 ? tiles : std::ceil(tiles / 256.0) * 256.0;
         const double e = shape_time(c, even / columns, dim, k);
         if (t == 0.0 || e < t) t = e;
       }
