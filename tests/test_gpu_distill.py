@@ -359,3 +359,18 @@ def test_gradients_against_differences(gpu):
             tol = float((dl.double() * (span ** 3 * eps ** 2 / 6 + 2 * ref.loss_bound / eps)).sum())
             tol += float((dl.double() * span).sum()) * 2.0 ** -24 / eps * 8
             assert abs(slope - float((grad.double() * v.double()).sum())) <= tol
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_the_largest_vocabulary(gpu, dt):
+    n, vocab, dim, top = 5, 1 << 21, 8, 1024
+    h, w, ids, z, _ = _inputs(gpu, n, vocab, dim, top, dt, "fp32")
+    ids[0, 0], ids[1, 1], ids[2, 2], ids[3, 3] = vocab - 1, vocab, 0, -1
+    dl = torch.rand(n, device=gpu) + 0.5
+    ref = Ref(h, w, ids, z, 1.0, dl, dt)
+    loss, lse, logp = M.distill_loss_forward(h, w, ids, z)
+    assert_within(loss, ref.loss, ref.loss_bound)
+    assert_within(logp, ref.logp, ref.logp_bound)
+    dh, dw = M.distill_loss_backward(h, w, ids, z, lse, logp, dl)
+    assert_within(dh, ref.dh, 1.01 * (ref.dh_err + ref.dh.abs() * HALF[DT[dt]]))
+    assert_within(dw, ref.dw, 1.01 * (ref.dw_err + ref.dw.abs() * HALF[DT[dt]]))

@@ -410,3 +410,30 @@ def test_gradients_against_differences(gpu):
         tol += float(dp.max()) * 0.05 * float((nll.abs() + 1).sum()) * U / eps * 4
         tol += 2.0 ** -20 * float((grad.abs()).sum())
         assert abs(slope - float((grad.double() * v.double()).sum())) <= tol
+
+
+@pytest.mark.parametrize("seqs,tail", [(3, 0), (1 << 24, 1000)])
+def test_most_tokens_and_most_sequences(gpu, seqs, tail):
+    # values that every sum holds exactly: small integers over 8
+    n = (1 << 26) - 1
+    g = torch.Generator(device=gpu)
+    g.manual_seed(seqs)
+    cuts = torch.randint(0, n - tail + 1, (seqs - 1,), generator=g, device=gpu).sort().values
+    off = torch.cat([cuts.new_zeros(1), cuts, cuts.new_full((1,), n - tail)]).int()
+    nll = torch.randint(0, 8, (n,), generator=g, device=gpu).float() / 8
+    mask = torch.randint(0, 2, (n,), generator=g, device=gpu, dtype=torch.uint8)
+    adv = torch.ones(seqs, device=gpu)
+    loss, kl, count, clipped = M.policy_loss_forward(nll, nll, adv, off, mask=mask, mean=False)
+    ends = torch.cat([off.new_zeros(1).long(), mask.long().cumsum(0)])[off.long()]
+    want = ends[1:] - ends[:-1]
+    assert torch.equal(count.long(), want) and not bool(clipped.any()) and not bool(kl.any())
+    assert torch.equal(loss, -want.float())          # a ratio of 1 for every token
+    dn = M.policy_loss_backward(nll, nll, adv, off, count, adv, mask=mask, mean=False,
+                                dnll=torch.full((n,), 7.0, device=gpu))
+    assert torch.equal(dn[:n - tail], mask[:n - tail].float())
+    assert bool((dn[n - tail:] == 7).all())
+    if seqs % 2 == 0:
+        loss, x, reward, count = M.preference_loss_forward(nll, off, mask=mask, beta=1.0)
+        ends = torch.cat([nll.new_zeros(1).double(), (nll * mask).double().cumsum(0)])[off.long()]
+        assert torch.equal(reward, -(ends[1:] - ends[:-1]).float())
+        assert torch.equal(count.long(), want)
