@@ -36,7 +36,7 @@ namespace {
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kPer = 8, kTile = 64 * kPer;  // tokens of a lane, of a wave's tile
 
-// first + 1 offsets, non-decreasing; whatever they hold, values are within
+// count + 1 offsets, non-decreasing; whatever they hold, values are within
 // [0, n].
 struct Offsets {
   const int32_t* p;
