@@ -622,7 +622,8 @@ size_t sequence_loss_workspace_size(int64_t n, int64_t sequences);
  * (r > 1 + clip_high with A > 0, r < 1 - clip_low with A < 0; a ratio on the
  * border is not held).  advantages: one a sequence, or with per_token != 0 one
  * a token.  ref_nll may be null if kl_weight is 0 (then kl is 0).  clip_low in
- * [0, 1], clip_high >= 0. */
+ * [0, 1], clip_high >= 0.  An advantage of 0 makes r A 0 for an infinite ratio
+ * too, and NaN for a ratio that is NaN. */
 int policy_loss_forward(const float* nll, const float* old_nll, const float* ref_nll,
                         const uint8_t* mask, const float* advantages, int32_t per_token,
                         const int32_t* offsets, int64_t sequences, int64_t n, double clip_low,

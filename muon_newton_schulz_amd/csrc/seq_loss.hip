@@ -310,9 +310,9 @@ struct PolicyArgs {
     if (per_token) load_values<WHOLE>(adv, i, n, t.adv);
   }
   // Which of the tokens the clip holds, and the ratios (0 where A is, so
-  // that no 0 inf comes of a ratio beyond fp32).  Rounding keeps the order, so
-  // unless d rounds to what the bound rounds to, fp32 decides as the exact
-  // difference does.
+  // that no 0 inf comes of a ratio beyond fp32; a NaN stays one).  Rounding
+  // keeps the order, so unless d rounds to what the bound rounds to, fp32
+  // decides as the exact difference does.
   __device__ __forceinline__ int ratios(const Tokens& t, const float (&a)[kPer],
                                         float (&r)[kPer]) const {
     int cut = 0;
@@ -323,7 +323,7 @@ struct PolicyArgs {
       const bool up = a[j] > 0.0f;
       cut |= static_cast<int>(up ? d > f_high : a[j] < 0.0f && d < f_low) << j;
       border |= d == (up ? f_high : f_low);
-      r[j] = a[j] == 0.0f ? 0.0f : expf(d);
+      r[j] = a[j] == 0.0f && d == d ? 0.0f : expf(d);
     }
     if (__ballot(border) == 0) return cut;
 #pragma unroll

@@ -1,0 +1,49 @@
+"""Values of the losses over packed sequences where a shortcut shows: a NaN
+beside an advantage of 0, sums that cancel, slopes far from and next to a
+border.
+
+U = 2^-24, half a step of fp32; bounds stand at the tests."""
+
+import math
+
+import pytest
+import torch
+
+import muon_newton_schulz_amd as M
+from train_ops_util import assert_within, same_bits
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+
+def _offsets(gpu, *values):
+    return torch.tensor(values, dtype=torch.int32, device=gpu)
+
+
+@pytest.mark.parametrize("per_token", [False, True])
+@pytest.mark.parametrize("which", ["nll", "old"])
+def test_nan_beside_an_advantage_of_zero(gpu, which, per_token):
+    # r A is NaN where r is, whatever A; an infinite ratio counts nothing at A = 0
+    n, off = 1300, _offsets(gpu, 0, 300, 700, 1300)
+    t = {"nll": torch.rand(n, device=gpu), "old": torch.rand(n, device=gpu)}
+    t[which][310] = math.nan
+    t["old"][900] = math.inf
+    adv = torch.zeros(n if per_token else 3, device=gpu)
+    loss, _, count, _ = M.policy_loss_forward(t["nll"], t["old"], adv, off, per_token=per_token)
+    assert loss.isnan().tolist() == [False, True, False]
+    assert float(loss[0]) == 0.0 and float(loss[2]) == 0.0
+    dn = M.policy_loss_backward(t["nll"], t["old"], adv, off, count, torch.ones(3, device=gpu),
+                                per_token=per_token)
+    assert dn.isnan().nonzero()[:, 0].tolist() == [310]
+    dn[310] = 0.0
+    assert not bool(dn.any())
+    # a masked NaN is not used
+    mask = torch.ones(n, dtype=torch.bool, device=gpu)
+    mask[310] = False
+    loss, _, count, _ = M.policy_loss_forward(t["nll"], t["old"], adv, off, mask=mask,
+                                              per_token=per_token)
+    assert not bool(loss.any())
+    dn = M.policy_loss_backward(t["nll"], t["old"], adv, off, count, torch.ones(3, device=gpu),
+                                mask=mask, per_token=per_token)
+    assert not bool(dn.any())
