@@ -604,8 +604,9 @@ int distill_loss_backward(const void* hidden, int64_t ld_hidden, const void* wei
  * not 0 there; N_s is the number of a sequence's tokens that count.  What the
  * other tokens hold is not used.  The backward calls write dnll of the tokens
  * that are in a sequence (0 for one that does not count) and leave the others
- * as they were; dnll is the dloss that lm_loss_backward takes.  Values are
- * fp32, sums fp64.  0 <= n < 2^26, 0 <= sequences <= 2^24. */
+ * as they were; dnll is the dloss that lm_loss_backward takes.  Values and
+ * the policy loss's terms are fp32, all sums fp64.  0 <= n < 2^26, 0 <=
+ * sequences <= 2^24. */
 
 /* Device workspace of the two forward calls (0 for sequences == 0 or sizes they
  * refuse).  Host-only. */

@@ -47,3 +47,19 @@ def test_nan_beside_an_advantage_of_zero(gpu, which, per_token):
     dn = M.policy_loss_backward(t["nll"], t["old"], adv, off, count, torch.ones(3, device=gpu),
                                 mask=mask, per_token=per_token)
     assert not bool(dn.any())
+
+
+@pytest.mark.parametrize("cuts", [(0, 3000), (0, 5, 6, 517, 1029, 1030, 1040, 2900, 3000),
+                                  (0, 0, 3, 3, 2000, 2000, 20000), (1, 9, 300000)])
+def test_sums_of_terms_that_cancel(gpu, cuts):
+    # A ratio of 1 and advantages of 2^24, 1, -2^24 and 1 in turns: a term is
+    # -A, and any fp32 sum of the first two loses the second.  All sums are
+    # whole numbers below 2^53, so the results are exact, rounded once.
+    off = _offsets(gpu, *cuts)
+    n = cuts[-1] + 3
+    nll = torch.rand(n, device=gpu)
+    adv = torch.tensor([2.0 ** 24, 1.0, -2.0 ** 24, 1.0], device=gpu).repeat(n // 4 + 1)[:n]
+    ends = torch.cat([adv.new_zeros(1).double(), adv.double().cumsum(0)])[off.long()]
+    want = -(ends[1:] - ends[:-1]).float()
+    loss, _, _, _ = M.policy_loss_forward(nll, nll, adv, off, per_token=True, mean=False)
+    assert torch.equal(loss, want)
