@@ -605,7 +605,12 @@ __device__ __forceinline__ double preference(const PreferenceHow& h, double x) {
 __device__ __forceinline__ float preference_slope(const PreferenceHow& h, float x) {
   if (h.kind == MUON_PREFERENCE_HINGE) return x < 1.0f ? -1.0f : (x >= 1.0f ? 0.0f : x);
   if (h.kind == MUON_PREFERENCE_SQUARED) return 2.0f * (x - 1.0f);
-  return h.smoothing - 1.0f / (1.0f + expf(x));
+  // smoothing s(x) - (1 - smoothing) s(-x), s(x) = 1 / (1 + e^-x): e^-|x| gives
+  // both s without a difference, which would lose the smaller one (smoothing - s(-x)
+  // all of it with smoothing 1 and x < -17)
+  const float t = expf(-fabsf(x)), big = 1.0f / (1.0f + t), small = t * big;
+  return h.smoothing * (x < 0.0f ? small : big) -
+         (1.0f - h.smoothing) * (x < 0.0f ? big : small);
 }
 
 struct PreferenceOut {

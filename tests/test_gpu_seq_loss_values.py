@@ -63,3 +63,23 @@ def test_sums_of_terms_that_cancel(gpu, cuts):
     want = -(ends[1:] - ends[:-1]).float()
     loss, _, _, _ = M.policy_loss_forward(nll, nll, adv, off, per_token=True, mean=False)
     assert torch.equal(loss, want)
+
+
+@pytest.mark.parametrize("smoothing", [0.0, 1.0, 0.25, 0.5])
+def test_logistic_slopes_far_from_zero(gpu, smoothing):
+    # f'(x) = e s(x) - (1 - e) s(-x), s(x) = 1 / (1 + exp(-x)), at margins given
+    # to the backward as they are.  Each s is off by exp's 2^-22 and 4 roundings
+    # of itself, each product by one more, the sum by U; then two factors of 1
+    # and their roundings, 2 U.
+    x = torch.cat([torch.linspace(-80, 80, 1601), torch.tensor([-17.0, -1e30, 1e30, 0.0])])
+    x = x.float().to(gpu)
+    pairs = x.numel()
+    off = torch.arange(2 * pairs + 1, dtype=torch.int32, device=gpu)
+    count = torch.ones(2 * pairs, dtype=torch.int32, device=gpu)
+    dn = M.preference_loss_backward(off, x, count, torch.ones(pairs, device=gpu), n=2 * pairs,
+                                    beta=1.0, smoothing=smoothing)
+    up, down = smoothing * torch.sigmoid(x.double()), (1 - smoothing) * torch.sigmoid(-x.double())
+    want = up - down
+    err = 1.01 * ((2.0 ** -22 + 6 * U) * (up + down) + 3 * U * want.abs()) + 2.0 ** -140
+    assert_within(dn[0::2], -want, err)
+    assert_within(dn[1::2], want, err)
