@@ -649,7 +649,8 @@ int policy_loss_backward(const float* nll, const float* old_nll, const float* re
  *   reward[s]  = beta * sum of (ref_nll - nll) over the tokens that count
  *                (/ N_s with mean != 0); ref_nll null: of -nll
  *   margins[i] = x = reward[2 i] - reward[2 i + 1] - margin,  loss[i] = f(x)
- * with f by kind (0 <= smoothing <= 1, 0 but for the logistic kind).  A
+ * with f by kind (0 <= smoothing <= 1, 0 but for the logistic kind).  margins
+ * is x rounded to fp32, but for the hinge no x below 1 becomes 1.  A
  * sequence without a token that counts has reward 0; its pair has loss 0 and
  * no gradient.  count[s] = N_s. */
 int preference_loss_forward(const float* nll, const float* ref_nll, const uint8_t* mask,

@@ -634,7 +634,11 @@ struct PreferenceOut {
     }
     if (i >= off.count / 2 || threadIdx.x % G != 0) return;
     const double x = value[0] - value[1] - h.margin;
-    margin[i] = static_cast<float>(x);
+    float r = static_cast<float>(x);
+    // the slope, which the backward takes from the margin, has a step at the
+    // hinge's border: a margin below it stays below
+    if (h.kind == MUON_PREFERENCE_HINGE && x < 1.0 && r == 1.0f) r = 1.0f - 0x1p-24f;
+    margin[i] = r;
     loss[i] = tokens[0] > 0 && tokens[1] > 0 ? static_cast<float>(preference(h, x)) : 0.0f;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {

@@ -83,3 +83,26 @@ def test_logistic_slopes_far_from_zero(gpu, smoothing):
     err = 1.01 * ((2.0 ** -22 + 6 * U) * (up + down) + 3 * U * want.abs()) + 2.0 ** -140
     assert_within(dn[0::2], -want, err)
     assert_within(dn[1::2], want, err)
+
+
+def test_hinge_next_to_its_border(gpu):
+    # x = 1 - 2^-k and 1 + 2^-k, exact in fp64: a pair with a loss has a slope
+    ks = [22, 23, 24, 25, 26, 30, 40, 50]
+    gaps = [2.0 ** -k for k in ks] + [0.0] + [-2.0 ** -k for k in ks]
+    pairs = len(gaps)
+    ref = torch.tensor([v for g in gaps for v in (1.0, g)], device=gpu)
+    nll = torch.zeros(2 * pairs, device=gpu)
+    off = torch.arange(2 * pairs + 1, dtype=torch.int32, device=gpu)
+    want = 1.0 - torch.tensor(gaps, dtype=torch.float64, device=gpu)
+    for kind in ("hinge", "squared", "logistic"):
+        loss, x, _, count = M.preference_loss_forward(nll, off, ref_nll=ref, beta=1.0, kind=kind)
+        if kind != "hinge":
+            assert torch.equal(x, want.float())
+            continue
+        # the margin moves by less than a step
+        assert torch.equal(x < 1, want < 1) and bool(((x.double() - want).abs() < 2.0 ** -23).all())
+        assert torch.equal(loss, (1 - want).clamp(min=0).float())
+        dn = M.preference_loss_backward(off, x, count, torch.ones(pairs, device=gpu), kind=kind,
+                                        n=2 * pairs, beta=1.0)
+        slope = (want < 1).float()
+        assert torch.equal(dn[0::2], slope) and torch.equal(dn[1::2], -slope)
