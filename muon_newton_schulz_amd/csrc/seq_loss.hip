@@ -96,9 +96,11 @@ struct Walk {
     offset = first + lane <= off.count ? off.at(first + lane) : off.n + kTile;
     value = valid(off, first + lane) ? w.of(first + lane) : Value{};
   }
-  // 64-way search for the number of offsets below `token`
-  __device__ __forceinline__ void find(const Offsets& off, const Source& w, int token, int lane) {
-    int lo = 0, len = off.count + 1;
+  // 64-way search for the first offset from lo on that is not below `token`:
+  // it is one of at most 64 from lo on, len of them
+  __device__ __forceinline__ static void search(const Offsets& off, int token, int lane, int& lo,
+                                                int& len) {
+    len = off.count + 1 - lo;
     while (len > 64) {
       const int step = (len + 63) >> 6, q = lane * step + step - 1;
       const bool below = q < len && off.at(lo + q) < token;
@@ -107,9 +109,22 @@ struct Walk {
       len = min(step - 1, len - c * step);
     }
     lo = __builtin_amdgcn_readfirstlane(lo);
+  }
+  __device__ __forceinline__ void find(const Offsets& off, const Source& w, int token, int lane) {
+    int lo = 0, len;
+    search(off, token, lane, lo, len);
     load(off, w, lo, lane);
     prior = valid(off, lo - 1) ? w.of(lo - 1) : Value{};
     next = lo + __popcll(__ballot(lane < len && offset < token));
+  }
+  // Past the sequences that start at `token` as the one before next does, and
+  // are empty but for the last.
+  __device__ __forceinline__ void skip(const Offsets& off, const Source& w, int token, int lane) {
+    int lo = next, len;
+    search(off, token + 1, lane, lo, len);
+    next = lo + __popcll(__ballot(lane < len && off.at(lo + lane) <= token));
+    load(off, w, next, lane);
+    prior = valid(off, next - 1) ? w.of(next - 1) : Value{};
   }
   // Marks the starts in the tile: start[j] is the sequence that starts at the
   // lane's token j, or -1; s: the one its first token is in unless it
@@ -121,9 +136,21 @@ struct Walk {
     bool any = false;
     while (next <= off.count) {
       if (next >= batch + 64) {
+        const int before = __builtin_amdgcn_readlane(offset, 63);
         prior = value.lane(63);
         load(off, w, next, lane);
         moved = any;
+        // A whole batch that starts where the one before it ended is part of a
+        // run of empty sequences (unused slots of a batch of fixed capacity),
+        // of which only the last one's mark counts.  (Forward and backward of
+        // 50001 tokens in 100 sequences, the other slots behind them, walked 64
+        // at a time, each load waiting for the one before, and this way: 2^13
+        // slots 58 and 88 us, 24 and 9; 2^20 9.3 and 12.6 ms, 0.39 and 0.01.)
+        if (any && __builtin_amdgcn_readlane(offset, 63) == before) {
+          skip(off, w, before, lane);
+          const int o = before - tile0;
+          if (lane == 0 && o >= 0 && o < kTile) atomicMax(&lds[o], next - 1);
+        }
       }
       const int o = offset - tile0;
       const uint64_t in = __ballot(batch + lane >= next && o < kTile);
