@@ -115,6 +115,29 @@ struct BackwardArgs {
                   hipStream_t s);
   const void* context;
 };
+// c: the largest finite |dloss| of the rows with a target, 1 if that is 0.
+void loss_scale(const BackwardArgs& b, float* c, hipStream_t s);
+// hidden with zeros in the rows without a target, [n][dim]: dW's sum runs over
+// all rows, and 0 times what such a row holds is 0 only where that is finite.
+void loss_rows(const BackwardArgs& b, void* rows, int32_t dtype, hipStream_t s);
+struct GradArgs {
+  const void* h;
+  const void* w;       // the piece's first row
+  const void* targets;
+  const float* lse;
+  const float* dloss;
+  const float* c;
+  void* g;             // [n][ldg], g / c; bf16: low plane, high plane
+  int64_t ldh, ldg, vocab, v0;
+  int n, dim, len, t64;  // len: vocabulary rows of the piece
+  float scale;           // of the logits
+};
+// g / c of a piece; grid: the operands are on the DMA core's grid
+void loss_g(const GradArgs& a, int32_t dtype, bool grid, hipStream_t s);
+// dhidden = sum of the splits [splits][n][dim], in order; of the sums' dim columns
+// the first cols.
+void loss_dh_join(const float* part, int splits, int n, int dim, int cols, void* out,
+                  int32_t out_dtype, int64_t ld, hipStream_t s);
 // dw (+)= nothing, for calls without rows
 int loss_no_rows(void* dw, int32_t dw_dtype, int64_t vocab, int64_t dim, int accumulate,
                  hipStream_t s);

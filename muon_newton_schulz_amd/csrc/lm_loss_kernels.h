@@ -1,8 +1,9 @@
-// The kernels behind the losses of a linear head over a large vocabulary, and
-// the choice of their tile cores: row statistics of the logits' tiles, g, and
-// the two products with g.  Included by the cross entropy (lm_loss.hip, where
-// the formulas stand) and, LISTS, by the distillation loss (distill.hip), which
-// also takes listed columns' logits from the statistics' tiles.
+// The kernels behind the losses of a linear head over a large vocabulary that
+// differ between them, and the choice of their tile cores: row statistics of the
+// logits' tiles, and the two products with g.  Included by the cross entropy
+// (lm_loss.hip, where the formulas and the kernels that do not differ stand) and,
+// LISTS, by the distillation loss (distill.hip), which also takes listed columns'
+// logits from the statistics' tiles.
 #pragma once
 
 #include <algorithm>
@@ -183,108 +184,6 @@ __global__ __launch_bounds__(kThreads, Core::kWaves) void k_loss_stats(StatsArgs
   stats_out<LISTS, Core, T>(a, w, acc);
 }
 
-
-// c: the largest finite |dloss| of the rows with a target, 1 if that is 0.
-constexpr int kScaleThreads = 1024;
-__global__ __launch_bounds__(kScaleThreads) void k_loss_scale(const float* __restrict__ dloss, int n,
-                                                              const void* targets, int t64,
-                                                              int64_t vocab, float* c) {
-  __shared__ float red[kScaleThreads / 64];
-  float m = 0.0f;
-  for (int t = threadIdx.x; t < n; t += kScaleThreads) {
-    const float a = fabsf(dloss[t]);
-    if (a < INFINITY && target_of(targets, t64, t, vocab) >= 0) m = fmaxf(m, a);
-  }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
-  __syncthreads();
-  if (threadIdx.x != 0) return;
-  for (int k = 1; k < kScaleThreads / 64; ++k) m = fmaxf(m, red[k]);
-  *c = m > 0.0f ? m : 1.0f;
-}
-
-struct GradArgs {
-  const void* h;
-  const void* w;       // the piece's first row
-  const void* targets;
-  const float* lse;
-  const float* dloss;
-  const float* c;
-  void* g;             // [n][ldg], g / c; bf16: low plane, high plane
-  int64_t ldh, ldg, vocab, v0;
-  int n, dim, len, t64;  // len: vocabulary rows of the piece
-  float scale;           // of the logits
-};
-
-// What rounding to bf16 leaves of each value (0 where that is not finite).
-template <int NJ, int MI>
-__device__ __forceinline__ void low_part(f32x16_t (&acc)[NJ][MI]) {
-#pragma unroll
-  for (int a = 0; a < NJ; ++a)
-#pragma unroll
-    for (int b = 0; b < MI; ++b)
-#pragma unroll
-      for (int v = 0; v < 16; v += 2) {
-        const uint32_t h = pack_bf16(acc[a][b][v], acc[a][b][v + 1]);
-        const float x = acc[a][b][v] - __uint_as_float(h << 16);
-        const float y = acc[a][b][v + 1] - __uint_as_float(h & 0xffff0000u);
-        acc[a][b][v] = fabsf(x) < INFINITY ? x : 0.0f;
-        acc[a][b][v + 1] = fabsf(y) < INFINITY ? y : 0.0f;
-      }
-}
-
-// g / c of the piece, in the operands' type (bf16: two planes).
-template <typename Core, typename T>
-__device__ __forceinline__ void g_out(const GradArgs& a, const LossTile<T>& w,
-                                      f32x16_t (&acc)[Core::NJ][Core::MI]) {
-  const int i0 = w.i0, j0 = w.j0;
-  const int lane = opaque_lane(), wave = threadIdx.x >> 6;
-  const int iw = (wave % Core::WM) * 32 * Core::MI + (lane & 31);
-  float lse[Core::MI], dl[Core::MI];
-  int64_t tgt[Core::MI];
-#pragma unroll
-  for (int bi = 0; bi < Core::MI; ++bi) {
-    const int64_t t = static_cast<int64_t>(i0) + iw + 32 * bi;
-    lse[bi] = dl[bi] = 0.0f;
-    tgt[bi] = -1;
-    if (t < a.n) {
-      tgt[bi] = target_of(a.targets, a.t64, t, a.vocab);
-      lse[bi] = a.lse[t];
-      dl[bi] = a.dloss[t] / *a.c;
-    }
-  }
-  // A row without a target has no loss, whatever dloss holds there.  On the
-  // grid the columns from the piece's end to ldg are stored as zeros, which
-  // the sums over the vocabulary read.
-  const int jw = (wave / Core::WM) * 32 * Core::NJ + 4 * (lane >> 5);
-  const int len = a.len - j0 - jw;
-#pragma unroll
-  for (int bi = 0; bi < Core::MI; ++bi) {
-    const bool row = tgt[bi] >= 0;
-    const int64_t at64 = tgt[bi] - a.v0 - j0 - jw;
-    const int at = row && at64 >= 0 && at64 < 32 * Core::NJ ? static_cast<int>(at64) : -1;
-    const int left = row ? len : 0;
-#pragma unroll
-    for (int bj = 0; bj < Core::NJ; ++bj)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const int j = 32 * bj + 8 * (v >> 2) + (v & 3);
-        const float p = exp_of<T>(__builtin_fmaf(acc[bj][bi][v], a.scale, -lse[bi]));
-        acc[bj][bi][v] = j < left ? (at == j ? p - 1.0f : p) * dl[bi] : 0.0f;
-      }
-    __builtin_amdgcn_sched_barrier(0);
-  }
-  T* low = static_cast<T*>(a.g) + i0 * a.ldg + j0;
-  const int cols = Core::kGrid ? static_cast<int>(a.ldg) - j0 : a.len - j0;
-  const T* none = nullptr;
-  if constexpr (sizeof(T) == 2) {
-    Core::write(acc, low + a.n * a.ldg, a.ldg, none, 0, a.n - i0, cols);
-    low_part(acc);
-  }
-  Core::write(acc, low, a.ldg, none, 0, a.n - i0, cols);
-}
-
 // A product with g: the sum over its planes, `plane` elements apart, the low one
 // first, or with TURNS (on the grid) a stage of each in turns, which reads the
 // other operand from memory once: distillation step of 57 x 151637 x 3008 1058
@@ -301,54 +200,6 @@ __device__ __forceinline__ void run_planes(LossTile<T>& w, int64_t plane,
     zero_acc(acc);
 #pragma unroll 1
     for (int p = 0; p < 2; ++p, w.P += plane) Core::template run<true>(w, acc);
-  }
-}
-
-template <typename Core, typename T>
-__global__ __launch_bounds__(kThreads, Core::kWaves) void k_loss_g(GradArgs a, int nx, int ny) {
-  using W = LossTile<T>;
-  int x, y;
-  if (!my_tile(nx, ny, x, y)) return;
-  W w;
-  w.i0 = x * Core::BM;
-  w.j0 = y * Core::BN;
-  w.P = static_cast<const T*>(a.h) + w.i0 * a.ldh;
-  w.ldp = a.ldh;
-  w.pn = a.n - w.i0;
-  w.Q = static_cast<const T*>(a.w) + static_cast<int64_t>(w.j0) * a.dim;
-  w.ldq = w.K = a.dim;
-  w.qn = a.len - w.j0;
-  f32x16_t acc[Core::NJ][Core::MI];
-  Core::run(w, acc);
-  g_out<Core, T>(a, w, acc);
-}
-
-// hidden with zeros in the rows without a target, [n][dim]: dW's sum runs over
-// all rows, and 0 times what such a row holds is 0 only where that is finite.
-// One read and one write of hidden (backward of 8192 x 32000 x 2048: 4.60 ms
-// against 4.56 without, of 33 x 32000 x 2048: 114 us against 112).
-template <typename T>
-__global__ __launch_bounds__(kThreads) void k_loss_rows(const T* __restrict__ h, int64_t ldh,
-                                                        const void* targets, int t64, int n,
-                                                        int dim, int64_t vocab,
-                                                        T* __restrict__ out) {
-  constexpr int E = 16 / sizeof(T);
-  const int per = (dim + E - 1) / E;
-  const int64_t total = static_cast<int64_t>(n) * per;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const int64_t t = i / per;
-    const int c = static_cast<int>(i - t * per) * E;
-    const bool row = target_of(targets, t64, t, vocab) >= 0;
-    const T* p = h + t * ldh + c;
-    T* o = out + t * dim + c;
-    if (c + E <= dim) {
-      u32x4_t v = {0, 0, 0, 0};
-      if (row) __builtin_memcpy(&v, p, 16);
-      __builtin_memcpy(o, &v, 16);
-    } else {
-      for (int e = 0; c + e < dim; ++e) o[e] = row ? p[e] : T{};
-    }
   }
 }
 
@@ -407,24 +258,6 @@ __global__ __launch_bounds__(kThreads, Core::kWaves) void k_loss_dh(DhArgs a, in
                 w.pn, w.qn);
 }
 
-// dhidden = sum of the splits, in order; of the sums' dim columns the first
-// cols.
-template <typename TO>
-__global__ __launch_bounds__(kThreads) void k_loss_dh_join(const float* __restrict__ part,
-                                                           int splits, int n, int dim, int cols,
-                                                           TO* out, int64_t ld) {
-  const int64_t total = static_cast<int64_t>(n) * dim;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * kThreads) {
-    float v = part[i];
-#pragma unroll 8
-    for (int s = 1; s < splits; ++s) v += part[s * total + i];
-    const int64_t t = i / dim;
-    const int d = static_cast<int>(i - t * dim);
-    if (d < cols) from_f32(v, out + t * ld + d);
-  }
-}
-
 struct DwArgs {
   const void* g;
   const void* h;  // k_loss_rows' copy
@@ -473,7 +306,6 @@ auto dh_tiles(int64_t n, int splits) {
   return [n, splits](int bm) { return static_cast<double>(ceil_div(n, bm) * splits); };
 }
 
-
 // bf16 operands on the 16-byte grid take the DMA core (grid), others the
 // core for any operands.
 template <bool LISTS, typename Core, typename T>
@@ -499,30 +331,6 @@ int run_stats(const StatsArgs& a, bool grid, hipStream_t s) {
   if (pick_any_large<T>(row_tiles(a.n), a.vocab, a.dim))
     return launch_stats<LISTS, OtherCore<T, false, false, 128>, T>(a, s);
   return launch_stats<LISTS, OtherCore<T, false, false, 64>, T>(a, s);
-}
-
-template <typename Core, typename T>
-void launch_g(const GradArgs& a, hipStream_t s) {
-  const int nx = static_cast<int>(ceil_div(a.n, Core::BM));
-  const int ny = static_cast<int>(ceil_div(a.len, Core::BN));
-  hipLaunchKernelGGL((k_loss_g<Core, T>), dim3(tile_blocks(nx, ny)),
-                     dim3(kThreads), 0, s, a, nx, ny);
-}
-template <typename T>
-void run_g(const GradArgs& a, bool grid, hipStream_t s) {
-  if constexpr (sizeof(T) == 2) {
-    if (grid) {
-      const Shape shape = pick_shape(kShapeNT, row_tiles(a.n), a.len, a.dim);
-      if (shape == kLarge) return launch_g<LargeCore<false, false>, T>(a, s);
-      if (shape == kHalf) return launch_g<HalfCore<false, false>, T>(a, s);
-      if (shape == kMedium) return launch_g<MediumCore<false, false>, T>(a, s);
-      return launch_g<ThinCore<false, false>, T>(a, s);
-    }
-  }
-  if (pick_any_large<T>(row_tiles(a.n), a.len, a.dim))
-    launch_g<OtherCore<T, false, false, 128>, T>(a, s);
-  else
-    launch_g<OtherCore<T, false, false, 64>, T>(a, s);
 }
 
 template <bool TURNS, typename Core, typename T, typename TO>
@@ -584,20 +392,17 @@ void run_dw(const DwArgs& a, bool grid, hipStream_t s) {
     launch_dw<TURNS, OtherCore<T, true, true, 64>, T, TO>(a, s);
 }
 
+template <typename T>
+constexpr int32_t kType = sizeof(T) == 2 ? MUON_DTYPE_BF16 : MUON_DTYPE_FP32;
 template <bool LISTS, typename T, typename TH, typename TW>
 void run_backward(const BackwardArgs& b, const LossWs& w, hipStream_t s) {
   T* g = reinterpret_cast<T*>(b.ws + w.g);
   float* part = reinterpret_cast<float*>(b.ws + w.part);
   float* c = reinterpret_cast<float*>(b.ws + w.c);
-  hipLaunchKernelGGL(k_loss_scale, dim3(1), dim3(kScaleThreads), 0, s, b.dloss,
-                     static_cast<int>(b.n), b.targets, b.t64, b.vocab, c);
+  loss_scale(b, c, s);
   T* rows = reinterpret_cast<T*>(b.ws + w.rows);
-  if (b.dw != nullptr && !LISTS) {
-    const int64_t pieces = b.n * ceil_div(b.dim, 16 / static_cast<int64_t>(sizeof(T)));
-    hipLaunchKernelGGL(k_loss_rows<T>,
-                       dim3(static_cast<unsigned>(std::min<int64_t>(8192, ceil_div(pieces, kThreads)))),
-                       dim3(kThreads), 0, s, static_cast<const T*>(b.h), b.ldh, b.targets, b.t64,
-                       static_cast<int>(b.n), static_cast<int>(b.dim), b.vocab, rows);
+  if constexpr (!LISTS) {
+    if (b.dw != nullptr) loss_rows(b, rows, kType<T>, s);
   }
   const bool grid = on_grid(b.h, b.ldh, b.dim) && on_grid(b.w, b.dim, b.dim);
   // operands laid out on the grid for results that are not: dh leaves the fp32
@@ -606,9 +411,9 @@ void run_backward(const BackwardArgs& b, const LossWs& w, hipStream_t s) {
   for (int64_t v0 = 0; v0 < b.vocab; v0 += w.piece) {
     const int len = static_cast<int>(std::min(w.piece, b.vocab - v0));
     const T* wp = static_cast<const T*>(b.w) + v0 * b.dim;
-    run_g<T>(GradArgs{b.h, wp, b.targets, b.lse, b.dloss, c, g, b.ldh, w.ldg, b.vocab, v0,
-                      static_cast<int>(b.n), static_cast<int>(b.dim), len, b.t64, b.scale},
-             grid, s);
+    loss_g(GradArgs{b.h, wp, b.targets, b.lse, b.dloss, c, g, b.ldh, w.ldg, b.vocab, v0,
+                    static_cast<int>(b.n), static_cast<int>(b.dim), len, b.t64, b.scale},
+           kType<T>, grid, s);
     if (b.after_g != nullptr) b.after_g(b.context, g, w.ldg, c, v0, len, s);
     if (b.dh != nullptr) {
       const bool last = v0 + len == b.vocab;
@@ -626,11 +431,8 @@ void run_backward(const BackwardArgs& b, const LossWs& w, hipStream_t s) {
           grid && (laid || on_grid(b.dw, b.dim, b.dim)), s);
   }
   if (b.dh != nullptr && (w.splits > 1 || laid))
-    hipLaunchKernelGGL(k_loss_dh_join<TH>,
-                       dim3(static_cast<unsigned>(std::min<int64_t>(4096, ceil_div(b.n * b.dim, kThreads)))),
-                       dim3(kThreads), 0, s, part, w.splits, static_cast<int>(b.n),
-                       static_cast<int>(b.dim), static_cast<int>(b.cols), static_cast<TH*>(b.dh),
-                       b.ld_dh);
+    loss_dh_join(part, w.splits, static_cast<int>(b.n), static_cast<int>(b.dim),
+                 static_cast<int>(b.cols), b.dh, kType<TH>, b.ld_dh, s);
 }
 
 // Row statistics of scale * h W^T, and what targets or keys name.  Returns the
