@@ -697,6 +697,10 @@ def muon_clip(plan: MuonClipPlan, params, mode, tau: float, max_logits=None, wor
 # streams.  What a call allocates (outputs and workspaces left out) belongs
 # to the stream the call runs on.
 #
+# bf16 matrix products are fast where base, row stride and row length of their
+# operands and results are multiples of 16 bytes; others take up to twice as
+# long.
+#
 # Like the steps, they are no autograd functions: nothing is recorded, tensors
 # that require gradients are read as they are, and an output has no graph.  A
 # program calls each gradient itself (or from its own autograd.Function).
@@ -1356,8 +1360,8 @@ def preference_loss_forward(nll, offsets, ref_nll=None, mask=None, beta: float =
     ``(1 - smoothing) log(1 + exp(-x)) + smoothing log(1 + exp(x))``; "hinge",
     ``max(0, 1 - x)``; "squared", ``(1 - x)**2``.  A pair with a sequence in
     which no token counts has loss 0 and no gradient.  Returns (loss, margins,
-    reward, count): fp32 of pairs (margins: the x), fp32 and int32 of
-    sequences."""
+    reward, count): fp32 of pairs (margins: the x, rounded; the hinge's stay
+    below 1 where x is), fp32 and int32 of sequences."""
     import torch
     f32, i32 = torch.float32, torch.int32
     device, n, sequences = _packed(nll, offsets)
@@ -1394,8 +1398,9 @@ def preference_loss_backward(offsets, margins, count, dloss, n=None, mask=None, 
                              kind="logistic", smoothing: float = 0.0, mean: bool = False,
                              dnll=None, stream=None):
     """The gradient of ``sum(dloss * loss)`` by nll; margins and count from
-    preference_loss_forward, whose nll it does not need; dloss fp32, one value
-    a pair.  dnll as for policy_loss_backward; without it, ``n`` (the mask's
+    preference_loss_forward, whose nll it does not need (f' is taken at the
+    rounded margins: near 0 it is off by 2^-24 |x| f'', not by a part of
+    itself); dloss fp32, one value a pair.  dnll as for policy_loss_backward; without it, ``n`` (the mask's
     size by default) is the number of tokens.  Returns dnll."""
     import torch
     f32, i32 = torch.float32, torch.int32
